@@ -85,8 +85,10 @@ enum pa_device_error {
                                a V element beyond +-65504*2^8 in a key tile the
                                chunk reads (the P.V product stages V in fp16), or
                                non-finite inputs */
-    PA_DEVERR_PLAN = 128    /* a pa_decode_planned item outside the call's bounds
+    PA_DEVERR_PLAN = 128,   /* a pa_decode_planned item outside the call's bounds
                                (that CTA did nothing) */
+    PA_DEVERR_POSITION = 256 /* a token position beyond the rotation table
+                               (that token was skipped) */
 };
 
 /* ------------------------------------------------------------------ decode */
@@ -231,6 +233,47 @@ int pa_reshape_and_cache(const void* k, const void* v, void* k_pool, void* v_poo
                          int head_dim, int block_size, int num_blocks, pa_stream_t stream);
 
 /*
+ * Rotary position rotation of q and k with the cache write, in one launch.
+ * Every pair of dims (x, y) of a head is turned by the angle of its token's
+ * position and its frequency i,
+ *     x' = x cos - y sin,  y' = y cos + x sin,  0 <= i < rot_dim / 2,
+ * where (x, y) are dims (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved is
+ * non-zero; dims from rot_dim on pass through. q_out receives the rotated q;
+ * the rotated k and the unrotated v go to the token's slot as
+ * pa_reshape_and_cache writes them (k_scale, v_scale NULL: bf16 pools), or as
+ * pa_reshape_and_cache_fp8 does (both given, fp32 [n_kv_heads]: E4M3 pools).
+ * Products and sums are rounded one by one in fp32 and the result once to its
+ * stored type (the E4M3 codes come from the fp32 result, not from a bf16 one).
+ *  q_out, q       bf16 [n_tokens][n_heads][head_dim]; q_out may be q (with
+ *                 q_out_stride == q_stride), and must not overlap it otherwise.
+ *                 Both NULL: only k and v are taken (n_heads is ignored)
+ *  k, v           bf16 [n_tokens][n_kv_heads][head_dim]
+ *  *_stride       elements from one token to the next, a multiple of 8, at
+ *                 least heads * head_dim: q, k and v may be views of one
+ *                 packed projection. Heads are contiguous
+ *  cos_sin        fp32 [max_position][rot_dim], 16-byte aligned: rot_dim/2
+ *                 cosines, then rot_dim/2 sines, of each position
+ *  positions      int64 [n_tokens]. A negative one skips its token: nothing
+ *                 of it is written. One >= max_position does too and sets
+ *                 PA_DEVERR_POSITION
+ *  slot_mapping   int64 [n_tokens]; negative: q is rotated, k and v are not
+ *                 written; >= num_blocks*16 likewise, and sets PA_DEVERR_SLOT.
+ *                 Two tokens naming the same slot race (which bytes win is
+ *                 not defined)
+ *  rot_dim        a multiple of 16 in [0, head_dim], else PA_ERR_UNSUPPORTED
+ *                 (PA_ERR_INVALID_ARG outside the range); 0: no rotation,
+ *                 cos_sin and positions are not read and may be NULL
+ * head_dim 64 or 128, else PA_ERR_UNSUPPORTED. Tensors 16-byte aligned.
+ */
+int pa_rope_and_cache(void* q_out, const void* q, const void* k, const void* v, void* k_pool,
+                      void* v_pool, const float* cos_sin, const int64_t* positions,
+                      const int64_t* slot_mapping, const float* k_scale, const float* v_scale,
+                      int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                      int n_tokens, int n_heads, int n_kv_heads, int head_dim, int rot_dim,
+                      int max_position, int interleaved, int block_size, int num_blocks,
+                      pa_stream_t stream);
+
+/*
  * copy_blocks ([MA] copy-on-write figure; [LD] only the diverging block is
  * copied): for each pair i, the whole block block_mapping[2i] (all KV heads,
  * all 16 slots) is copied to block block_mapping[2i+1], in k_pool and v_pool.
@@ -353,6 +396,47 @@ int pa_decode_fp8(void* out, const void* q, const void* k_pool, const void* v_po
                   int head_dim, int block_size, int n_seqs, int max_blocks_per_seq,
                   int max_context_len, int num_blocks, int partition_tokens, void* workspace,
                   size_t workspace_bytes, pa_stream_t stream);
+
+/* -------------------------- fp8 (E4M3) KV cache with a scale per block */
+
+/*
+ * The same codes and pools as the fp8 cache above, but with one fp32 scale for
+ * each (block, KV head) of K and of V instead of one per head for the whole
+ * cache: no scale has to be known beforehand, and one loud token costs
+ * precision in its own block only.
+ *  k_scale, v_scale  fp32 [num_blocks][n_kv_heads], device memory, 4-byte
+ *                    aligned. The write below sets them: the smallest power
+ *                    of two 2^e, -32 <= e <= 32, with max |x| <= 448 * 2^e
+ *                    over the block's tokens, or a larger one of an earlier
+ *                    maximum. The attention calls take any value in
+ *                    [2^-32, 2^32] and clamp others to that range.
+ * pa_copy_blocks_fp8_block copies blocks with their scales; a swapped block's
+ * scales are the row [block] of each array.
+ */
+
+/*
+ * pa_rope_and_cache into such a cache: element x of the rotated k (or of v)
+ * is stored as the E4M3 code of x / scale (nearest even; beyond +-448
+ * saturates, NaN stays NaN). The new tokens of a block in one call form a run:
+ *  - a run that starts at the block's first slot gives the block its scale
+ *    (what the block held is void: a block's first slot is written first);
+ *  - any other run raises the block's scale where its own tokens need a
+ *    larger one, and the block's other slots are then encoded again: exact,
+ *    unless the new code is an E4M3 subnormal (off by at most 2^-10 of the
+ *    new scale).
+ * Infinite and NaN elements do not enter the maximum. A call's tokens of one
+ * block must be next to each other in slot_mapping with consecutive slots (as
+ * pa_bm_append_tokens gives them); two runs of one block in one call race.
+ * Tokens skipped by a negative position or slot end a run.
+ * Arguments as for pa_rope_and_cache, with rot_dim = 0 for a plain write.
+ */
+int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const void* v, void* k_pool,
+                                void* v_pool, float* k_scale, float* v_scale, const float* cos_sin,
+                                const int64_t* positions, const int64_t* slot_mapping,
+                                int64_t q_out_stride, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, int n_tokens, int n_heads, int n_kv_heads,
+                                int head_dim, int rot_dim, int max_position, int interleaved,
+                                int block_size, int num_blocks, pa_stream_t stream);
 
 /*
  * Host-side work plan for one decode call, for callers that hold the batch's

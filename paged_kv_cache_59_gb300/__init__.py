@@ -23,7 +23,8 @@ __all__ = [
     "pa_decode", "pa_decode_tc", "pa_decode_workspace_bytes", "pa_decode_partition_tokens", "decode_workspace", "pa_decode_noalloc", "pa_reshape_and_cache",
     "pa_copy_blocks", "pa_prefill_paged", "pa_prefill_paged_ex", "pa_prefill_workspace_bytes",
     "prefill_workspace", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_window",
-    "pa_swap_out_blocks", "pa_swap_in_blocks", "pa_get_device_error",
+    "pa_swap_out_blocks", "pa_swap_in_blocks", "pa_get_device_error", "pa_rope_and_cache",
+    "pa_rope_and_cache_fp8_block",
     "BlockManager", "load", "PagedKVError",
 ]
 
@@ -330,6 +331,121 @@ def pa_decode_planned(out, q, k_pool, v_pool, block_tables, context_lens, scale:
         int(max_context_len), num_blocks, int(window), int(partition_tokens),
         _ptr(items, "items", dtype=torch.int32), items.shape[0], ws_ptr, ws_bytes, _stream(stream))
     check("pa_decode_planned", st)
+
+
+def _same_device(**tensors) -> int:
+    """The tensors' one CUDA device; None entries are left out."""
+    index = None
+    for what, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor (the library has no CPU path)")
+        if index is None:
+            index = t.get_device()
+        elif t.get_device() != index:
+            raise ValueError("the tensors are on different devices")
+    return index
+
+
+def _call(fn: str, device: int, stream, *args) -> None:
+    """Calls the C entry point with `device` current, on `stream` or that
+    device's current stream."""
+    torch = _torch()
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    check(fn, getattr(load(), fn)(*args, s.cuda_stream))
+
+
+def _token_stride(t, what: str) -> int:
+    """Elements between the tokens of [n_tokens][heads][head_dim], whose heads
+    must be contiguous (a view of a packed projection will do)."""
+    n, heads, dim = t.shape
+    st = t.stride()
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+        raise ValueError(f"{what} must have contiguous heads")
+    return st[0] if n > 1 else heads * dim
+
+
+def _bf16(t, what: str) -> int:
+    """The address of a bf16 (or 16-bit integer) tensor, whatever its strides."""
+    torch = _torch()
+    if t.dtype not in (torch.bfloat16, torch.int16, getattr(torch, "uint16", torch.int16)):
+        raise TypeError(f"{what} must hold bf16 (bfloat16 or 16-bit integer bits), got {t.dtype}")
+    return t.data_ptr()
+
+
+def _rope(fn: str, q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, scale_numel, cos_sin, positions, slot_mapping,
+          interleaved, stream) -> None:
+    torch = _torch()
+    n_tokens, n_kv_heads, head_dim = k.shape
+    num_blocks, hk2, block_size, hd2 = k_pool.shape
+    if (hk2, hd2) != (n_kv_heads, head_dim) or v.shape != k.shape or v_pool.shape != k_pool.shape:
+        raise ValueError("shape mismatch between k/v and the pools")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    n_heads = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != n_tokens or q.shape[2] != head_dim or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [n_tokens][n_heads][head_dim]")
+        n_heads = q.shape[1]
+    if slot_mapping.numel() != n_tokens:
+        raise ValueError("slot_mapping must have n_tokens entries")
+    rot = max_position = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions is None or positions.numel() != n_tokens:
+            raise ValueError("cos_sin must be [max_position][rot_dim], positions [n_tokens]")
+        max_position, rot = cos_sin.shape
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    if k_scale is not None and (k_scale.numel() != scale_numel or v_scale.numel() != scale_numel):
+        raise ValueError(f"k_scale and v_scale need {scale_numel} entries")
+    dev = _same_device(k=k, v=v, q=q, q_out=q_out, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
+                       cos_sin=cos_sin, positions=positions, slot_mapping=slot_mapping)
+    if k_scale is None:
+        kp, vp_ = _ptr(k_pool, "k_pool", bf16=True), _ptr(v_pool, "v_pool", bf16=True)
+    else:
+        kp, vp_ = _fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool")
+    _call(fn, dev, stream, None if q is None else _bf16(q_out, "q_out"), None if q is None else _bf16(q, "q"),
+          _bf16(k, "k"), _bf16(v, "v"), kp, vp_,
+          *_rope_tail(fn, torch, k_scale, v_scale, cos_sin, positions if rot else None, slot_mapping),
+          _token_stride(q_out, "q_out") if n_heads else 0, _token_stride(q, "q") if n_heads else 0,
+          _token_stride(k, "k"), _token_stride(v, "v"), n_tokens, n_heads, n_kv_heads, head_dim, rot, max_position,
+          1 if interleaved else 0, block_size, num_blocks)
+
+
+def _rope_tail(fn, torch, k_scale, v_scale, cos_sin, positions, slot_mapping):
+    scales = [None if t is None else _ptr(t, what, dtype=torch.float32)
+              for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
+    rest = [None if cos_sin is None else _ptr(cos_sin, "cos_sin", dtype=torch.float32),
+            None if positions is None else _ptr(positions, "positions", dtype=torch.int64),
+            _ptr(slot_mapping, "slot_mapping", dtype=torch.int64)]
+    return scales + rest if fn.endswith("_block") else rest + scales
+
+
+def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, cos_sin, positions, slot_mapping, interleaved: bool = False,
+                      k_scale=None, v_scale=None, stream=None) -> None:
+    """Rotates q and k by their tokens' positions and writes k and v to
+    slot_mapping[t], in one launch. q, k, v: [n_tokens][heads][head_dim], bf16,
+    views of a packed projection allowed (contiguous heads); q_out may be q.
+    cos_sin fp32 [max_position][rot_dim] (cosines, then sines), positions int64;
+    cos_sin None: no rotation; q and q_out None: only k and v. bf16 pools, or
+    uint8 pools with k_scale and v_scale fp32 [n_kv_heads]."""
+    _rope("pa_rope_and_cache", q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, k.shape[1], cos_sin, positions,
+          slot_mapping, interleaved, stream)
+
+
+def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, cos_sin, positions, slot_mapping,
+                                interleaved: bool = False, stream=None) -> None:
+    """pa_rope_and_cache into E4M3 pools with a scale per block and head:
+    k_scale, v_scale fp32 [num_blocks][n_kv_heads], set and raised by the call.
+    A call's tokens of one block must be next to each other, in slot order."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale are needed")
+    _rope("pa_rope_and_cache_fp8_block", q_out, q, k, v, k_pool, v_pool, k_scale, v_scale,
+          k_pool.shape[0] * k_pool.shape[1], cos_sin, positions, slot_mapping, interleaved, stream)
 
 
 def pa_copy_blocks(k_pool, v_pool, block_mapping, stream=None) -> None:

@@ -29,6 +29,7 @@ PA_DEVERR_CONTEXT = 16
 PA_DEVERR_LAYOUT = 32
 PA_DEVERR_RANGE = 64
 PA_DEVERR_PLAN = 128
+PA_DEVERR_POSITION = 256
 
 vp = C.c_void_p
 i32 = C.c_int
@@ -49,6 +50,10 @@ SIGNATURES = {
     "pa_decode_noalloc": (i32, [vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32,
                                 i32, vp]),
     "pa_reshape_and_cache": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
+    "pa_rope_and_cache": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, i32, i32,
+                                i32, i32, i32, i32, i32, vp]),
+    "pa_rope_and_cache_fp8_block": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32,
+                                          i32, i32, i32, i32, i32, i32, i32, vp]),
     "pa_copy_blocks": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp]),
     "pa_copy_blocks_ex": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
     "pa_decode_window": (i32, [vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32, i32,

@@ -1,0 +1,39 @@
+"""C ABI argument checks of the rotated cache write and of attention over
+windows with sinks and block-scaled E4M3 caches; none needs a GPU."""
+import ctypes as C
+
+import pytest
+
+
+# ------------------------------------------------- rotated cache write --
+
+def _rope_args(**over):
+    p = C.c_void_p(4096)
+    a = dict(qo=C.c_void_p(8192), q=p, k=p, v=p, kp=p, vp=p, cs=p, pos=p, slots=p, ks=None, vs=None, qos=256, qs=256,
+             kst=128, vst=128, T=4, H=4, Hk=2, D=64, rot=64, maxp=100, il=0, bs=16, nb=16)
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(T=0), 0), (dict(T=-1), -1), (dict(Hk=0), -1), (dict(nb=-1), -1), (dict(D=96), -2), (dict(bs=8), -2),
+    (dict(rot=24), -2), (dict(rot=80), -1), (dict(rot=-16), -1), (dict(q=None), -1), (dict(qo=None), -1),
+    (dict(H=0), -1), (dict(k=None), -1), (dict(slots=None), -1), (dict(cs=None), -1), (dict(pos=None), -1),
+    (dict(cs=C.c_void_p(4100)), -1), (dict(k=C.c_void_p(4104)), -1), (dict(q=C.c_void_p(4104)), -1),
+    (dict(slots=C.c_void_p(4100)), -1), (dict(kst=64), -1), (dict(vst=132), -1), (dict(qs=0), -1), (dict(qos=128), -1),
+    (dict(qo=C.c_void_p(4096), qs=512), -1), (dict(ks=C.c_void_p(4096)), -1),
+    (dict(ks=C.c_void_p(4098), vs=C.c_void_p(4096)), -1),
+])
+def test_rope_argument_errors_need_no_device(capi, over, status):
+    a = _rope_args(**over)
+    tail = [a["qos"], a["qs"], a["kst"], a["vst"], a["T"], a["H"], a["Hk"], a["D"], a["rot"], a["maxp"], a["il"],
+            a["bs"], a["nb"], None]
+    assert capi.pa_rope_and_cache(a["qo"], a["q"], a["k"], a["v"], a["kp"], a["vp"], a["cs"], a["pos"], a["slots"],
+                                  a["ks"], a["vs"], *tail) == status
+    p = C.c_void_p(4096)
+    if "ks" not in over:
+        assert capi.pa_rope_and_cache_fp8_block(a["qo"], a["q"], a["k"], a["v"], a["kp"], a["vp"], p, p, a["cs"], a["pos"],
+                                                a["slots"], *tail) == status
+        if a["T"] > 0:
+            assert capi.pa_rope_and_cache_fp8_block(a["qo"], a["q"], a["k"], a["v"], a["kp"], a["vp"], None, p, a["cs"],
+                                                    a["pos"], a["slots"], *tail) == -1
