@@ -347,6 +347,27 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
                      int partition_tokens, void* workspace, size_t workspace_bytes,
                      pa_stream_t stream);
 
+/*
+ * Sliding window with sinks: as pa_decode_window, and positions 0 ..
+ * n_sinks - 1 stay visible too, however long the sequence (the first tokens
+ * collect attention that has nowhere else to go; a model that loses them
+ * answers worse than one that keeps them). The query at i = context_lens[b]-1
+ * attends to t <= i with t >= i - window or t < n_sinks:
+ *     out[b][h] = sum_t softmax_t(scale * q[b][h] . K_b[t]) V_b[t].
+ * Only blocks with such a position are read: table entries of the blocks
+ * between the sinks and the window may be -1 (pa_bm_release_between). K and V
+ * rows of positions that are not visible may hold anything, NaN included.
+ * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG; n_sinks = 0 is
+ * pa_decode_window. bf16 pools (k_scale, v_scale NULL) or E4M3 pools with
+ * per-head scales (both given); workspace as for pa_decode_ex.
+ */
+int pa_decode_sinks(void* out, const void* q, const void* k_pool, const void* v_pool,
+                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                    const int32_t* context_lens, float scale, int n_heads, int n_kv_heads, int head_dim,
+                    int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len,
+                    int num_blocks, int window, int n_sinks, int partition_tokens, void* workspace,
+                    size_t workspace_bytes, pa_stream_t stream);
+
 /* ------------------------------------------------- fp8 (E4M3) KV cache */
 
 /*
@@ -437,6 +458,23 @@ int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const
                                 int64_t v_stride, int n_tokens, int n_heads, int n_kv_heads,
                                 int head_dim, int rot_dim, int max_position, int interleaved,
                                 int block_size, int num_blocks, pa_stream_t stream);
+
+/*
+ * Decode over such a cache: pa_decode_fp8 with the scales of each block,
+ *     K_b[t] = code * k_scale[block of t][kv head], V_b[t] likewise.
+ * window -1: every position; window >= 0: as pa_decode_sinks, n_sinks too
+ * (n_sinks is ignored without a window). Workspace, partitions and kernels as
+ * for pa_decode_fp8. V's scale is folded into the softmax weight, w = p *
+ * v_scale = 2^(s + log2 v_scale - m), which enters the P.V product as one
+ * fp16 term at head_dim 128: within 2^-11 of w, or 2^-25 of the reference weight.
+ */
+int pa_decode_fp8_block(void* out, const void* q, const void* k_pool, const void* v_pool,
+                        const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                        const int32_t* context_lens, float scale, int n_heads, int n_kv_heads,
+                        int head_dim, int block_size, int n_seqs, int max_blocks_per_seq,
+                        int max_context_len, int num_blocks, int window, int n_sinks,
+                        int partition_tokens, void* workspace, size_t workspace_bytes,
+                        pa_stream_t stream);
 
 /*
  * Host-side work plan for one decode call, for callers that hold the batch's

@@ -24,7 +24,7 @@ __all__ = [
     "pa_copy_blocks", "pa_prefill_paged", "pa_prefill_paged_ex", "pa_prefill_workspace_bytes",
     "prefill_workspace", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_window",
     "pa_swap_out_blocks", "pa_swap_in_blocks", "pa_get_device_error", "pa_rope_and_cache",
-    "pa_rope_and_cache_fp8_block",
+    "pa_rope_and_cache_fp8_block", "pa_decode_sinks", "pa_decode_fp8_block",
     "BlockManager", "load", "PagedKVError",
 ]
 
@@ -274,6 +274,57 @@ def pa_decode_fp8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, contex
         head_dim, block_size, n_seqs, block_tables.shape[1], int(max_context_len), num_blocks,
         int(partition_tokens), ws_ptr, ws_bytes, _stream(stream))
     check("pa_decode_fp8", st)
+
+
+def _decode_call(fn: str, out, q, k_pool, v_pool, k_scale, v_scale, scale_numel, block_tables, context_lens, scale,
+                 max_context_len, window, n_sinks, workspace, partition_tokens, stream) -> None:
+    torch = _torch()
+    n_seqs, n_heads, head_dim = q.shape
+    num_blocks, n_kv_heads, block_size, hd2 = k_pool.shape
+    if hd2 != head_dim or v_pool.shape != k_pool.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the pools")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n_seqs or context_lens.numel() != n_seqs:
+        raise ValueError("block_tables must be [n_seqs][max_blocks], context_lens [n_seqs]")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    dev = _same_device(q=q, out=out, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
+                       block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    if k_scale is None:
+        kp, vp_, ks, vs = _ptr(k_pool, "k_pool", bf16=True), _ptr(v_pool, "v_pool", bf16=True), None, None
+    else:
+        if k_scale.numel() != scale_numel or v_scale.numel() != scale_numel:
+            raise ValueError(f"k_scale and v_scale need {scale_numel} entries")
+        kp, vp_ = _fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool")
+        ks = _ptr(k_scale, "k_scale", dtype=torch.float32)
+        vs = _ptr(v_scale, "v_scale", dtype=torch.float32)
+    ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace, "workspace"),
+                                                        workspace.numel() * workspace.element_size())
+    _call(fn, dev, stream, _ptr(out, "out", bf16=True), _ptr(q, "q", bf16=True), kp, vp_, ks, vs,
+          _ptr(block_tables, "block_tables", dtype=torch.int32), _ptr(context_lens, "context_lens", dtype=torch.int32),
+          scale, n_heads, n_kv_heads, head_dim, block_size, n_seqs, block_tables.shape[1], max_context_len, num_blocks,
+          window, n_sinks, partition_tokens, ws, ws_bytes)
+
+
+def pa_decode_sinks(out, q, k_pool, v_pool, block_tables, context_lens, scale: float, max_context_len: int,
+                    window: int, n_sinks: int, k_scale=None, v_scale=None, workspace=None, partition_tokens: int = 0,
+                    stream=None) -> None:
+    """Sliding-window decode whose first n_sinks positions stay visible: the
+    query at i = ctx-1 attends to t <= i with t >= i-window or t < n_sinks.
+    bf16 pools, or uint8 pools with k_scale and v_scale fp32 [n_kv_heads]."""
+    _decode_call("pa_decode_sinks", out, q, k_pool, v_pool, k_scale, v_scale, k_pool.shape[1], block_tables,
+                 context_lens, scale, max_context_len, window, n_sinks, workspace, partition_tokens, stream)
+
+
+def pa_decode_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale: float,
+                        max_context_len: int, window: int = -1, n_sinks: int = 0, workspace=None,
+                        partition_tokens: int = 0, stream=None) -> None:
+    """Decode over an E4M3 cache with a scale per block and head (k_scale,
+    v_scale fp32 [num_blocks][n_kv_heads], see pa_rope_and_cache_fp8_block);
+    window >= 0: as pa_decode_sinks."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale are needed")
+    _decode_call("pa_decode_fp8_block", out, q, k_pool, v_pool, k_scale, v_scale, k_pool.shape[0] * k_pool.shape[1],
+                 block_tables, context_lens, scale, max_context_len, window, n_sinks, workspace, partition_tokens, stream)
 
 
 def pa_decode_plan(context_lens, n_heads: int, n_kv_heads: int, head_dim: int, max_blocks_per_seq: int,

@@ -63,6 +63,10 @@ SIGNATURES = {
     "pa_reshape_and_cache_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
     "pa_decode_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32,
                             i32, i32, vp, C.c_size_t, vp]),
+    "pa_decode_sinks": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32, i32,
+                              i32, i32, i32, vp, C.c_size_t, vp]),
+    "pa_decode_fp8_block": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32, i32,
+                                  i32, i32, i32, vp, C.c_size_t, vp]),
     "pa_decode_plan": (i32, [vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp, i32]),
     "pa_decode_planned": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32,
                                 i32, i32, i32, vp, i32, vp, C.c_size_t, vp]),

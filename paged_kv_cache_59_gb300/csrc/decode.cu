@@ -57,8 +57,8 @@ struct DecodeParams {
     const uint16_t* q;
     const unsigned char* k_pool;  // bf16 or E4M3 elements (see the kernel's EB)
     const unsigned char* v_pool;
-    const float* k_scale;         // E4M3 cache: per-KV-head scales (else unused)
-    const float* v_scale;
+    const float* k_scale;         // E4M3 cache: scales [n_kv_heads], or [num_blocks][n_kv_heads]
+    const float* v_scale;         // (the kernel's BSC); unused for bf16
     const int32_t* tables;
     const int32_t* ctx;
     float* ws_ml;  // [B][H][P][2]
@@ -71,6 +71,7 @@ struct DecodeParams {
     int part_blocks;
     int max_parts;
     int window;  // >= 0: the query at position ctx-1 sees positions ctx-1-window .. ctx-1
+    int n_sinks; // and, with a window, positions 0 .. n_sinks-1
     unsigned int* err;
     // optional plan (pa_decode_planned): CTA i runs item i = (partition, KV head,
     // sequence, unused) instead of the one its grid position names
@@ -100,10 +101,42 @@ __device__ __forceinline__ bool cta_item(const DecodeParams& P, int& p, int& kvh
     return true;
 }
 
-// First block and partition count of a sequence's (windowed) context.
-__device__ __forceinline__ int first_position(const DecodeParams& P, int ctx) {
-    return P.window >= 0 ? max(0, ctx - 1 - P.window) : 0;
+// The blocks a sequence of ctx > 0 tokens attends to: the leading n_sink_blk
+// blocks that hold sinks, then blocks blk_first .. nblk - 1 from the window's
+// first position on (all of them without a window). Blocks between are never
+// read (their table entries may be released). The `total` blocks are numbered
+// 0 .. total-1 and cut into nparts partitions.
+struct Span {
+    int first_pos, blk_first, nblk, n_sink_blk, total, nparts;
+    bool over;  // the context or its partitions exceed the call's bounds (clamped)
+    __device__ __forceinline__ Span(const DecodeParams& P, int ctx) {
+        nblk = (ctx + kBS - 1) / kBS;
+        first_pos = P.window >= 0 ? max(0, ctx - 1 - P.window) : 0;
+        blk_first = first_pos / kBS;
+        n_sink_blk = min((P.n_sinks + kBS - 1) / kBS, blk_first);
+        total = n_sink_blk + nblk - blk_first;
+        nparts = (total + P.part_blocks - 1) / P.part_blocks;
+        over = nblk > P.max_blocks || nparts > P.max_parts;
+        if (over) {  // caller broke the bounds it passed
+            nblk = min(nblk, P.max_blocks);
+            blk_first = min(blk_first, nblk);
+            n_sink_blk = min(n_sink_blk, blk_first);
+            total = n_sink_blk + nblk - blk_first;
+            nparts = min((total + P.part_blocks - 1) / P.part_blocks, P.max_parts);
+            total = min(total, nparts * P.part_blocks);
+        }
+    }
+    // the logical block of number i
+    __device__ __forceinline__ int block(int i) const { return i < n_sink_blk ? i : i - n_sink_blk + blk_first; }
+};
+
+// Whether the query attends to position pos.
+__device__ __forceinline__ bool visible(int pos, int ctx, int first_pos, int n_sinks) {
+    return pos < ctx && (pos >= first_pos || pos < n_sinks);
 }
+
+// A block-scaled cache's scale, within the range the library works with.
+__device__ __forceinline__ float clamp_scale(float s) { return fminf(fmaxf(s, 0x1p-32f), 0x1p32f); }
 
 // Transposing butterfly: N values per lane are summed across the lanes that
 // differ in bits M, M/2, ..., 1; each level keeps half of the values.
@@ -129,7 +162,38 @@ struct TransposeReduce {
     }
 };
 
-// EB = bytes per cached element: 2 (bf16) or 1 (E4M3 codes with per-head scales).
+// The scales of a warp's blocks in a block-scaled cache: lane l holds those of
+// the warp's block l, take(i) broadcasts block i's.
+template <bool BSC>
+struct BlockScales {
+    float my_k, my_e, my_inv;  // K scale times `factor`; log2 and inverse of V's scale
+    float k, e, inv;
+    __device__ __forceinline__ BlockScales(const DecodeParams& P, int bid, int kvh, float factor) {
+        const bool ok = bid >= 0 && bid < P.num_blocks;
+        const size_t at = ok ? (size_t)bid * P.n_kv_heads + kvh : 0;
+        const float ks = ok ? clamp_scale(P.k_scale[at]) : 1.f;
+        const float vs = ok ? clamp_scale(P.v_scale[at]) : 1.f;
+        my_k = ks * factor;
+        my_e = log2f(vs);
+        my_inv = 1.f / vs;
+    }
+    __device__ __forceinline__ void take(int i) {
+        k = __shfl_sync(kFull, my_k, i);
+        e = __shfl_sync(kFull, my_e, i);
+        inv = __shfl_sync(kFull, my_inv, i);
+    }
+    __device__ __forceinline__ float score(float s) const { return fmaf(s, k, e); }
+    __device__ __forceinline__ float weight(float w) const { return w * inv; }
+};
+template <>
+struct BlockScales<false> {
+    __device__ __forceinline__ BlockScales(const DecodeParams&, int, int, float) {}
+    __device__ __forceinline__ void take(int) {}
+    __device__ __forceinline__ float score(float s) const { return s; }
+    __device__ __forceinline__ float weight(float w) const { return w; }
+};
+
+// EB = bytes per cached element: 2 (bf16) or 1 (E4M3 codes with scales).
 template <int D, int G, int LPT, int EB>
 struct Shape {
     static constexpr int NCH = D / (8 * LPT);      // 16-byte chunks per lane per token row
@@ -196,7 +260,13 @@ struct Chunk8<1> {
     }
 };
 
-template <int D, int G, int LPT, int EB, int NW, int S, int MINB>
+// BSC: an E4M3 cache with a scale per (block, KV head). K's scale multiplies
+// the block's scores. V's is folded into the exponent: with e = log2(v_scale),
+//     w_t = 2^(s_t + e - m) = p_t v_scale,   out = sum w_t code_t / sum w_t / v_scale,
+// so the P.V product runs on the codes with one running reference m for loud
+// and quiet blocks alike, no output is ever rescaled for a scale, and the only
+// extra work is one multiply-add per score and one multiply per block.
+template <int D, int G, int LPT, int EB, bool BSC, int NW, int S, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB)
 pa_decode_partition_kernel(const DecodeParams P) {
     using SH = Shape<D, G, LPT, EB>;
@@ -230,22 +300,12 @@ pa_decode_partition_kernel(const DecodeParams P) {
         }
         return;
     }
-    int nblk = (ctx + kBS - 1) / kBS;
-    // sliding window: blocks wholly before the window are never read (their
-    // table entries may be released); positions before it are masked
-    const int first_pos = first_position(P, ctx);
-    int blk_first = first_pos / kBS;
-    int nparts = (nblk - blk_first + P.part_blocks - 1) / P.part_blocks;
-    if (nblk > P.max_blocks || nparts > P.max_parts) {  // caller broke the bounds it passed
-        if (p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
-        nblk = min(nblk, P.max_blocks);
-        blk_first = min(blk_first, nblk);
-        nparts = min((nblk - blk_first + P.part_blocks - 1) / P.part_blocks, P.max_parts);
-        nblk = min(nblk, blk_first + nparts * P.part_blocks);
-    }
-    if (p >= nparts) return;
-    const int blk_begin = blk_first + p * P.part_blocks;
-    const int nb_local = min(blk_begin + P.part_blocks, nblk) - blk_begin;
+    const Span sp(P, ctx);
+    if (sp.over && p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
+    if (p >= sp.nparts) return;
+    const int first_pos = sp.first_pos;
+    const int blk_begin = p * P.part_blocks;  // numbered as in Span
+    const int nb_local = min(blk_begin + P.part_blocks, sp.total) - blk_begin;
     const int my_n = nb_local > warp ? (nb_local - warp + NW - 1) / NW : 0;  // <= 32
 
     const int c = lane % LPT;   // chunk lane within a token row
@@ -265,7 +325,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
 
     // one block-table entry per lane: local block warp + NW*lane
     int my_bid = -1;
-    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + blk_begin + warp + NW * lane];
+    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + sp.block(blk_begin + warp + NW * lane)];
 
     const uint64_t pol = pa::l2_evict_first_policy();
     const size_t head_stride = (size_t)SH::TILE_BYTES;
@@ -289,7 +349,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
 
     // q for the G heads, this lane's dims, pre-scaled into the base-2 domain
     // (an E4M3 cache folds the KV head's K scale in here: q.(code*s) = (q*s).code)
-    const float qscale = EB == 1 ? P.scale_log2 * P.k_scale[kvh] : P.scale_log2;
+    const float qscale = EB == 1 && !BSC ? P.scale_log2 * P.k_scale[kvh] : P.scale_log2;
     float2 qf[G][NCH][4];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
@@ -333,6 +393,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
             for (int k = 0; k < 4; ++k) o[h][j][k] = make_float2(0.f, 0.f);
 
     for (int s = 0; s < S && s < my_n; ++s) issue(s);
+    BlockScales<BSC> scales(P, my_bid, kvh, 1.f);
 
     int consumed = 0;
     bool aborted = false;
@@ -348,7 +409,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
         if (bid >= 0 && bid < P.num_blocks) {
             const unsigned char* sK = my_stages + (size_t)st * 2 * SH::TILE_BYTES;
             const unsigned char* sV = sK + SH::TILE_BYTES;
-            const int tok0 = (blk_begin + warp + NW * i) * kBS;
+            const int tok0 = sp.block(blk_begin + warp + NW * i) * kBS;
 
             // ---- scores: partial dots over this lane's dims
             float sc[NV];
@@ -376,11 +437,12 @@ pa_decode_partition_kernel(const DecodeParams P) {
             TransposeReduce<NV, LPT / 2>::run(sc, lane);
 
             // ---- online softmax for this lane's head
+            scales.take(i);
             float tmax = -INFINITY;
 #pragma unroll
             for (int k = 0; k < NKEEP; ++k) {
                 const int t = (ip0 + k) * TPP + tg;
-                sc[k] = (tok0 + t < ctx && tok0 + t >= first_pos) ? sc[k] : -INFINITY;
+                sc[k] = visible(tok0 + t, ctx, first_pos, P.n_sinks) ? scales.score(sc[k]) : -INFINITY;
                 tmax = fmaxf(tmax, sc[k]);
             }
 #pragma unroll
@@ -396,7 +458,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
                 psum += pk;
                 pbuf[h_own * kBS + tg * NPASS + ip0 + k] = pk;
             }
-            l_run = l_run * alpha + psum;
+            l_run = l_run * alpha + scales.weight(psum);
             m_run = m_new;
             if (alpha_writer) abuf[h_own] = alpha;
             const bool any_changed = __any_sync(kFull, changed);
@@ -428,7 +490,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
 #pragma unroll
             for (int ip = 0; ip < NPASS; ++ip) {
                 const int t = ip * TPP + tg;
-                if (tok0 + t < ctx && tok0 + t >= first_pos) {
+                if (visible(tok0 + t, ctx, first_pos, P.n_sinks)) {
 #pragma unroll
                     for (int j = 0; j < NCH; ++j) {
                         float2 vf[4];
@@ -492,8 +554,8 @@ pa_decode_partition_kernel(const DecodeParams P) {
     }
     __syncthreads();
 
-    const bool single = (nparts == 1);
-    const float vscale = EB == 1 ? P.v_scale[kvh] : 1.f;  // sum p (code*s) = s * sum p code
+    const bool single = (sp.nparts == 1);
+    const float vscale = EB == 1 && !BSC ? P.v_scale[kvh] : 1.f;  // sum p (code*s) = s * sum p code
     for (int e = threadIdx.x; e < G * D / 2; e += NW * 32) {
         const int h = e / (D / 2), d = (e % (D / 2)) * 2;
         float M = -INFINITY;
@@ -630,7 +692,7 @@ __device__ __forceinline__ uint32_t sw_off(int row, int dims8) {
 
 }  // namespace mma
 
-template <int G, int EB>
+template <int G, int EB, bool BSC>
 __global__ void __launch_bounds__(mma::kNW * 32, EB == 1 ? 4 : 3)
 pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
@@ -664,20 +726,12 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
         }
         return;
     }
-    int nblk = (ctx + kBS - 1) / kBS;
-    const int first_pos = first_position(P, ctx);
-    int blk_first = first_pos / kBS;
-    int nparts = (nblk - blk_first + P.part_blocks - 1) / P.part_blocks;
-    if (nblk > P.max_blocks || nparts > P.max_parts) {  // caller broke the bounds it passed
-        if (p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
-        nblk = min(nblk, P.max_blocks);
-        blk_first = min(blk_first, nblk);
-        nparts = min((nblk - blk_first + P.part_blocks - 1) / P.part_blocks, P.max_parts);
-        nblk = min(nblk, blk_first + nparts * P.part_blocks);
-    }
-    if (p >= nparts) return;
-    const int blk_begin = blk_first + p * P.part_blocks;
-    const int nb_local = min(blk_begin + P.part_blocks, nblk) - blk_begin;
+    const Span sp(P, ctx);
+    if (sp.over && p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
+    if (p >= sp.nparts) return;
+    const int first_pos = sp.first_pos;
+    const int blk_begin = p * P.part_blocks;  // numbered as in Span
+    const int nb_local = min(blk_begin + P.part_blocks, sp.total) - blk_begin;
     const int my_n = nb_local > warp ? (nb_local - warp + NW - 1) / NW : 0;  // <= 32
 
     unsigned char* my_stages = stages + (size_t)warp * kWarp;
@@ -690,7 +744,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
     __syncwarp();
 
     int my_bid = -1;  // one block-table entry per lane: local block warp + NW*lane
-    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + blk_begin + warp + NW * lane];
+    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + sp.block(blk_begin + warp + NW * lane)];
 
     const uint64_t pol = pa::l2_evict_first_policy();
     auto issue = [&](int i) {  // all lanes call (shuffle); lanes 0..3 issue the four boxes
@@ -750,9 +804,10 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
     // their sums (the same reference on the 8 lanes of a head)
     float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
     // E4M3 cache: q.(code*s_k) = s_k (q.code), folded into the score scale
-    const float sc = EB == 1 ? P.scale_log2 * P.k_scale[kvh] : P.scale_log2;
+    const float sc = EB == 1 && !BSC ? P.scale_log2 * P.k_scale[kvh] : P.scale_log2;
 
     for (int s = 0; s < S && s < my_n; ++s) issue(s);
+    BlockScales<BSC> scales(P, my_bid, kvh, P.scale_log2);  // BSC: a score is s * k + e instead of s * sc
     int consumed = 0;
     bool aborted = false;
     for (int i = 0; i < my_n; ++i) {
@@ -767,7 +822,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
         if (bid >= 0 && bid < P.num_blocks) {
             const uint32_t kb = pa::smem_u32(my_stages + (size_t)st * kStage);
             const uint32_t vb = kb + 4096;  // bf16 cache: the V tile
-            const int tok0 = (blk_begin + warp + NW * i) * kBS;
+            const int tok0 = sp.block(blk_begin + warp + NW * i) * kBS;
             // ---- S = Q K^T: two n-tiles of 8 tokens
             float s_acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
             if constexpr (EB == 2) {
@@ -809,10 +864,12 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
                 // so far on the head's first visible keys and whenever a p could leave
                 // fp16's range (the key at the maximum gets p = 1 exactly)
                 float sv[4], pv[4];
+                scales.take(i);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int pos = tok0 + g + 8 * (u >> 1);
-                    sv[u] = (pos < ctx && pos >= first_pos) ? sT[u] * sc : -INFINITY;
+                    const float s2 = BSC ? scales.score(sT[u]) : sT[u] * sc;
+                    sv[u] = visible(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
                 }
                 auto exps = [&]() {
 #pragma unroll
@@ -848,8 +905,8 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
                     }
                     exps();
                 }
-                l2[0] += pv[0] + pv[2];
-                l2[1] += pv[1] + pv[3];
+                l2[0] += scales.weight(pv[0] + pv[2]);
+                l2[1] += scales.weight(pv[1] + pv[3]);
                 // P^T as the B operand (tokens 2t, 2t+1 | 2t+8, 2t+9 of head g): the
                 // fp16 pairs (token g; heads 2t, 2t+1) of each 8 x 8 half, transposed
                 ph[0] = movmatrix_t(f2_to_h2(pv[0], pv[1]));
@@ -863,7 +920,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int pos = tok0 + 8 * n + 2 * t + k;
-                        sv[2 * n + k] = (pos < ctx && pos >= first_pos) ? s_acc[n][k] * sc : -INFINITY;
+                        sv[2 * n + k] = visible(pos, ctx, first_pos, P.n_sinks) ? s_acc[n][k] * sc : -INFINITY;
                     }
                 float tmax = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
                 tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 1));
@@ -902,15 +959,14 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
                                                  pv[2 * n + 1] - __uint_as_float(by & 0xffff0000u));
                 }
             }
-            // V rows of the sequence's last, partial block past the context hold
-            // whatever the pool has there (p = 0 must not meet a NaN): zero them
-            // (E4M3: in registers, below)
-            if (EB == 2 && ctx < tok0 + kBS) {
-                const int r0 = ctx - tok0;
+            // V rows that the query does not see (past the context, before the
+            // window) hold whatever the pool has there, and p = 0 must not meet
+            // a NaN: zero them (E4M3: in registers, below)
+            if (EB == 2 && (ctx < tok0 + kBS || (tok0 < first_pos && tok0 + kBS > P.n_sinks))) {
                 unsigned char* vt = my_stages + (size_t)st * kStage + 4096;
-                for (int e = lane; e < (kBS - r0) * 32; e += 32)  // a row: 2 boxes x 128 B
-                    *reinterpret_cast<uint2*>(vt + ((e & 31) >> 4) * 2048 + (r0 + (e >> 5)) * 128 + (e & 15) * 8) =
-                        make_uint2(0u, 0u);
+                for (int r = 0; r < kBS; ++r)
+                    if (!visible(tok0 + r, ctx, first_pos, P.n_sinks))  // a row: 2 boxes x 128 B
+                        *reinterpret_cast<uint2*>(vt + (lane >> 4) * 2048 + r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
                 tc::fence_async_smem();  // before the stage's next TMA fill
                 __syncwarp();
             }
@@ -932,10 +988,11 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
                 // codes 4t, 4t+1 are rows 2t, 2t+1 and codes 4t+2, 4t+3 rows 8+2t,
                 // 9+2t. Widened to fp16 pairs they are the m8n8 fragments of V's
                 // four 8 x 8 (token, dim) blocks; a movmatrix transpose makes each
-                // the matching block of V^T, the A operand. Token rows past the
-                // context are zero (p = 0 must not meet a NaN).
+                // the matching block of V^T, the A operand. Token rows that the
+                // query does not see are zero (p = 0 must not meet a NaN).
                 const unsigned char* rv = my_stages + (size_t)st * kStage + 2048;
-                const bool lo_ok = tok0 + g < ctx, hi_ok = tok0 + g + 8 < ctx;
+                const bool lo_ok = visible(tok0 + g, ctx, first_pos, P.n_sinks);
+                const bool hi_ok = visible(tok0 + g + 8, ctx, first_pos, P.n_sinks);
 #pragma unroll
                 for (int mt = 0; mt < 8; ++mt) {
                     const int off = ((mt ^ (g & 7)) << 4) + 4 * t;  // rows g and g + 8 share the swizzle
@@ -1000,7 +1057,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
     }
     __syncthreads();
 
-    const bool single = (nparts == 1);
+    const bool single = (sp.nparts == 1);
     for (int e = threadIdx.x; e < G * D / 2; e += NW * 32) {
         const int h = e / (D / 2), d = (e % (D / 2)) * 2;
         float M = -INFINITY;
@@ -1015,7 +1072,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
             O0 += ov.x * f;
             O1 += ov.y * f;
         }
-        if constexpr (EB == 1) {  // sum p (code * s_v) = s_v * sum p code
+        if constexpr (EB == 1 && !BSC) {  // sum p (code * s_v) = s_v * sum p code
             O0 *= P.v_scale[kvh];
             O1 *= P.v_scale[kvh];
         }
@@ -1051,9 +1108,7 @@ pa_decode_merge_kernel(const DecodeParams P, int n_rows) {
     const int b = row / H;
     const int ctx = P.ctx[b];
     if (ctx <= 0) return;
-    const int nblk = min((ctx + kBS - 1) / kBS, P.max_blocks);
-    const int blk_first = min(first_position(P, ctx) / kBS, nblk);
-    const int nparts = min((nblk - blk_first + P.part_blocks - 1) / P.part_blocks, P.max_parts);
+    const int nparts = Span(P, ctx).nparts;
     if (nparts <= 1) return;  // the partition kernel wrote this row
     const size_t slot0 = (size_t)row * P.max_parts;
     float m_mine = -INFINITY, l_mine = 0.f;  // this lane's partitions, relative to m_mine
@@ -1130,11 +1185,11 @@ struct Launch {
     static constexpr int S = FP8_WIDE ? 2 : (D == 128 ? 2 : 4) * (MINB == 3 ? 1 : 3) / (MINB == 3 ? 1 : 2) * (2 / EB);
 };
 
-template <int D, int G, int EB>
+template <int D, int G, int EB, bool BSC>
 int launch_partition(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     using LC = Launch<D, G, EB>;
     using SM = Smem<D, G, LC::LPT, EB, kNW, LC::S>;
-    auto kern = pa_decode_partition_kernel<D, G, LC::LPT, EB, kNW, LC::S, LC::MINB>;
+    auto kern = pa_decode_partition_kernel<D, G, LC::LPT, EB, BSC, kNW, LC::S, LC::MINB>;
     static bool attr_done[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1148,22 +1203,22 @@ int launch_partition(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     return pa_launch_pdl(kern, grid, dim3(kNW * 32), SM::TOTAL, stream, P);
 }
 
-template <int D, int EB>
+template <int D, int EB, bool BSC = false>
 int dispatch_group(int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_partition<D, 1, EB>(P, n_seqs, stream);
-        case 2: return launch_partition<D, 2, EB>(P, n_seqs, stream);
-        case 4: return launch_partition<D, 4, EB>(P, n_seqs, stream);
-        case 8: return launch_partition<D, 8, EB>(P, n_seqs, stream);
+        case 1: return launch_partition<D, 1, EB, BSC>(P, n_seqs, stream);
+        case 2: return launch_partition<D, 2, EB, BSC>(P, n_seqs, stream);
+        case 4: return launch_partition<D, 4, EB, BSC>(P, n_seqs, stream);
+        case 8: return launch_partition<D, 8, EB, BSC>(P, n_seqs, stream);
         default: return PA_ERR_UNSUPPORTED;
     }
 }
 
 // The tensor-core partition kernel (head_dim 128, bf16 cache): K and V pools
 // as 2-D TMA maps of [num_blocks * n_kv_heads * 16 rows][128 dims].
-template <int G, int EB>
+template <int G, int EB, bool BSC>
 int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
-    auto kern = pa_decode_mma_kernel<G, EB>;
+    auto kern = pa_decode_mma_kernel<G, EB, BSC>;
     constexpr int kSmem = mma::Lay<EB>::kSmem;
     static bool attr_done[64] = {false};
     int dev = 0;
@@ -1182,6 +1237,17 @@ int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream)
     if (!maps) return PA_ERR_CUDA;
     const dim3 grid = P.items ? dim3((unsigned)P.n_items) : dim3(P.max_parts, P.n_kv_heads, n_seqs);
     return pa_launch_pdl(kern, grid, dim3(mma::kNW * 32), kSmem, stream, P, tk, tv);
+}
+
+template <int EB, bool BSC = false>
+int dispatch_group_mma(int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
+    switch (G) {
+        case 1: return launch_partition_mma<1, EB, BSC>(P, n_seqs, stream);
+        case 2: return launch_partition_mma<2, EB, BSC>(P, n_seqs, stream);
+        case 4: return launch_partition_mma<4, EB, BSC>(P, n_seqs, stream);
+        case 8: return launch_partition_mma<8, EB, BSC>(P, n_seqs, stream);
+        default: return PA_ERR_UNSUPPORTED;
+    }
 }
 
 constexpr int kDefaultPartitionTokens = 512;
@@ -1239,9 +1305,10 @@ int wave_partition_tokens(int n_seqs, int n_kv_heads, int context, int sms, int 
 }
 
 int default_partition_tokens(bool tensor, int eb, int n_seqs, int n_kv_heads, int G, int head_dim,
-                             int max_context_len, int window) {
+                             int max_context_len, int window, int n_sinks = 0) {
     if (tensor) return 2 * kDefaultPartitionTokens;
-    const int span = window >= 0 && window + 2 * kBS < max_context_len ? window + 2 * kBS : max_context_len;
+    const long long wide = (long long)window + n_sinks + (n_sinks > 0 ? 3 : 2) * kBS;  // a window and its sinks
+    const int span = window >= 0 && wide < max_context_len ? (int)wide : max_context_len;
     const int sms = sm_count();
     return wave_partition_tokens(n_seqs, n_kv_heads, span, sms, sms * k1_ctas_per_sm(head_dim, G, eb));
 }
@@ -1289,7 +1356,8 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
                 const int32_t* context_lens, float scale, int n_heads, int n_kv_heads, int head_dim,
                 int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len, int num_blocks,
                 int window, int partition_tokens, void* workspace, size_t workspace_bytes,
-                pa_stream_t stream, bool force_tc = false, const int32_t* items = nullptr, int n_items = 0) {
+                pa_stream_t stream, bool force_tc = false, const int32_t* items = nullptr, int n_items = 0,
+                int n_sinks = 0, bool block_scaled = false) {
     if (n_seqs < 0 || max_context_len < 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
         n_heads <= 0 || n_kv_heads <= 0)
         return PA_ERR_INVALID_ARG;
@@ -1313,7 +1381,8 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     // CTA's fixed cost over more of them (measured 3-5% faster). The workspace
     // for 512 covers every one of them.
     const int pt = partition_tokens == 0
-                       ? default_partition_tokens(tensor, eb, n_seqs, n_kv_heads, G, head_dim, max_context_len, window)
+                       ? default_partition_tokens(tensor, eb, n_seqs, n_kv_heads, G, head_dim, max_context_len, window,
+                                                  n_sinks)
                        : resolve_partition_tokens(partition_tokens);
     if (pt < 0) return PA_ERR_INVALID_ARG;
     if (pt / kBS > 32 * kNW) return PA_ERR_INVALID_ARG;  // one table entry per lane
@@ -1326,10 +1395,10 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
         return PA_ERR_INVALID_ARG;
     if (out == q) return PA_ERR_INVALID_ARG;
     int max_parts = max_context_len > 0 ? (max_context_len + pt - 1) / pt : 1;
-    if (window >= 0) {  // W + 1 positions touch at most ceil((W + 16) / 16) blocks
-        const int wblocks = (window + 2 * kBS - 1) / kBS;
-        const int wparts = (wblocks + pt / kBS - 1) / (pt / kBS);
-        if (wparts < max_parts) max_parts = wparts;
+    if (window >= 0) {  // W + 1 positions touch at most ceil((W + 16) / 16) blocks, the sinks ceil(S / 16)
+        const long long wblocks = ((long long)window + 2 * kBS - 1) / kBS + ((long long)n_sinks + kBS - 1) / kBS;
+        const long long wparts = (wblocks + pt / kBS - 1) / (pt / kBS);
+        if (wparts < max_parts) max_parts = (int)wparts;
     }
     const size_t need = workspace_bytes_for(n_seqs, n_heads, head_dim, max_parts);
     if (need > 0 && (!workspace || workspace_bytes < need || !pa_aligned16(workspace)))
@@ -1359,6 +1428,7 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     P.part_blocks = pt / kBS;
     P.max_parts = max_parts;
     P.window = window;
+    P.n_sinks = n_sinks;
     P.err = err;
     P.items = reinterpret_cast<const int4*>(items);
     P.n_items = n_items;
@@ -1367,25 +1437,17 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int st;
     if (tensor) {
-        if (eb == 2) {
-            switch (G) {
-                case 1: st = launch_partition_mma<1, 2>(P, n_seqs, s); break;
-                case 2: st = launch_partition_mma<2, 2>(P, n_seqs, s); break;
-                case 4: st = launch_partition_mma<4, 2>(P, n_seqs, s); break;
-                default: st = launch_partition_mma<8, 2>(P, n_seqs, s); break;
-            }
-        } else {
-            switch (G) {
-                case 1: st = launch_partition_mma<1, 1>(P, n_seqs, s); break;
-                case 2: st = launch_partition_mma<2, 1>(P, n_seqs, s); break;
-                case 4: st = launch_partition_mma<4, 1>(P, n_seqs, s); break;
-                default: st = launch_partition_mma<8, 1>(P, n_seqs, s); break;
-            }
-        }
-    } else if (eb == 1)
+        st = eb == 2 ? dispatch_group_mma<2>(G, P, n_seqs, s)
+             : block_scaled ? dispatch_group_mma<1, true>(G, P, n_seqs, s)
+                            : dispatch_group_mma<1>(G, P, n_seqs, s);
+    } else if (eb == 1 && block_scaled) {
+        st = head_dim == 128 ? dispatch_group<128, 1, true>(G, P, n_seqs, s)
+                             : dispatch_group<64, 1, true>(G, P, n_seqs, s);
+    } else if (eb == 1) {
         st = head_dim == 128 ? dispatch_group<128, 1>(G, P, n_seqs, s) : dispatch_group<64, 1>(G, P, n_seqs, s);
-    else
+    } else {
         st = head_dim == 128 ? dispatch_group<128, 2>(G, P, n_seqs, s) : dispatch_group<64, 2>(G, P, n_seqs, s);
+    }
     if (st != PA_OK || max_parts <= 1) return st;
     const int n_rows = n_seqs * n_heads;
     dim3 grid((n_rows + 3) / 4);
@@ -1444,6 +1506,34 @@ extern "C" int pa_decode_fp8(void* out, const void* q, const void* k_pool, const
                        stream);
 }
 
+extern "C" int pa_decode_sinks(void* out, const void* q, const void* k_pool, const void* v_pool,
+                               const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                               const int32_t* context_lens, float scale, int n_heads, int n_kv_heads, int head_dim,
+                               int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len, int num_blocks,
+                               int window, int n_sinks, int partition_tokens, void* workspace, size_t workspace_bytes,
+                               pa_stream_t stream) {
+    if (window < 0 || n_sinks < 0 || (k_scale == nullptr) != (v_scale == nullptr)) return PA_ERR_INVALID_ARG;
+    if (n_sinks > max_context_len) n_sinks = max_context_len;
+    return decode_impl(k_scale ? 1 : 2, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                       n_heads, n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len,
+                       num_blocks, window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0,
+                       n_sinks);
+}
+
+extern "C" int pa_decode_fp8_block(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                   const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                   const int32_t* context_lens, float scale, int n_heads, int n_kv_heads, int head_dim,
+                                   int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len,
+                                   int num_blocks, int window, int n_sinks, int partition_tokens, void* workspace,
+                                   size_t workspace_bytes, pa_stream_t stream) {
+    if (window < -1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
+    if (window < 0) n_sinks = 0;  // everything is visible
+    if (n_sinks > max_context_len) n_sinks = max_context_len;
+    return decode_impl(1, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, n_heads,
+                       n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len, num_blocks,
+                       window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0, n_sinks, true);
+}
+
 extern "C" int pa_decode(void* out, const void* q, const void* k_pool, const void* v_pool,
                          const int32_t* block_tables, const int32_t* context_lens, float scale,
                          int n_heads, int n_kv_heads, int head_dim, int block_size, int n_seqs,
@@ -1482,9 +1572,9 @@ extern "C" int pa_decode_plan(const int32_t* context_lens, int n_seqs, int n_hea
     const int part_blocks = pt / kBS;
     int max_parts = max_context_len > 0 ? (max_context_len + pt - 1) / pt : 1;
     if (window >= 0) {
-        const int wblocks = (window + 2 * kBS - 1) / kBS;
-        const int wparts = (wblocks + part_blocks - 1) / part_blocks;
-        if (wparts < max_parts) max_parts = wparts;
+        const long long wblocks = ((long long)window + 2 * kBS - 1) / kBS;
+        const long long wparts = (wblocks + part_blocks - 1) / part_blocks;
+        if (wparts < max_parts) max_parts = (int)wparts;
     }
     // per sequence: its partition count and the blocks of its last partition
     std::vector<int> nparts(n_seqs), last_blocks(n_seqs);

@@ -37,3 +37,36 @@ def test_rope_argument_errors_need_no_device(capi, over, status):
         if a["T"] > 0:
             assert capi.pa_rope_and_cache_fp8_block(a["qo"], a["q"], a["k"], a["v"], a["kp"], a["vp"], None, p, a["cs"],
                                                     a["pos"], a["slots"], *tail) == -1
+
+
+# -------------------------------- decode: window with sinks, block scales --
+
+def _dec(capi, fn, **over):
+    p = C.c_void_p(4096)
+    a = dict(out=C.c_void_p(8192), q=p, k=p, v=p, ks=None, vs=None, tab=p, ctx=p, scale=0.1, H=8, Hk=2, D=128, bs=16,
+             B=4, maxb=64, maxctx=1024, nb=256, window=100, sinks=4, pt=0, ws=None, wsb=0)
+    if fn == "pa_decode_fp8_block":
+        a.update(ks=p, vs=p)
+    a.update(over)
+    return getattr(capi, fn)(a["out"], a["q"], a["k"], a["v"], a["ks"], a["vs"], a["tab"], a["ctx"], a["scale"], a["H"],
+                             a["Hk"], a["D"], a["bs"], a["B"], a["maxb"], a["maxctx"], a["nb"], a["window"], a["sinks"],
+                             a["pt"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("fn", ["pa_decode_sinks", "pa_decode_fp8_block"])
+@pytest.mark.parametrize("over,status", [
+    (dict(B=0), 0), (dict(window=-2), -1), (dict(sinks=-1), -1), (dict(D=96), -2), (dict(bs=32), -2),
+    (dict(H=6, Hk=2), -2), (dict(H=7, Hk=2), -1), (dict(q=None), -1), (dict(out=C.c_void_p(4096)), -1),
+    (dict(k=C.c_void_p(4104)), -1), (dict(pt=100), -1), (dict(maxb=8), -1), (dict(vs=None, ks=C.c_void_p(4096)), -1),
+    (dict(ks=C.c_void_p(4098), vs=C.c_void_p(4096)), -1),
+    # 100 + 2048 positions in 64-token partitions need split-K scratch; a window alone of 20 does not
+    (dict(window=2000, sinks=100, maxctx=4096, maxb=256, pt=64), -3), (dict(B=-1), -1),
+])
+def test_decode_sinks_argument_errors_need_no_device(capi, fn, over, status):
+    assert _dec(capi, fn, **over) == status
+
+
+def test_decode_sinks_needs_a_window(capi):
+    assert _dec(capi, "pa_decode_sinks", window=-1) == -1
+    assert _dec(capi, "pa_decode_fp8_block", window=-1, B=0) == 0
+    assert _dec(capi, "pa_decode_fp8_block", ks=None, vs=None) == -1
