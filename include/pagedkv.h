@@ -460,6 +460,14 @@ int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const
                                 int block_size, int num_blocks, pa_stream_t stream);
 
 /*
+ * pa_copy_blocks_ex (E4M3 pools) that copies the blocks' rows of k_scale and
+ * v_scale too, in the same launch.
+ */
+int pa_copy_blocks_fp8_block(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                             const int64_t* block_mapping, int n_pairs, int n_kv_heads, int head_dim,
+                             int block_size, int num_blocks, pa_stream_t stream);
+
+/*
  * Decode over such a cache: pa_decode_fp8 with the scales of each block,
  *     K_b[t] = code * k_scale[block of t][kv head], V_b[t] likewise.
  * window -1: every position; window >= 0: as pa_decode_sinks, n_sinks too
@@ -575,6 +583,45 @@ int pa_prefill_paged_ex(void* out, const void* q, const void* k_pool, const void
                         int max_chunk_len, int num_blocks, int splits, void* workspace,
                         size_t workspace_bytes, pa_stream_t stream);
 
+/*
+ * Prefill under a sliding window with sinks: pa_prefill_paged_ex where row i
+ * of a chunk, at position p = context_lens[s] - L_s + i, attends to t <= p with
+ * t >= p - window or t < n_sinks (the rule of pa_decode_sinks, so a prompt
+ * prefilled in chunks and then decoded sees one mask).
+ * Only key tiles with a visible position are read: table entries of blocks
+ * between the sinks and the window of the chunk's first row, position
+ * context_lens[s] - L_s - window, may be -1. V rows of positions that no row
+ * of the chunk sees may hold anything; a non-finite V element of a visible
+ * position spoils (and flags) the rows that share its key tile, also where it
+ * is masked for them, as in pa_prefill_paged.
+ * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG. splits and workspace
+ * as for pa_prefill_paged_ex.
+ */
+int pa_prefill_sinks(void* out, const void* q, const void* k_pool, const void* v_pool,
+                     const int32_t* block_tables, const int32_t* context_lens,
+                     const int32_t* q_start_loc, float scale, int n_heads, int n_kv_heads,
+                     int head_dim, int block_size, int n_seqs, int max_blocks_per_seq,
+                     int max_chunk_len, int num_blocks, int window, int n_sinks, int splits,
+                     void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * Prefill over an E4M3 cache with a scale per (block, KV head) (see
+ * pa_rope_and_cache_fp8_block): pa_prefill_paged_ex (window -1; n_sinks is
+ * ignored) or pa_prefill_sinks (window >= 0) with K and V as codes times their
+ * block's scale. Q.K^T and P.V run on the tcgen05 tensor cores in fp16 with
+ * fp32 accumulation: codes widen exactly, q is converted to fp16 (exact for
+ * |q| in its normal range, 2^-14 .. 65504; larger ones give non-finite outputs
+ * and set PA_DEVERR_RANGE), and the softmax weight times V's scale is rounded
+ * to fp16, as in pa_decode_fp8_block.
+ */
+int pa_prefill_fp8_block(void* out, const void* q, const void* k_pool, const void* v_pool,
+                         const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                         const int32_t* context_lens, const int32_t* q_start_loc, float scale,
+                         int n_heads, int n_kv_heads, int head_dim, int block_size, int n_seqs,
+                         int max_blocks_per_seq, int max_chunk_len, int num_blocks, int window,
+                         int n_sinks, int splits, void* workspace, size_t workspace_bytes,
+                         pa_stream_t stream);
+
 /* ----------------------------------------------------------- diagnostics */
 
 /* Reads the current device's error word into *flags_out (a PA_DEVERR_* mask)
@@ -644,6 +691,14 @@ int pa_bm_free_seq(pa_bm* bm, int64_t seq_id);
  * PA_ERR_INVALID_ARG. *n_released_out = entries dropped by this call.
  */
 int pa_bm_release_before(pa_bm* bm, int64_t seq_id, int64_t first_pos, int* n_released_out);
+
+/*
+ * The same for a window with sinks (pa_decode_sinks): drops every block that
+ * lies wholly in [from_pos, to_pos) (clamped to [0, len]), so that the blocks
+ * of the sinks stay; pa_bm_release_before is from_pos = 0.
+ * PA_ERR_INVALID_ARG if from_pos > to_pos or from_pos < 0.
+ */
+int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t to_pos, int* n_released_out);
 
 /*
  * Preemption by swapping ([MA] 9.1 "Batching and the scheduler": a preempted

@@ -25,6 +25,7 @@ __all__ = [
     "prefill_workspace", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_window",
     "pa_swap_out_blocks", "pa_swap_in_blocks", "pa_get_device_error", "pa_rope_and_cache",
     "pa_rope_and_cache_fp8_block", "pa_decode_sinks", "pa_decode_fp8_block",
+    "pa_prefill_sinks", "pa_prefill_fp8_block", "pa_copy_blocks_fp8_block",
     "BlockManager", "load", "PagedKVError",
 ]
 
@@ -573,6 +574,69 @@ def pa_prefill_paged_ex(out, q, k_pool, v_pool, block_tables, context_lens, q_st
     check("pa_prefill_paged_ex", st)
 
 
+def _prefill_call(fn: str, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, q_start_loc, scale,
+                  max_chunk_len, window, n_sinks, splits, workspace, stream) -> None:
+    torch = _torch()
+    n_rows, n_heads, head_dim = q.shape
+    num_blocks, n_kv_heads, block_size, hd2 = k_pool.shape
+    n_seqs = context_lens.numel()
+    if hd2 != head_dim or v_pool.shape != k_pool.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the pools")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n_seqs or q_start_loc.numel() != n_seqs + 1:
+        raise ValueError("block_tables must be [n_seqs][max_blocks], q_start_loc [n_seqs + 1]")
+    dev = _same_device(q=q, out=out, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
+                       block_tables=block_tables, context_lens=context_lens, q_start_loc=q_start_loc, workspace=workspace)
+    if k_scale is None:
+        pools = [_ptr(k_pool, "k_pool", bf16=True), _ptr(v_pool, "v_pool", bf16=True)]
+    else:
+        n = num_blocks * n_kv_heads
+        if k_scale.numel() != n or v_scale.numel() != n:
+            raise ValueError(f"k_scale and v_scale need {n} entries")
+        pools = [_fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool"),
+                 _ptr(k_scale, "k_scale", dtype=torch.float32), _ptr(v_scale, "v_scale", dtype=torch.float32)]
+    ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace, "workspace"),
+                                                        workspace.numel() * workspace.element_size())
+    _call(fn, dev, stream, _ptr(out, "out", bf16=True), _ptr(q, "q", bf16=True), *pools,
+          _ptr(block_tables, "block_tables", dtype=torch.int32), _ptr(context_lens, "context_lens", dtype=torch.int32),
+          _ptr(q_start_loc, "q_start_loc", dtype=torch.int32), scale, n_heads, n_kv_heads, head_dim, block_size, n_seqs,
+          block_tables.shape[1], max_chunk_len, num_blocks, window, n_sinks, splits, ws, ws_bytes)
+
+
+def pa_prefill_sinks(out, q, k_pool, v_pool, block_tables, context_lens, q_start_loc, scale: float, max_chunk_len: int,
+                     window: int, n_sinks: int, splits: int = 0, workspace=None, stream=None) -> None:
+    """pa_prefill_paged_ex under a sliding window whose first n_sinks positions
+    stay visible: a row at position p attends to t <= p with t >= p-window or
+    t < n_sinks. Workspace: prefill_workspace."""
+    _prefill_call("pa_prefill_sinks", out, q, k_pool, v_pool, None, None, block_tables, context_lens, q_start_loc, scale,
+                  max_chunk_len, window, n_sinks, splits, workspace, stream)
+
+
+def pa_prefill_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, q_start_loc, scale: float,
+                         max_chunk_len: int, window: int = -1, n_sinks: int = 0, splits: int = 0, workspace=None,
+                         stream=None) -> None:
+    """pa_prefill_paged_ex (or, with window >= 0, pa_prefill_sinks) over an E4M3
+    cache with a scale per block and head."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale are needed")
+    _prefill_call("pa_prefill_fp8_block", out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                  q_start_loc, scale, max_chunk_len, window, n_sinks, splits, workspace, stream)
+
+
+def pa_copy_blocks_fp8_block(k_pool, v_pool, k_scale, v_scale, block_mapping, stream=None) -> None:
+    """pa_copy_blocks of an E4M3 cache with a scale per block and head: the
+    blocks' rows of k_scale and v_scale [num_blocks][n_kv_heads] are copied too."""
+    torch = _torch()
+    num_blocks, n_kv_heads, block_size, head_dim = k_pool.shape
+    if v_pool.shape != k_pool.shape or k_scale.numel() != num_blocks * n_kv_heads or v_scale.numel() != k_scale.numel():
+        raise ValueError("k_pool and v_pool must have one shape, the scales num_blocks * n_kv_heads entries")
+    n_pairs = block_mapping.shape[0] if block_mapping.numel() else 0
+    dev = _same_device(k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, block_mapping=block_mapping)
+    _call("pa_copy_blocks_fp8_block", dev, stream, _fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool"),
+          _ptr(k_scale, "k_scale", dtype=torch.float32), _ptr(v_scale, "v_scale", dtype=torch.float32),
+          _ptr(block_mapping, "block_mapping", dtype=torch.int64) if n_pairs else None, n_pairs, n_kv_heads, head_dim,
+          block_size, num_blocks)
+
+
 def pa_get_device_error() -> int:
     """Reads and clears the device error word (a PA_DEVERR_* mask)."""
     v = C.c_int(0)
@@ -669,6 +733,14 @@ class BlockManager:
         window); their table entries become -1. Returns how many were dropped."""
         n = C.c_int(0)
         check("pa_bm_release_before", self._lib.pa_bm_release_before(self._h, seq_id, first_pos, C.byref(n)))
+        return n.value
+
+    def release_between(self, seq_id: int, from_pos: int, to_pos: int) -> int:
+        """Drops the blocks that lie wholly in [from_pos, to_pos), as
+        release_before does (a window whose sinks, positions below from_pos,
+        stay). Returns how many were dropped."""
+        n = C.c_int(0)
+        check("pa_bm_release_between", self._lib.pa_bm_release_between(self._h, seq_id, from_pos, to_pos, C.byref(n)))
         return n.value
 
     def block_table(self, seq_id: int) -> List[int]:

@@ -72,6 +72,11 @@ SIGNATURES = {
                                 i32, i32, i32, vp, i32, vp, C.c_size_t, vp]),
     "pa_prefill_paged": (i32, [vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32,
                                i32, i32, vp]),
+    "pa_prefill_sinks": (i32, [vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                               i32, vp, C.c_size_t, vp]),
+    "pa_prefill_fp8_block": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32, i32, i32,
+                                   i32, i32, i32, vp, C.c_size_t, vp]),
+    "pa_copy_blocks_fp8_block": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
     "pa_prefill_workspace_bytes": (C.c_size_t, [i32, i32, i32, i32, i32]),
     "pa_prefill_paged_ex": (i32, [vp, vp, vp, vp, vp, vp, vp, C.c_float, i32, i32, i32, i32, i32, i32,
                                   i32, i32, i32, vp, C.c_size_t, vp]),
@@ -86,6 +91,7 @@ SIGNATURES = {
     "pa_bm_fork": (i32, [vp, i64, i64]),
     "pa_bm_free_seq": (i32, [vp, i64]),
     "pa_bm_release_before": (i32, [vp, i64, i64, C.POINTER(C.c_int)]),
+    "pa_bm_release_between": (i32, [vp, i64, i64, i64, C.POINTER(C.c_int)]),
     "pa_bm_swap_out": (i32, [vp, i64, p_i32, i32, C.POINTER(C.c_int)]),
     "pa_bm_swap_in": (i32, [vp, i64, p_i32, i32, C.POINTER(C.c_int)]),
     "pa_bm_cache_blocks": (i32, [vp, i64, p_i32, i64, C.POINTER(C.c_int)]),

@@ -237,16 +237,20 @@ int pa_bm_free_seq(pa_bm* bm, int64_t seq_id) {
 }
 
 int pa_bm_release_before(pa_bm* bm, int64_t seq_id, int64_t first_pos, int* n_released_out) {
-    if (!bm || !n_released_out) return PA_ERR_INVALID_ARG;
+    return pa_bm_release_between(bm, seq_id, 0, first_pos < 0 ? 0 : first_pos, n_released_out);
+}
+
+int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t to_pos, int* n_released_out) {
+    if (!bm || !n_released_out || from_pos < 0 || from_pos > to_pos) return PA_ERR_INVALID_ARG;
     auto it = bm->seqs.find(seq_id);
     if (it == bm->seqs.end()) return PA_ERR_REFCOUNT;
     pa_bm::Seq& s = it->second;
     if (s.swapped >= 0) return PA_ERR_INVALID_ARG;
-    if (first_pos < 0) first_pos = 0;
-    if (first_pos > s.len) first_pos = s.len;
-    const int64_t whole = first_pos / bm->block_size;  // blocks wholly before first_pos
+    if (from_pos > s.len) from_pos = s.len;
+    if (to_pos > s.len) to_pos = s.len;
+    const int64_t end = to_pos / bm->block_size;  // blocks wholly before to_pos
     int n = 0;
-    for (int64_t j = 0; j < whole && j < (int64_t)s.table.size(); ++j) {
+    for (int64_t j = (from_pos + bm->block_size - 1) / bm->block_size; j < end && j < (int64_t)s.table.size(); ++j) {
         if (s.table[j] >= 0) {
             bm->put(s.table[j]);
             s.table[j] = -1;

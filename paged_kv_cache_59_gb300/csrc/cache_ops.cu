@@ -106,16 +106,23 @@ reshape_and_cache_fp8_kernel(const uint4* __restrict__ k, const uint4* __restric
 }
 
 // grid.x = pair, grid.y = slice of the block; each CTA copies its slice of K
-// and of V for one pair. A block is n_kv_heads*16*head_dim*2 bytes.
+// and of V for one pair. A block is n_kv_heads*16*head_dim*2 bytes. A cache
+// with a scale per (block, KV head) has its rows of scales copied too.
 __global__ void __launch_bounds__(256)
 copy_blocks_kernel(uint4* __restrict__ k_pool, uint4* __restrict__ v_pool,
                    const int64_t* __restrict__ pairs, int chunks_per_block, int num_blocks,
-                   unsigned int* err) {
+                   unsigned int* err, float* __restrict__ k_scale, float* __restrict__ v_scale, int n_kv_heads) {
     const int pr = blockIdx.x;
     const int64_t src = pairs[2 * pr], dst = pairs[2 * pr + 1];
     if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
         if (blockIdx.y == 0 && threadIdx.x == 0) pa::set_error(err, PA_DEVERR_PAIR);
         return;
+    }
+    if (k_scale && blockIdx.y == 0) {
+        for (int h = threadIdx.x; h < n_kv_heads; h += blockDim.x) {
+            k_scale[dst * n_kv_heads + h] = k_scale[src * n_kv_heads + h];
+            v_scale[dst * n_kv_heads + h] = v_scale[src * n_kv_heads + h];
+        }
     }
     const long long s0 = src * (long long)chunks_per_block, d0 = dst * (long long)chunks_per_block;
     for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < chunks_per_block;
@@ -253,7 +260,8 @@ extern "C" int pa_reshape_and_cache_fp8(const void* k, const void* v, void* k_po
 
 namespace {
 int copy_blocks(void* k_pool, void* v_pool, const int64_t* block_mapping, int n_pairs, int n_kv_heads,
-                int head_dim, int block_size, int elem_bytes, int num_blocks, pa_stream_t stream) {
+                int head_dim, int block_size, int elem_bytes, int num_blocks, pa_stream_t stream,
+                float* k_scale = nullptr, float* v_scale = nullptr) {
     if (n_pairs < 0 || n_kv_heads <= 0 || head_dim <= 0 || num_blocks < 0) return PA_ERR_INVALID_ARG;
     if (elem_bytes != 1 && elem_bytes != 2) return PA_ERR_INVALID_ARG;
     if (block_size != kBS) return PA_ERR_UNSUPPORTED;
@@ -276,7 +284,7 @@ int copy_blocks(void* k_pool, void* v_pool, const int64_t* block_mapping, int n_
     dim3 grid(n_pairs, slices);
     copy_blocks_kernel<<<grid, threads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
         static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), block_mapping, (int)chunks, num_blocks,
-        err);
+        err, k_scale, v_scale, n_kv_heads);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 }  // namespace
@@ -293,4 +301,14 @@ extern "C" int pa_copy_blocks_ex(void* k_pool, void* v_pool, const int64_t* bloc
                                  pa_stream_t stream) {
     return copy_blocks(k_pool, v_pool, block_mapping, n_pairs, n_kv_heads, head_dim, block_size, elem_bytes,
                        num_blocks, stream);
+}
+
+extern "C" int pa_copy_blocks_fp8_block(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                        const int64_t* block_mapping, int n_pairs, int n_kv_heads, int head_dim,
+                                        int block_size, int num_blocks, pa_stream_t stream) {
+    if (n_pairs > 0 && (!k_scale || !v_scale || (reinterpret_cast<uintptr_t>(k_scale) & 3u) ||
+                        (reinterpret_cast<uintptr_t>(v_scale) & 3u)))
+        return PA_ERR_INVALID_ARG;
+    return copy_blocks(k_pool, v_pool, block_mapping, n_pairs, n_kv_heads, head_dim, block_size, 1, num_blocks, stream,
+                       k_scale, v_scale);
 }

@@ -41,7 +41,7 @@ bool pa_make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, ui
 }
 
 bool pa_make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
-                        uint64_t row_stride_bytes, uint32_t box_x, uint32_t box_y) {
+                        uint64_t row_stride_bytes, uint32_t box_x, uint32_t box_y, bool swizzle) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {inner, rows};
@@ -49,6 +49,7 @@ bool pa_make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint
     const cuuint32_t box[2] = {box_x, box_y};
     const cuuint32_t estride[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estride,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

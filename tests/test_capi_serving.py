@@ -70,3 +70,66 @@ def test_decode_sinks_needs_a_window(capi):
     assert _dec(capi, "pa_decode_sinks", window=-1) == -1
     assert _dec(capi, "pa_decode_fp8_block", window=-1, B=0) == 0
     assert _dec(capi, "pa_decode_fp8_block", ks=None, vs=None) == -1
+
+
+# ------------------------------- prefill: window with sinks, block scales --
+
+def _pf(capi, fn, **over):
+    p = C.c_void_p(4096)
+    a = dict(out=C.c_void_p(8192), q=p, k=p, v=p, ks=p, vs=p, tab=p, ctx=p, loc=p, scale=0.1, H=8, Hk=2, D=128, bs=16,
+             B=4, maxb=64, chunk=100, nb=256, window=100, sinks=4, splits=1, ws=None, wsb=0)
+    a.update(over)
+    scales = [a["ks"], a["vs"]] if fn == "pa_prefill_fp8_block" else []
+    return getattr(capi, fn)(a["out"], a["q"], a["k"], a["v"], *scales, a["tab"], a["ctx"], a["loc"], a["scale"], a["H"],
+                             a["Hk"], a["D"], a["bs"], a["B"], a["maxb"], a["chunk"], a["nb"], a["window"], a["sinks"],
+                             a["splits"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("fn", ["pa_prefill_sinks", "pa_prefill_fp8_block"])
+@pytest.mark.parametrize("over,status", [
+    (dict(B=0), 0), (dict(chunk=0), 0), (dict(window=-2), -1), (dict(sinks=-1), -1), (dict(D=96), -2), (dict(bs=32), -2),
+    (dict(H=6, Hk=2), -2), (dict(H=7, Hk=2), -1), (dict(q=None), -1), (dict(loc=None), -1),
+    (dict(out=C.c_void_p(4096)), -1), (dict(k=C.c_void_p(4104)), -1), (dict(splits=65), -1), (dict(splits=3), -3),
+    (dict(nb=2 ** 27), -2), (dict(B=-1), -1),
+])
+def test_prefill_sinks_argument_errors_need_no_device(capi, fn, over, status):
+    assert _pf(capi, fn, **over) == status
+
+
+def test_prefill_scales_and_windows(capi):
+    assert _pf(capi, "pa_prefill_sinks", window=-1) == -1
+    for over in (dict(ks=None), dict(vs=None), dict(ks=C.c_void_p(4098))):
+        assert _pf(capi, "pa_prefill_fp8_block", **over) == -1
+
+
+def test_copy_blocks_with_scales_argument_errors(capi):
+    p = C.c_void_p(4096)
+    assert capi.pa_copy_blocks_fp8_block(p, p, None, p, p, 3, 2, 64, 16, 16, None) == -1
+    assert capi.pa_copy_blocks_fp8_block(p, p, p, C.c_void_p(4098), p, 3, 2, 64, 16, 16, None) == -1
+    assert capi.pa_copy_blocks_fp8_block(p, p, p, p, p, 3, 2, 64, 8, 16, None) == -2
+    assert capi.pa_copy_blocks_fp8_block(p, p, p, p, None, 0, 2, 64, 16, 16, None) == 0
+
+
+# ------------------------------------------------ block manager: sinks stay --
+
+def test_release_between(capi):
+    from paged_kv_cache_59_gb300 import BlockManager, PagedKVError
+    bm = BlockManager(20, 16)
+    bm.add_seq(1)
+    bm.append_tokens(1, 200)                       # 13 blocks
+    tab = bm.block_table(1)
+    assert bm.release_between(1, 0, 0) == 0 and bm.release_between(1, 5, 31) == 0
+    assert bm.release_between(1, 17, 100) == 4     # blocks 2..5; 1 holds position 16, 6 position 100
+    assert bm.block_table(1) == tab[:2] + [-1] * 4 + tab[6:]
+    assert bm.release_between(1, 17, 100) == 0 and bm.num_free() == 7 + 4
+    assert bm.release_between(1, 16, 10 ** 9) == 7   # 1 and 6..11: the last block is not wholly before 200
+    assert bm.block_table(1) == tab[:1] + [-1] * 11 + tab[12:]
+    bm.fork(1, 2)
+    assert bm.release_between(2, 0, 16) == 1 and bm.refcount(tab[0]) == 1
+    for bad in ((-1, 5), (6, 5)):
+        with pytest.raises(PagedKVError):
+            bm.release_between(1, *bad)
+    with pytest.raises(PagedKVError):
+        bm.release_between(9, 0, 5)
+    bm.free_seq(1), bm.free_seq(2)
+    assert bm.num_free() == 20
