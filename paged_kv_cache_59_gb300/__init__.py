@@ -277,33 +277,41 @@ def pa_decode_fp8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, contex
     check("pa_decode_fp8", st)
 
 
-def _decode_call(fn: str, out, q, k_pool, v_pool, k_scale, v_scale, scale_numel, block_tables, context_lens, scale,
-                 max_context_len, window, n_sinks, workspace, partition_tokens, stream) -> None:
-    torch = _torch()
-    n_seqs, n_heads, head_dim = q.shape
-    num_blocks, n_kv_heads, block_size, hd2 = k_pool.shape
-    if hd2 != head_dim or v_pool.shape != k_pool.shape or out.shape != q.shape:
+def _attention_args(out, q, k_pool, v_pool, k_scale, v_scale, per_block, block_tables, context_lens, n_seqs):
+    """What the attention calls below check alike: (device, the addresses up to
+    the scales, those of the tables and lengths, the sizes)."""
+    dev = _device(q, "q")
+    T = _Types
+    n, n_heads, head_dim = shape = q.shape
+    num_blocks, n_kv_heads, block_size, hd2 = pool_shape = k_pool.shape
+    if hd2 != head_dim or v_pool.shape != pool_shape or out.shape != shape:
         raise ValueError("shape mismatch between q, out and the pools")
-    if block_tables.dim() != 2 or block_tables.shape[0] != n_seqs or context_lens.numel() != n_seqs:
+    rows, max_blocks = block_tables.shape
+    if rows != n_seqs or context_lens.numel() != n_seqs:
         raise ValueError("block_tables must be [n_seqs][max_blocks], context_lens [n_seqs]")
-    if (k_scale is None) != (v_scale is None):
+    pool_types, ks, vs = T.bf16, None, None
+    if k_scale is not None and v_scale is not None:
+        ns = num_blocks * n_kv_heads if per_block else n_kv_heads
+        if k_scale.numel() != ns or v_scale.numel() != ns:
+            raise ValueError(f"k_scale and v_scale need {ns} entries")
+        ks, vs = _at(k_scale, "k_scale", T.f32, dev), _at(v_scale, "v_scale", T.f32, dev)
+        pool_types = T.e4m3
+    elif per_block:
+        raise ValueError("k_scale and v_scale are needed")
+    elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale go together")
-    dev = _same_device(q=q, out=out, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
-                       block_tables=block_tables, context_lens=context_lens, workspace=workspace)
-    if k_scale is None:
-        kp, vp_, ks, vs = _ptr(k_pool, "k_pool", bf16=True), _ptr(v_pool, "v_pool", bf16=True), None, None
-    else:
-        if k_scale.numel() != scale_numel or v_scale.numel() != scale_numel:
-            raise ValueError(f"k_scale and v_scale need {scale_numel} entries")
-        kp, vp_ = _fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool")
-        ks = _ptr(k_scale, "k_scale", dtype=torch.float32)
-        vs = _ptr(v_scale, "v_scale", dtype=torch.float32)
-    ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace, "workspace"),
-                                                        workspace.numel() * workspace.element_size())
-    _call(fn, dev, stream, _ptr(out, "out", bf16=True), _ptr(q, "q", bf16=True), kp, vp_, ks, vs,
-          _ptr(block_tables, "block_tables", dtype=torch.int32), _ptr(context_lens, "context_lens", dtype=torch.int32),
-          scale, n_heads, n_kv_heads, head_dim, block_size, n_seqs, block_tables.shape[1], max_context_len, num_blocks,
-          window, n_sinks, partition_tokens, ws, ws_bytes)
+    data = (_at(out, "out", T.bf16, dev), _at(q, "q", T.bf16, dev), _at(k_pool, "k_pool", pool_types, dev),
+            _at(v_pool, "v_pool", pool_types, dev), ks, vs)
+    tables = (_at(block_tables, "block_tables", T.i32, dev), _at(context_lens, "context_lens", T.i32, dev))
+    return dev, data, tables, (n_heads, n_kv_heads, head_dim, block_size, n_seqs, max_blocks), num_blocks
+
+
+def _decode_call(fn: str, per_block: bool, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                 max_context_len, window, n_sinks, workspace, partition_tokens, stream) -> None:
+    dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale, per_block,
+                                                           block_tables, context_lens, q.shape[0])
+    _call(fn, dev, stream, *data, *tables, scale, *sizes, max_context_len, num_blocks, window, n_sinks,
+          partition_tokens, *_workspace(workspace, dev))
 
 
 def pa_decode_sinks(out, q, k_pool, v_pool, block_tables, context_lens, scale: float, max_context_len: int,
@@ -312,8 +320,8 @@ def pa_decode_sinks(out, q, k_pool, v_pool, block_tables, context_lens, scale: f
     """Sliding-window decode whose first n_sinks positions stay visible: the
     query at i = ctx-1 attends to t <= i with t >= i-window or t < n_sinks.
     bf16 pools, or uint8 pools with k_scale and v_scale fp32 [n_kv_heads]."""
-    _decode_call("pa_decode_sinks", out, q, k_pool, v_pool, k_scale, v_scale, k_pool.shape[1], block_tables,
-                 context_lens, scale, max_context_len, window, n_sinks, workspace, partition_tokens, stream)
+    _decode_call("pa_decode_sinks", False, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                 max_context_len, window, n_sinks, workspace, partition_tokens, stream)
 
 
 def pa_decode_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale: float,
@@ -322,10 +330,8 @@ def pa_decode_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, 
     """Decode over an E4M3 cache with a scale per block and head (k_scale,
     v_scale fp32 [num_blocks][n_kv_heads], see pa_rope_and_cache_fp8_block);
     window >= 0: as pa_decode_sinks."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale are needed")
-    _decode_call("pa_decode_fp8_block", out, q, k_pool, v_pool, k_scale, v_scale, k_pool.shape[0] * k_pool.shape[1],
-                 block_tables, context_lens, scale, max_context_len, window, n_sinks, workspace, partition_tokens, stream)
+    _decode_call("pa_decode_fp8_block", True, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                 max_context_len, window, n_sinks, workspace, partition_tokens, stream)
 
 
 def pa_decode_plan(context_lens, n_heads: int, n_kv_heads: int, head_dim: int, max_blocks_per_seq: int,
@@ -385,96 +391,122 @@ def pa_decode_planned(out, q, k_pool, v_pool, block_tables, context_lens, scale:
     check("pa_decode_planned", st)
 
 
-def _same_device(**tensors) -> int:
-    """The tensors' one CUDA device; None entries are left out."""
-    index = None
-    for what, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{what} must be a CUDA tensor (the library has no CPU path)")
-        if index is None:
-            index = t.get_device()
-        elif t.get_device() != index:
-            raise ValueError("the tensors are on different devices")
-    return index
+class _Types:
+    """dtypes an argument may have, and the per-device stream lookup; filled on
+    first use, as torch is imported lazily."""
+    ready = False
+
+    @classmethod
+    def fill(cls):
+        torch = _torch()
+        cls.bf16 = (torch.bfloat16, torch.int16, getattr(torch, "uint16", torch.int16))
+        cls.e4m3 = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+        cls.f32, cls.i32, cls.i64 = (torch.float32,), (torch.int32,), (torch.int64,)
+        cls.current_device = torch.cuda.current_device
+        # torch.cuda.current_stream() takes 3 us to build its object; a small launch takes 2
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        cls.raw_stream = staticmethod(raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        cls.ready = True
 
 
-def _call(fn: str, device: int, stream, *args) -> None:
-    """Calls the C entry point with `device` current, on `stream` or that
+def _device(t, what: str) -> int:
+    """The CUDA device index of the call's first tensor."""
+    if not _Types.ready:
+        _Types.fill()
+    dev = t.get_device() if isinstance(t, _torch().Tensor) else -1
+    if dev < 0:
+        _refuse(t, what, None, 0)
+    return dev
+
+
+def _at(t, what: str, dtypes, dev: int, strided: bool = False) -> int:
+    """The address of an argument on device `dev`, contiguous (or not, if
+    strided), of one of `dtypes` (None: any)."""
+    try:
+        if t.get_device() == dev and (dtypes is None or t.dtype in dtypes) and (strided or t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, what, dtypes, dev)
+
+
+def _refuse(t, what: str, dtypes, dev: int):
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (the library has no CPU path)")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the other tensors on cuda:{dev}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dict.fromkeys(dtypes))}, got {t.dtype}")
+    raise ValueError(f"{what} must be contiguous")
+
+
+def _call(fn: str, dev: int, stream, *args) -> None:
+    """Calls the C entry point with device `dev` current, on `stream` or that
     device's current stream."""
-    torch = _torch()
-    if device != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(fn, device, stream, *args)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    check(fn, getattr(load(), fn)(*args, s.cuda_stream))
+    if dev != _Types.current_device():
+        with _torch().cuda.device(dev):
+            return _call(fn, dev, stream, *args)
+    st = getattr(_capi._lib or load(), fn)(*args, _Types.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        check(fn, st)
 
 
-def _token_stride(t, what: str) -> int:
-    """Elements between the tokens of [n_tokens][heads][head_dim], whose heads
-    must be contiguous (a view of a packed projection will do)."""
-    n, heads, dim = t.shape
-    st = t.stride()
-    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+def _workspace(t, dev: int):
+    return (None, 0) if t is None else (_at(t, "workspace", None, dev), t.numel() * t.element_size())
+
+
+def _token_stride(t, what: str, n: int, heads: int, dim: int) -> int:
+    """Elements between the tokens of [n][heads][dim], whose heads must be
+    contiguous (a view of a packed projection will do)."""
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != dim and heads > 1):
         raise ValueError(f"{what} must have contiguous heads")
-    return st[0] if n > 1 else heads * dim
+    return s0 if n > 1 else heads * dim
 
 
-def _bf16(t, what: str) -> int:
-    """The address of a bf16 (or 16-bit integer) tensor, whatever its strides."""
-    torch = _torch()
-    if t.dtype not in (torch.bfloat16, torch.int16, getattr(torch, "uint16", torch.int16)):
-        raise TypeError(f"{what} must hold bf16 (bfloat16 or 16-bit integer bits), got {t.dtype}")
-    return t.data_ptr()
-
-
-def _rope(fn: str, q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, scale_numel, cos_sin, positions, slot_mapping,
+def _rope(fn: str, per_block: bool, q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, cos_sin, positions, slot_mapping,
           interleaved, stream) -> None:
-    torch = _torch()
-    n_tokens, n_kv_heads, head_dim = k.shape
-    num_blocks, hk2, block_size, hd2 = k_pool.shape
-    if (hk2, hd2) != (n_kv_heads, head_dim) or v.shape != k.shape or v_pool.shape != k_pool.shape:
+    dev = _device(k, "k")
+    T = _Types
+    n_tokens, n_kv_heads, head_dim = shape = k.shape
+    num_blocks, hk2, block_size, hd2 = pool_shape = k_pool.shape
+    if hk2 != n_kv_heads or hd2 != head_dim or v.shape != shape or v_pool.shape != pool_shape:
         raise ValueError("shape mismatch between k/v and the pools")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    n_heads = 0
-    if q is not None:
-        if q.dim() != 3 or q.shape[0] != n_tokens or q.shape[2] != head_dim or q_out.shape != q.shape:
+    n_heads = rot = max_position = qo_stride = q_stride = 0
+    q_at = qo_at = cs_at = pos_at = ks_at = vs_at = None
+    if q is not None and q_out is not None:
+        nq, n_heads, dq = q.shape
+        if nq != n_tokens or dq != head_dim or q_out.shape != q.shape:
             raise ValueError("q and q_out must be [n_tokens][n_heads][head_dim]")
-        n_heads = q.shape[1]
+        q_at, qo_at = _at(q, "q", T.bf16, dev, True), _at(q_out, "q_out", T.bf16, dev, True)
+        q_stride = _token_stride(q, "q", n_tokens, n_heads, head_dim)
+        qo_stride = _token_stride(q_out, "q_out", n_tokens, n_heads, head_dim)
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out go together")
     if slot_mapping.numel() != n_tokens:
         raise ValueError("slot_mapping must have n_tokens entries")
-    rot = max_position = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2 or positions is None or positions.numel() != n_tokens:
             raise ValueError("cos_sin must be [max_position][rot_dim], positions [n_tokens]")
         max_position, rot = cos_sin.shape
-    if (k_scale is None) != (v_scale is None):
+        cs_at, pos_at = _at(cos_sin, "cos_sin", T.f32, dev), _at(positions, "positions", T.i64, dev)
+    pool_types = T.bf16
+    if k_scale is not None and v_scale is not None:
+        n = num_blocks * n_kv_heads if per_block else n_kv_heads
+        if k_scale.numel() != n or v_scale.numel() != n:
+            raise ValueError(f"k_scale and v_scale need {n} entries")
+        ks_at, vs_at = _at(k_scale, "k_scale", T.f32, dev), _at(v_scale, "v_scale", T.f32, dev)
+        pool_types = T.e4m3
+    elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale go together")
-    if k_scale is not None and (k_scale.numel() != scale_numel or v_scale.numel() != scale_numel):
-        raise ValueError(f"k_scale and v_scale need {scale_numel} entries")
-    dev = _same_device(k=k, v=v, q=q, q_out=q_out, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
-                       cos_sin=cos_sin, positions=positions, slot_mapping=slot_mapping)
-    if k_scale is None:
-        kp, vp_ = _ptr(k_pool, "k_pool", bf16=True), _ptr(v_pool, "v_pool", bf16=True)
-    else:
-        kp, vp_ = _fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool")
-    _call(fn, dev, stream, None if q is None else _bf16(q_out, "q_out"), None if q is None else _bf16(q, "q"),
-          _bf16(k, "k"), _bf16(v, "v"), kp, vp_,
-          *_rope_tail(fn, torch, k_scale, v_scale, cos_sin, positions if rot else None, slot_mapping),
-          _token_stride(q_out, "q_out") if n_heads else 0, _token_stride(q, "q") if n_heads else 0,
-          _token_stride(k, "k"), _token_stride(v, "v"), n_tokens, n_heads, n_kv_heads, head_dim, rot, max_position,
-          1 if interleaved else 0, block_size, num_blocks)
-
-
-def _rope_tail(fn, torch, k_scale, v_scale, cos_sin, positions, slot_mapping):
-    scales = [None if t is None else _ptr(t, what, dtype=torch.float32)
-              for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
-    rest = [None if cos_sin is None else _ptr(cos_sin, "cos_sin", dtype=torch.float32),
-            None if positions is None else _ptr(positions, "positions", dtype=torch.int64),
-            _ptr(slot_mapping, "slot_mapping", dtype=torch.int64)]
-    return scales + rest if fn.endswith("_block") else rest + scales
+    rest = (cs_at, pos_at, _at(slot_mapping, "slot_mapping", T.i64, dev))
+    _call(fn, dev, stream, qo_at, q_at, _at(k, "k", T.bf16, dev, True), _at(v, "v", T.bf16, dev, True),
+          _at(k_pool, "k_pool", pool_types, dev), _at(v_pool, "v_pool", pool_types, dev),
+          *((ks_at, vs_at) + rest if per_block else rest + (ks_at, vs_at)), qo_stride, q_stride,
+          _token_stride(k, "k", n_tokens, n_kv_heads, head_dim), _token_stride(v, "v", n_tokens, n_kv_heads, head_dim),
+          n_tokens, n_heads, n_kv_heads, head_dim, rot, max_position, 1 if interleaved else 0, block_size, num_blocks)
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, cos_sin, positions, slot_mapping, interleaved: bool = False,
@@ -485,8 +517,8 @@ def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, cos_sin, positions, slot_m
     cos_sin fp32 [max_position][rot_dim] (cosines, then sines), positions int64;
     cos_sin None: no rotation; q and q_out None: only k and v. bf16 pools, or
     uint8 pools with k_scale and v_scale fp32 [n_kv_heads]."""
-    _rope("pa_rope_and_cache", q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, k.shape[1], cos_sin, positions,
-          slot_mapping, interleaved, stream)
+    _rope("pa_rope_and_cache", False, q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, cos_sin, positions, slot_mapping,
+          interleaved, stream)
 
 
 def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, cos_sin, positions, slot_mapping,
@@ -496,8 +528,8 @@ def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_pool, v_pool, k_scale, v_scale
     A call's tokens of one block must be next to each other, in slot order."""
     if k_scale is None or v_scale is None:
         raise ValueError("k_scale and v_scale are needed")
-    _rope("pa_rope_and_cache_fp8_block", q_out, q, k, v, k_pool, v_pool, k_scale, v_scale,
-          k_pool.shape[0] * k_pool.shape[1], cos_sin, positions, slot_mapping, interleaved, stream)
+    _rope("pa_rope_and_cache_fp8_block", True, q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, cos_sin, positions,
+          slot_mapping, interleaved, stream)
 
 
 def pa_copy_blocks(k_pool, v_pool, block_mapping, stream=None) -> None:
@@ -574,32 +606,15 @@ def pa_prefill_paged_ex(out, q, k_pool, v_pool, block_tables, context_lens, q_st
     check("pa_prefill_paged_ex", st)
 
 
-def _prefill_call(fn: str, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, q_start_loc, scale,
-                  max_chunk_len, window, n_sinks, splits, workspace, stream) -> None:
-    torch = _torch()
-    n_rows, n_heads, head_dim = q.shape
-    num_blocks, n_kv_heads, block_size, hd2 = k_pool.shape
+def _prefill_call(fn: str, per_block: bool, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                  q_start_loc, scale, max_chunk_len, window, n_sinks, splits, workspace, stream) -> None:
     n_seqs = context_lens.numel()
-    if hd2 != head_dim or v_pool.shape != k_pool.shape or out.shape != q.shape:
-        raise ValueError("shape mismatch between q, out and the pools")
-    if block_tables.dim() != 2 or block_tables.shape[0] != n_seqs or q_start_loc.numel() != n_seqs + 1:
-        raise ValueError("block_tables must be [n_seqs][max_blocks], q_start_loc [n_seqs + 1]")
-    dev = _same_device(q=q, out=out, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
-                       block_tables=block_tables, context_lens=context_lens, q_start_loc=q_start_loc, workspace=workspace)
-    if k_scale is None:
-        pools = [_ptr(k_pool, "k_pool", bf16=True), _ptr(v_pool, "v_pool", bf16=True)]
-    else:
-        n = num_blocks * n_kv_heads
-        if k_scale.numel() != n or v_scale.numel() != n:
-            raise ValueError(f"k_scale and v_scale need {n} entries")
-        pools = [_fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool"),
-                 _ptr(k_scale, "k_scale", dtype=torch.float32), _ptr(v_scale, "v_scale", dtype=torch.float32)]
-    ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace, "workspace"),
-                                                        workspace.numel() * workspace.element_size())
-    _call(fn, dev, stream, _ptr(out, "out", bf16=True), _ptr(q, "q", bf16=True), *pools,
-          _ptr(block_tables, "block_tables", dtype=torch.int32), _ptr(context_lens, "context_lens", dtype=torch.int32),
-          _ptr(q_start_loc, "q_start_loc", dtype=torch.int32), scale, n_heads, n_kv_heads, head_dim, block_size, n_seqs,
-          block_tables.shape[1], max_chunk_len, num_blocks, window, n_sinks, splits, ws, ws_bytes)
+    if q_start_loc.numel() != n_seqs + 1:
+        raise ValueError("q_start_loc must have n_seqs + 1 entries")
+    dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale, per_block,
+                                                           block_tables, context_lens, n_seqs)
+    _call(fn, dev, stream, *(data if per_block else data[:4]), *tables, _at(q_start_loc, "q_start_loc", _Types.i32, dev),
+          scale, *sizes, max_chunk_len, num_blocks, window, n_sinks, splits, *_workspace(workspace, dev))
 
 
 def pa_prefill_sinks(out, q, k_pool, v_pool, block_tables, context_lens, q_start_loc, scale: float, max_chunk_len: int,
@@ -607,8 +622,8 @@ def pa_prefill_sinks(out, q, k_pool, v_pool, block_tables, context_lens, q_start
     """pa_prefill_paged_ex under a sliding window whose first n_sinks positions
     stay visible: a row at position p attends to t <= p with t >= p-window or
     t < n_sinks. Workspace: prefill_workspace."""
-    _prefill_call("pa_prefill_sinks", out, q, k_pool, v_pool, None, None, block_tables, context_lens, q_start_loc, scale,
-                  max_chunk_len, window, n_sinks, splits, workspace, stream)
+    _prefill_call("pa_prefill_sinks", False, out, q, k_pool, v_pool, None, None, block_tables, context_lens, q_start_loc,
+                  scale, max_chunk_len, window, n_sinks, splits, workspace, stream)
 
 
 def pa_prefill_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, q_start_loc, scale: float,
@@ -616,24 +631,22 @@ def pa_prefill_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
                          stream=None) -> None:
     """pa_prefill_paged_ex (or, with window >= 0, pa_prefill_sinks) over an E4M3
     cache with a scale per block and head."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale are needed")
-    _prefill_call("pa_prefill_fp8_block", out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+    _prefill_call("pa_prefill_fp8_block", True, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
                   q_start_loc, scale, max_chunk_len, window, n_sinks, splits, workspace, stream)
 
 
 def pa_copy_blocks_fp8_block(k_pool, v_pool, k_scale, v_scale, block_mapping, stream=None) -> None:
     """pa_copy_blocks of an E4M3 cache with a scale per block and head: the
     blocks' rows of k_scale and v_scale [num_blocks][n_kv_heads] are copied too."""
-    torch = _torch()
+    dev = _device(k_pool, "k_pool")
+    T = _Types
     num_blocks, n_kv_heads, block_size, head_dim = k_pool.shape
     if v_pool.shape != k_pool.shape or k_scale.numel() != num_blocks * n_kv_heads or v_scale.numel() != k_scale.numel():
         raise ValueError("k_pool and v_pool must have one shape, the scales num_blocks * n_kv_heads entries")
     n_pairs = block_mapping.shape[0] if block_mapping.numel() else 0
-    dev = _same_device(k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, block_mapping=block_mapping)
-    _call("pa_copy_blocks_fp8_block", dev, stream, _fp8_pool(k_pool, "k_pool"), _fp8_pool(v_pool, "v_pool"),
-          _ptr(k_scale, "k_scale", dtype=torch.float32), _ptr(v_scale, "v_scale", dtype=torch.float32),
-          _ptr(block_mapping, "block_mapping", dtype=torch.int64) if n_pairs else None, n_pairs, n_kv_heads, head_dim,
+    _call("pa_copy_blocks_fp8_block", dev, stream, _at(k_pool, "k_pool", T.e4m3, dev), _at(v_pool, "v_pool", T.e4m3, dev),
+          _at(k_scale, "k_scale", T.f32, dev), _at(v_scale, "v_scale", T.f32, dev),
+          _at(block_mapping, "block_mapping", T.i64, dev) if n_pairs else None, n_pairs, n_kv_heads, head_dim,
           block_size, num_blocks)
 
 
