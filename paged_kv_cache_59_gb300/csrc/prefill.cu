@@ -80,8 +80,8 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
     CUtensorMap tk, tv;
     const bool maps = eb == 2 ? pa_make_tmap_2d_bf16(&tk, k_pool, head_dim, (uint64_t)rows, head_dim * 2, 64, kBS) &&
                                     pa_make_tmap_2d_bf16(&tv, v_pool, head_dim, (uint64_t)rows, head_dim * 2, 64, kBS)
-                              : pa_make_tmap_2d_u8(&tk, k_pool, head_dim, (uint64_t)rows, head_dim, head_dim, kBS, false) &&
-                                    pa_make_tmap_2d_u8(&tv, v_pool, head_dim, (uint64_t)rows, head_dim, head_dim, kBS, false);
+                              : pa_make_tmap_2d_u8(&tk, k_pool, head_dim, (uint64_t)rows, head_dim, head_dim, kBS, head_dim == 128) &&
+                                    pa_make_tmap_2d_u8(&tv, v_pool, head_dim, (uint64_t)rows, head_dim, head_dim, kBS, head_dim == 128);
     if (!maps) return PA_ERR_CUDA;
     PrefillParams Pp;
     Pp.out = static_cast<uint16_t*>(out);

@@ -173,11 +173,14 @@ struct KeyTiles {
 // A block-scaled cache's scale, within the range the library works with.
 __device__ __forceinline__ float clamp_scale(float s) { return fminf(fmaxf(s, 0x1p-32f), 0x1p32f); }
 
-// Two E4M3 codes -> two fp16 values (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two_codes));
-    return r;
+// Four E4M3 codes -> four fp16 values (exact), two a register.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& a, uint32_t& b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(codes));
 }
 
 // A piece's partial for one row: the un-normalised O (head_dim floats from
@@ -269,14 +272,38 @@ pa_prefill_tc_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap 
     // the grid position. Balanced mode: the work-list entries this CTA takes
     // from the counter, one at a time.
     int* next = reinterpret_cast<int*>(sm + kMisc + 8);  // [2] the entry taken, by segment parity
+    int entry_at = 0, entry_end = 0;                     // even mode
+    int4 entry_next = make_int4(0, 0, 0, 0);
     bool have_tmem = false;
     uint32_t tbase = 0;
+    if constexpr (WIN) {
+        pa::launch_dependents();     // the merge may be scheduled
+        pa::grid_dependency_wait();  // the plan, and whatever wrote the cache, is complete
+    }
     int n_run = 0;  // segments run so far
     for (int seg = 0;; ++seg) {
         int s, kvh, qp, kt0 = 0, kt1 = 0;
         bool direct = true;
         float* part_base = nullptr;
-        if (P.work) {
+        if (WIN && P.work) {
+            // even mode: this CTA's run of entries; the next one is loaded ahead
+            if (seg == 0) {
+                const int4 c = P.work[P.n_items + P.n_cta + blockIdx.x];
+                entry_at = c.x;
+                entry_end = c.y;
+                if (entry_at < entry_end) entry_next = P.work[entry_at];
+            }
+            if (entry_at >= entry_end) break;
+            const int4 e = entry_next;
+            if (++entry_at < entry_end) entry_next = P.work[entry_at];
+            kt0 = e.y;
+            kt1 = e.z;
+            direct = e.w < 0;
+            if (!direct) part_base = P.part + (size_t)e.w * 2 * 128 * kPartStride;
+            s = e.x / (Hk * P.n_qp);
+            kvh = (e.x / P.n_qp) % Hk;
+            qp = e.x % P.n_qp;
+        } else if (P.work) {
             if (threadIdx.x == 0) next[seg & 1] = atomicAdd(&P.sched[0], 1);
             __syncthreads();
             const int w = next[seg & 1];
@@ -599,30 +626,50 @@ pa_prefill_tc_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap 
                     if (lane == 0) pa::mbar_arrive(&v_conv[j % kVS]);
                 }
             } else {
-                // E4M3: 16 codes (one row's 16-byte chunk) become two 16-byte fp16 chunks of the
-                // stage. Consecutive threads read consecutive chunks; those of a row's second
-                // 64-dim half write their odd chunk first, so that eight threads always write
-                // eight different bank groups.
+                // E4M3: 16 codes (one 16-byte chunk of a row) become two 16-byte fp16 chunks of
+                // the stage. Eight threads that access shared memory together should touch
+                // eight different bank groups in the read and in both writes, whose chunks
+                // are 2 c and 2 c + 1 of a row (XOR the row, modulo 8). D = 64: two rows of
+                // four chunks, read in a run; the rows differ in parity, so their chunks do.
+                // D = 128: chunks c .. c + 3 (of one 64-dim half) of rows r and r ^ 5; TMA
+                // stored the codes with the same XOR, so the reads differ in bit 2, and the
+                // writes in bit 0.
+                int row0, c16;
+                if constexpr (D == 64) {
+                    row0 = t >> 2;
+                    c16 = t & 3;
+                } else {
+                    const int u = t >> 4;  // 0..7: rows {0, 5}, {1, 4}, {2, 7}, {3, 6} and the same plus 8
+                    c16 = (t & 3) + ((t >> 1) & 4);
+                    row0 = (u & 4) * 2 + ((t & 4) ? (u & 3) ^ 5 : (u & 3));
+                }
+                constexpr int kStep = D == 64 ? 32 : 16;  // rows per pass
+                const uint32_t src0 = row0 * D + (D == 64 ? c16 * 16 : ((c16 ^ (row0 & 7)) << 4));
+                const uint32_t half = (c16 >> 2) * 16384, ch = 2 * (c16 & 3);
+                const uint32_t dst0 = half + tc::sw128_offset(row0, ch), dst1 = half + tc::sw128_offset(row0, ch + 1);
                 auto widen = [&](int x, unsigned char* dst, int kb) {
-                    const uint4* raw = reinterpret_cast<const uint4*>(sm + L_::kRaw + x * L_::kRawTile);
+                    const unsigned char* raw = sm + L_::kRaw + x * L_::kRawTile + src0;
                     const int valid = ctx - kb;
-                    const bool partial = x == 1 && (valid < kKT || (WIN && kb < keys.lo && kb + kKT > P.n_sinks));
+                    auto pass = [&](auto partial) {
 #pragma unroll 4
-                    for (int c = 0; c < (int)(L_::kRawTile / 2048); ++c) {
-                        const int e = t + 128 * c, row = e / (D / 16), c16 = e % (D / 16);
-                        uint4 w = raw[e];
-                        // V rows that no query of the pair sees are zero (p = 0 must not meet a NaN)
-                        if (partial && (row >= valid || (WIN && !keys.seen(P, kb + row, kb + row + 1))))
-                            w = make_uint4(0, 0, 0, 0);
-                        const uint4 lo = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16),
-                                                    e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
-                        const uint4 hi = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16),
-                                                    e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
-                        const int g = c16 >> 2, ch = 2 * (c16 & 3);
-                        unsigned char* half = dst + g * 16384;
-                        *reinterpret_cast<uint4*>(half + tc::sw128_offset(row, ch + g)) = g ? hi : lo;
-                        *reinterpret_cast<uint4*>(half + tc::sw128_offset(row, ch + 1 - g)) = g ? lo : hi;
-                    }
+                        for (int c = 0; c < kKT / kStep; ++c) {
+                            uint4 w = *reinterpret_cast<const uint4*>(raw + c * kStep * D);
+                            // V rows that no query of the pair sees are zero (p = 0 must not meet a NaN)
+                            if constexpr (decltype(partial)::value) {
+                                const int row = row0 + c * kStep;
+                                if (row >= valid || !keys.seen(P, kb + row, kb + row + 1)) w = make_uint4(0, 0, 0, 0);
+                            }
+                            uint4 lo, hi;
+                            e4m3x4_to_f16x4(w.x, lo.x, lo.y);
+                            e4m3x4_to_f16x4(w.y, lo.z, lo.w);
+                            e4m3x4_to_f16x4(w.z, hi.x, hi.y);
+                            e4m3x4_to_f16x4(w.w, hi.z, hi.w);
+                            *reinterpret_cast<uint4*>(dst + dst0 + c * kStep * 128) = lo;
+                            *reinterpret_cast<uint4*>(dst + dst1 + c * kStep * 128) = hi;
+                        }
+                    };
+                    if (x == 1 && (valid < kKT || (kb < keys.lo && kb + kKT > P.n_sinks))) pass(std::true_type{});
+                    else pass(std::false_type{});
                     tc::fence_async_smem();  // generic-proxy writes, read next by the tensor core
                     __syncwarp();
                     if (lane == 0) pa::mbar_arrive(&raw_free[x]);
@@ -691,11 +738,11 @@ pa_prefill_tc_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap 
             }
             for (int j = 0; j < n_kt; ++j) {
                 float my_k = 0.f, my_e = 0.f, my_inv = 0.f;
-                if constexpr (EB == 1) {
+                if constexpr (EB == 1) {  // the approximate log2 and reciprocal are off by 2^-22, far below w's rounding
                     const float vs = clamp_scale(vs_next);
                     my_k = clamp_scale(ks_next) * sc;
-                    my_e = log2f(vs);
-                    my_inv = 1.f / vs;
+                    my_e = __log2f(vs);
+                    my_inv = __fdividef(1.f, vs);
                     ks_next = scale_of(P.k_scale, bid_next);
                     vs_next = scale_of(P.v_scale, bid_next);
                     bid_next = block_id(j + 2);
@@ -986,6 +1033,105 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_kernel(const PrefillPara
     }
 }
 
+// Even mode (windowed and E4M3 instantiations): the work list. The key tiles
+// of all non-empty items, T in item order, are cut into C runs of equal length,
+// C the CTAs (fewer when a run would be shorter than 4 tiles), so that every
+// CTA walks T / C tiles: at most one piece of an item begun by the CTA before,
+// whole items, and one piece of an item that the next CTA goes on with. (A
+// window makes the items equally long and few waves deep: 256 items of 35 tiles
+// on 152 CTAs take 4 segments on the busiest CTA with whole waves and cut
+// tails, 2 or 3 here, and no CTA idles.) When the items are at most the CTAs and
+// none is much longer than the mean (by 8 tiles, about what starting another
+// segment and merging costs), each runs whole.
+// Item r (its rank among the non-empty ones) and CTA c share at most one
+// entry, number r + c. P.work[n_items + n_cta + c] = (first entry, end entry,
+// item cut first between CTA c - 1 and c or -1, its pieces). Piece k of an item
+// that CTA c0 begins: slot 2 c0 + 1 for k = 0, else 2 (c0 + k).
+template <int G>
+__global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const PrefillParams P) {
+    __shared__ long long wsum[32];
+    __shared__ int wcnt[32], wmax[32];
+    pa::launch_dependents();     // the prefill kernel may be scheduled
+    pa::grid_dependency_wait();  // the lengths are written
+    const int n = P.n_items, t = threadIdx.x, lane = t & 31, wid = t >> 5;
+    const int per = (n + 1023) / 1024;
+    const int b0 = (int)min((long long)n, (long long)t * per), b1 = min(n, b0 + per);
+    int4* cta = P.work + n + P.n_cta;
+    for (int c = t; c < P.n_cta; c += 1024) cta[c] = make_int4(0, 0, -1, 0);
+    long long mine = 0;
+    int cnt = 0, most = 0;
+    for (int it = b0; it < b1; ++it) {
+        const int nk = item_tiles<G>(P, it);
+        mine += nk;
+        cnt += nk > 0;
+        most = max(most, nk);
+    }
+    long long incl = mine;  // inclusive sums within the warp
+    int icnt = cnt;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(kFull, incl, o);
+        const int u = __shfl_up_sync(kFull, icnt, o);
+        if (lane >= o) {
+            incl += v;
+            icnt += u;
+        }
+        most = max(most, __shfl_xor_sync(kFull, most, o));
+    }
+    if (lane == 31) {
+        wsum[wid] = incl;
+        wcnt[wid] = icnt;
+        wmax[wid] = most;
+    }
+    __syncthreads();
+    if (wid == 0) {
+        long long v = wsum[lane];
+        int u = wcnt[lane], m = wmax[lane];
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFull, v, o);
+            const int z = __shfl_up_sync(kFull, u, o);
+            if (lane >= o) {
+                v += y;
+                u += z;
+            }
+            m = max(m, __shfl_xor_sync(kFull, m, o));
+        }
+        wsum[lane] = v;  // inclusive over warps
+        wcnt[lane] = u;
+        wmax[lane] = m;
+    }
+    __syncthreads();
+    const long long T = wsum[31];
+    const int np = wcnt[31];
+    const bool whole = np <= P.n_cta && wmax[0] <= T / P.n_cta + 8;
+    const long long C = max(1LL, min((long long)P.n_cta, T / 4));
+    long long off = incl - mine + (wid > 0 ? wsum[wid - 1] : 0);
+    int r = icnt - cnt + (wid > 0 ? wcnt[wid - 1] : 0);
+    for (int it = b0; it < b1; ++it) {
+        const int nk = item_tiles<G>(P, it);
+        if (nk <= 0) continue;
+        if (whole) {
+            P.work[r] = make_int4(it, 0, nk, -1);
+            cta[r] = make_int4(r, r + 1, -1, 0);
+        } else {
+            // run c: tiles [c T / C, (c + 1) T / C); c0, c1: the CTAs of the item's first and last tile
+            const int c0 = (int)(((off + 1) * C - 1) / T), c1 = (int)(((off + nk) * C - 1) / T);
+            for (int c = c0; c <= c1; ++c) {
+                const long long lo = c * T / C, hi = (c + 1) * T / C;
+                const int a = (int)max(0LL, lo - off), b = (int)min((long long)nk, hi - off);
+                P.work[r + c] = make_int4(it, a, b, c0 == c1 ? -1 : c == c0 ? 2 * c + 1 : 2 * c);
+                if (off <= lo) cta[c].x = r + c;
+                if (off + nk >= hi) cta[c].y = r + c + 1;
+                if (c == c0 + 1) {
+                    cta[c].z = it;
+                    cta[c].w = c1 - c0 + 1;
+                }
+            }
+        }
+        off += nk;
+        ++r;
+    }
+}
+
 // Combines the pieces of one output row: O = sum_k O_k 2^(m_k - M),
 // l = sum_k l_k 2^(m_k - M), out = O / l (lane: D / 32 consecutive dims).
 // Piece k covers key tiles piece_range(n_kt_all, k, n_pieces); empty ones
@@ -1016,7 +1162,13 @@ __device__ __forceinline__ void load_slice(const float* src, int lane, float (&v
     }
 }
 template <int D, typename PartOf>
-__device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf part_of, int lane, uint16_t* out_row) {
+__device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf part_of, int lane, uint16_t* out_row,
+                                          bool even = false) {
+    auto range = [even](int n_kt, int k, int n, int& a, int& b) {
+        a = 0;
+        b = 1;  // even mode: no piece is empty
+        if (!even) piece_range(n_kt, k, n, a, b);
+    };
     constexpr int NV = D / 32;  // dims per lane: 4 or 2
     if (n_pieces <= 8) {
         float v[8][NV];
@@ -1024,7 +1176,7 @@ __device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf par
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             int a = 0, b = 0;
-            if (k < n_pieces) piece_range(n_kt_all, k, n_pieces, a, b);
+            if (k < n_pieces) range(n_kt_all, k, n_pieces, a, b);
             ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int e = 0; e < NV; ++e) v[k][e] = 0.f;
@@ -1051,7 +1203,7 @@ __device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf par
     float m_mine = -INFINITY, l_mine = 0.f;
     for (int k = lane; k < n_pieces; k += 32) {
         int a, b;
-        piece_range(n_kt_all, k, n_pieces, a, b);
+        range(n_kt_all, k, n_pieces, a, b);
         if (b > a) {
             const float2 ml = *reinterpret_cast<const float2*>(part_of(k) + kPartML);
             if (ml.x > m_mine) {  // keep the larger reference; rescale the other sum
@@ -1076,7 +1228,7 @@ __device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf par
         for (int u = 0; u < 8; ++u) {
             const int k = k0 + u;
             int a = 0, b = 0;
-            if (k < n_pieces) piece_range(n_kt_all, k, n_pieces, a, b);
+            if (k < n_pieces) range(n_kt_all, k, n_pieces, a, b);
             f[u] = 0.f;
 #pragma unroll
             for (int e = 0; e < NV; ++e) v[u][e] = 0.f;
@@ -1148,6 +1300,29 @@ __global__ void __launch_bounds__(128) pa_prefill_merge_cut_kernel(const Prefill
                  lane, P.out + ((size_t)(q0 + i) * P.n_heads + kvh * G + r % G) * D);
 }
 
+// Even mode: one warp per (row, head) of the cut items, found at the CTA that
+// holds an item's second piece.
+template <int G, int D>
+__global__ void __launch_bounds__(128) pa_prefill_merge_even_kernel(const PrefillParams P) {
+    constexpr int QT = kRows / G;
+    pa::grid_dependency_wait();  // every piece's partial is written
+    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int c = w >> 8, x = (w >> 7) & 1, r = w & 127;
+    const int4 e = P.work[P.n_items + P.n_cta + c];
+    if (e.z < 0) return;
+    const int item = e.z, Hk = P.n_kv_heads;
+    const int s = item / (Hk * P.n_qp), kvh = (item / P.n_qp) % Hk, qp = item % P.n_qp;
+    const int q0 = P.qsl[s], L = P.qsl[s + 1] - q0;
+    const int i = qp * 2 * QT + x * QT + r / G;
+    if (i >= L) return;
+    merge_row<D>(e.w, 0,
+                 [&](int k) {
+                     const size_t slot = k == 0 ? 2 * c - 1 : 2 * (c - 1 + k);
+                     return P.part + ((slot * 2 + x) * 128 + r) * kPartStride;
+                 },
+                 lane, P.out + ((size_t)(q0 + i) * P.n_heads + kvh * G + r % G) * D, true);
+}
+
 template <int G, int D, int EB, bool WIN>
 int launch_prefill(const PrefillParams& Pp, const CUtensorMap& tk, const CUtensorMap& tv, int n_seqs,
                    int max_chunk_len, int n_rows, cudaStream_t stream) {
@@ -1164,6 +1339,13 @@ int launch_prefill(const PrefillParams& Pp, const CUtensorMap& tk, const CUtenso
     }
     constexpr int QT = kRows / G;
     const int n_qp = (max_chunk_len + 2 * QT - 1) / (2 * QT);
+    if (WIN && Pp.work) {  // even mode: plan, one CTA per SM, merge; each launched ahead of the one before's end
+        int st = pa_launch_pdl(pa_prefill_plan_even_kernel<G>, dim3(1), dim3(1024), 0, stream, Pp);
+        if (st == PA_OK) st = pa_launch_pdl(kern, dim3((unsigned)Pp.n_cta), dim3(kThreads), kSmemBytes, stream, Pp, tk, tv);
+        if (st == PA_OK)
+            st = pa_launch_pdl(pa_prefill_merge_even_kernel<G, D>, dim3((unsigned)Pp.n_cta * 64), dim3(128), 0, stream, Pp);
+        return st;
+    }
     if (Pp.work) {  // balanced mode: plan, then one CTA per SM taking work-list entries
         pa_prefill_plan_kernel<G><<<1, 1024, 0, stream>>>(Pp);
         kern<<<Pp.n_cta, kThreads, kSmemBytes, stream>>>(Pp, tk, tv);

@@ -111,18 +111,19 @@ def test_extreme_block_scales(pk):
 
 
 def test_rows_as_wide_windows_equal_full_prefill(pk):
-    """A window past the context is no window: the same bits as pa_prefill_paged_ex."""
+    """A window past the context is no window: the same bits as pa_prefill_paged_ex,
+    unsplit (splits = 0 cuts the key ranges at other places, and where a row's
+    partial sums are joined decides their fp32 roundings)."""
     torch = torch_cuda()
     chunk = [100, 33]
     c = Cache(5, "bf16", [300, 33], 2, 128, chunk=chunk)
     c.window, c.n_sinks, c.scale = 2 ** 31 - 1, 2 ** 31 - 1, 128 ** -0.5
     q = f32_to_bf16_bits(np.random.default_rng(2).standard_normal((133, 8, 128)).astype(np.float32))
-    got = run(pk, c, q, chunk, 0)
+    got = run(pk, c, q, chunk, 1)
     qd = dev(q)
     out = torch.zeros_like(qd)
     t = tensors_of(c, chunk)
-    pk.pa_prefill_paged_ex(out, qd, t[0], t[1], t[4], t[5], t[6], c.scale, 100,
-                           workspace=pk.prefill_workspace(qd, 2, 2, 100))
+    pk.pa_prefill_paged_ex(out, qd, t[0], t[1], t[4], t[5], t[6], c.scale, 100, splits=1)
     assert np.array_equal(got, host_bits(out))
     check_device_error(0)
 
