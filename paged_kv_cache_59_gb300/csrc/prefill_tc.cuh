@@ -1033,20 +1033,25 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_kernel(const PrefillPara
     }
 }
 
-// Even mode (windowed and E4M3 instantiations): the work list. The key tiles
-// of all non-empty items, T in item order, are cut into C runs of equal length,
-// C the CTAs (fewer when a run would be shorter than 4 tiles), so that every
-// CTA walks T / C tiles: at most one piece of an item begun by the CTA before,
-// whole items, and one piece of an item that the next CTA goes on with. (A
-// window makes the items equally long and few waves deep: 256 items of 35 tiles
-// on 152 CTAs take 4 segments on the busiest CTA with whole waves and cut
-// tails, 2 or 3 here, and no CTA idles.) When the items are at most the CTAs and
-// none is much longer than the mean (by 8 tiles, about what starting another
-// segment and merging costs), each runs whole.
+// Even mode (windowed and E4M3 instantiations): the work list. An item costs
+// its key tiles plus kStart, what starting and finishing a segment takes in
+// units of a tile (Q, the pipeline's fill, the epilogue: about 10 us against
+// 1.9). The costs of all non-empty items, in item order, are cut into C runs of
+// equal length, C the CTAs (fewer when a run would be shorter than kStart + 4),
+// so that all CTAs finish together: each has at most one piece of an item begun
+// by the CTA before, whole items, and one piece of an item that the next CTA
+// goes on with. (A window makes the items equally long and few waves deep: 256
+// items of 35 tiles on 152 CTAs take 4 segments on the busiest CTA with whole
+// waves and cut tails, 2 or 3 here, and no CTA idles.) A cut that would leave
+// fewer than kLeast tiles on one side moves to that end of the item. When the
+// items are at most the CTAs and none is much longer than the mean, each runs
+// whole, which saves the merge.
 // Item r (its rank among the non-empty ones) and CTA c share at most one
-// entry, number r + c. P.work[n_items + n_cta + c] = (first entry, end entry,
-// item cut first between CTA c - 1 and c or -1, its pieces). Piece k of an item
-// that CTA c0 begins: slot 2 c0 + 1 for k = 0, else 2 (c0 + k).
+// entry, number r + c; a CTA's entries are consecutive. P.work[n_items + n_cta
+// + c] = (first entry, end entry, item cut first between CTA c - 1 and c or -1,
+// its pieces). Piece k of an item that CTA c0 begins: slot 2 c0 + 1 for k = 0,
+// else 2 (c0 + k).
+constexpr int kStart = 5, kLeast = 3;
 template <int G>
 __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const PrefillParams P) {
     __shared__ long long wsum[32];
@@ -1057,12 +1062,12 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
     const int per = (n + 1023) / 1024;
     const int b0 = (int)min((long long)n, (long long)t * per), b1 = min(n, b0 + per);
     int4* cta = P.work + n + P.n_cta;
-    for (int c = t; c < P.n_cta; c += 1024) cta[c] = make_int4(0, 0, -1, 0);
+    for (int c = t; c < P.n_cta; c += 1024) cta[c] = make_int4(0x7fffffff, 0, -1, 0);
     long long mine = 0;
     int cnt = 0, most = 0;
     for (int it = b0; it < b1; ++it) {
         const int nk = item_tiles<G>(P, it);
-        mine += nk;
+        mine += nk > 0 ? nk + kStart : 0;
         cnt += nk > 0;
         most = max(most, nk);
     }
@@ -1102,8 +1107,8 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
     __syncthreads();
     const long long T = wsum[31];
     const int np = wcnt[31];
-    const bool whole = np <= P.n_cta && wmax[0] <= T / P.n_cta + 8;
-    const long long C = max(1LL, min((long long)P.n_cta, T / 4));
+    const bool whole = np <= P.n_cta && wmax[0] <= T / P.n_cta + 2 * kStart;
+    const long long C = max(1LL, min((long long)P.n_cta, T / (kStart + 4)));
     long long off = incl - mine + (wid > 0 ? wsum[wid - 1] : 0);
     int r = icnt - cnt + (wid > 0 ? wcnt[wid - 1] : 0);
     for (int it = b0; it < b1; ++it) {
@@ -1113,21 +1118,28 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
             P.work[r] = make_int4(it, 0, nk, -1);
             cta[r] = make_int4(r, r + 1, -1, 0);
         } else {
-            // run c: tiles [c T / C, (c + 1) T / C); c0, c1: the CTAs of the item's first and last tile
-            const int c0 = (int)(((off + 1) * C - 1) / T), c1 = (int)(((off + nk) * C - 1) / T);
-            for (int c = c0; c <= c1; ++c) {
-                const long long lo = c * T / C, hi = (c + 1) * T / C;
-                const int a = (int)max(0LL, lo - off), b = (int)min((long long)nk, hi - off);
-                P.work[r + c] = make_int4(it, a, b, c0 == c1 ? -1 : c == c0 ? 2 * c + 1 : 2 * c);
-                if (off <= lo) cta[c].x = r + c;
-                if (off + nk >= hi) cta[c].y = r + c + 1;
-                if (c == c0 + 1) {
-                    cta[c].z = it;
-                    cta[c].w = c1 - c0 + 1;
-                }
+            // run c: costs [c T / C, (c + 1) T / C); the item's costs are [off, off + nk + kStart)
+            const int c0 = (int)(((off + 1) * C - 1) / T), c1 = (int)(((off + nk + kStart) * C - 1) / T);
+            auto cut = [&](int c) {  // the item's tile at which run c begins
+                if (c <= c0) return 0;
+                if (c > c1) return nk;
+                const int x = (int)(c * T / C - off) - kStart;
+                return x < kLeast ? 0 : x > nk - kLeast ? nk : x;
+            };
+            int ca = c0, cb = c1;  // the CTAs that get tiles
+            while (cut(ca + 1) == 0) ++ca;
+            while (cut(cb) == nk) --cb;
+            for (int c = ca; c <= cb; ++c) {
+                P.work[r + c] = make_int4(it, cut(c), cut(c + 1), ca == cb ? -1 : c == ca ? 2 * c + 1 : 2 * c);
+                atomicMin(&cta[c].x, r + c);
+                atomicMax(&cta[c].y, r + c + 1);
+            }
+            if (cb > ca) {
+                cta[ca + 1].z = it;
+                cta[ca + 1].w = cb - ca + 1;
             }
         }
-        off += nk;
+        off += nk + kStart;
         ++r;
     }
 }
