@@ -232,6 +232,95 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, unsigne
     }
 }
 
+// Even mode: a warp's 32 rows (thread = row) of a cut item. There is no merge
+// launch: whichever piece of these rows comes last joins all of them, so no
+// CTA ever waits for another. A piece that finds the others' partials complete
+// keeps its own in tensor memory and joins; any other writes its partial, and
+// joins if the rest became complete meanwhile. The sum over pieces runs in
+// their order, whoever makes it, so the result does not depend on timing.
+// (About 40 MB of partials less to read than with a merge kernel, and a launch
+// less: the piece a CTA passes on is its last, the rest its successor's first,
+// so it nearly always is the last one and never writes.)
+// Partial of a slot's tile x: float4 [D / 4][128 rows] of O, then float2 [128]
+// of (m, l). `own(c, v)` gives columns 32 c .. 32 c + 31 of this row's O (warp-
+// collective); `put(c, v)` takes the joined ones, normalised.
+__device__ __forceinline__ float* slot_part(const PrefillParams& P, int slot, int x) {
+    return P.part + ((size_t)slot * 2 + x) * 128 * kPartStride;
+}
+template <int D, typename Own, typename Put>
+__device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, int x, int r, int warp, int lane, float m,
+                                            float l, Own own, Put put) {
+    const int4* cta = P.work + P.n_items + P.n_cta;
+    const int c = slot >> 1;
+    const int4 info = cta[slot & 1 ? c + 1 : c];
+    const int ca = info.z, n = info.w, me = c - ca;
+    int* count = const_cast<int*>(reinterpret_cast<const int*>(cta + P.n_cta)) + (ca + 1) * 8 + warp;
+    auto counted = [&]() {  // every lane acquires: it reads other CTAs' partials itself
+        int v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+        return v;
+    };
+    bool last = __all_sync(kFull, counted() == n - 1);
+    if (!last) {
+        float* dst = slot_part(P, slot, x);
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+            float v[32];
+            own(q, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                reinterpret_cast<float4*>(dst)[(8 * q + k) * 128 + r] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+        reinterpret_cast<float2*>(dst + 128 * D)[r] = make_float2(m, l);
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(count, 1);
+        last = __shfl_sync(kFull, before, 0) == n - 1;
+        if (last) last = __all_sync(kFull, counted() == n);  // (always: all have been counted)
+    }
+    if (!last) return;
+    auto ml = [&](int k) {
+        return k == me ? make_float2(m, l)
+                       : __ldcg(reinterpret_cast<const float2*>(slot_part(P, k == 0 ? 2 * ca + 1 : 2 * (ca + k), x) + 128 * D) + r);
+    };
+    float M = -INFINITY, sum = 0.f;
+    for (int k = 0; k < n; ++k) M = fmaxf(M, ml(k).x);
+    auto factor = [&](float mk) { return mk == -INFINITY ? 0.f : pa::fast_exp2(mk - M); };
+    for (int k = 0; k < n; ++k) {
+        const float2 p = ml(k);
+        sum += p.y * factor(p.x);
+    }
+    const float inv = 1.f / sum;
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+        float acc[32] = {};
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            const float f = factor(ml(k).x);
+            float v[32];
+            if (k == me) {  // warp-uniform
+                own(q, v);
+            } else {
+                const float4* src = reinterpret_cast<const float4*>(slot_part(P, k == 0 ? 2 * ca + 1 : 2 * (ca + k), x));
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float4 w = __ldcg(src + (8 * q + u) * 128 + r);
+                    v[4 * u] = w.x;
+                    v[4 * u + 1] = w.y;
+                    v[4 * u + 2] = w.z;
+                    v[4 * u + 3] = w.w;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 32; ++u) acc[u] += v[u] * f;
+        }
+#pragma unroll
+        for (int u = 0; u < 32; ++u) acc[u] *= inv;
+        put(q, acc);
+    }
+}
+
 // WIN: rows may have a lower bound (a window with sinks). EB = 1: an E4M3 cache
 // with a scale per (block, KV head).
 template <int G, int D, int EB, bool WIN>
@@ -277,13 +366,14 @@ pa_prefill_tc_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap 
     bool have_tmem = false;
     uint32_t tbase = 0;
     if constexpr (WIN) {
-        pa::launch_dependents();     // the merge may be scheduled
+        pa::launch_dependents();     // the next kernel may be scheduled
         pa::grid_dependency_wait();  // the plan, and whatever wrote the cache, is complete
     }
     int n_run = 0;  // segments run so far
     for (int seg = 0;; ++seg) {
         int s, kvh, qp, kt0 = 0, kt1 = 0;
         bool direct = true;
+        int slot = -1;  // even mode: this piece's slot, or a whole item
         float* part_base = nullptr;
         if (WIN && P.work) {
             // even mode: this CTA's run of entries; the next one is loaded ahead
@@ -298,8 +388,7 @@ pa_prefill_tc_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap 
             if (++entry_at < entry_end) entry_next = P.work[entry_at];
             kt0 = e.y;
             kt1 = e.z;
-            direct = e.w < 0;
-            if (!direct) part_base = P.part + (size_t)e.w * 2 * 128 * kPartStride;
+            slot = e.w;
             s = e.x / (Hk * P.n_qp);
             kvh = (e.x / P.n_qp) % Hk;
             qp = e.x % P.n_qp;
@@ -883,7 +972,31 @@ pa_prefill_tc_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap 
             tc::tmem_wait_st();  // no store may be pending when the columns are released
             if (ok) ok = wait_bar(&pv_done[x], (uint32_t)((n_kt - 1) & 1), P.err, abort_flag);
             ok = __all_sync(kFull, ok);
-            if (ok && !direct) {
+            if (WIN && ok && slot >= 0) {
+                tc::fence_after_sync();
+                bool finite = true;
+                uint4* dst = reinterpret_cast<uint4*>(P.out + ((size_t)(q0 + i) * H + h0 + r % G) * D);
+                join_pieces<D>(
+                    P, slot, x, r, warp, lane, m_used, l,
+                    [&](int c, float (&v)[32]) {
+                        uint32_t raw[32];
+                        tc::tmem_ld32(tO + c * 32, raw);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]) * (EB == 2 ? 256.f : 1.f);  // undo V's 2^-8
+                    },
+                    [&](int c, const float (&v)[32]) {
+                        if (i >= L) return;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) finite &= fabsf(v[k]) < INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+                            dst[(c * 32 + k) / 8] =
+                                make_uint4(pa::float2_to_bf16x2(v[k], v[k + 1]), pa::float2_to_bf16x2(v[k + 2], v[k + 3]),
+                                           pa::float2_to_bf16x2(v[k + 4], v[k + 5]), pa::float2_to_bf16x2(v[k + 6], v[k + 7]));
+                    });
+                if (!finite) pa::set_error(P.err, PA_DEVERR_RANGE);
+            } else if (ok && !direct) {
                 // a piece: keep O, m and l for the merge
                 tc::fence_after_sync();
                 float* dst = part_base + ((size_t)x * 128 + r) * kPartStride;
@@ -1045,12 +1158,13 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_kernel(const PrefillPara
 // waves and cut tails, 2 or 3 here, and no CTA idles.) A cut that would leave
 // fewer than kLeast tiles on one side moves to that end of the item. When the
 // items are at most the CTAs and none is much longer than the mean, each runs
-// whole, which saves the merge.
+// whole, which saves joining pieces.
 // Item r (its rank among the non-empty ones) and CTA c share at most one
 // entry, number r + c; a CTA's entries are consecutive. P.work[n_items + n_cta
-// + c] = (first entry, end entry, item cut first between CTA c - 1 and c or -1,
-// its pieces). Piece k of an item that CTA c0 begins: slot 2 c0 + 1 for k = 0,
-// else 2 (c0 + k).
+// + c] = (first entry, end entry, the CTA ca that begins the item cut between
+// CTA c - 1 and c, its pieces or 0). Piece k of that item: slot 2 ca + 1 for
+// k = 0, else 2 (ca + k). Behind that table, 8 counters for each CTA (see
+// join_pieces), zeroed here.
 constexpr int kStart = 5, kLeast = 3;
 template <int G>
 __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const PrefillParams P) {
@@ -1062,7 +1176,10 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
     const int per = (n + 1023) / 1024;
     const int b0 = (int)min((long long)n, (long long)t * per), b1 = min(n, b0 + per);
     int4* cta = P.work + n + P.n_cta;
-    for (int c = t; c < P.n_cta; c += 1024) cta[c] = make_int4(0x7fffffff, 0, -1, 0);
+    for (int c = t; c < P.n_cta; c += 1024) {
+        cta[c] = make_int4(0x7fffffff, 0, -1, 0);
+        cta[P.n_cta + 2 * c] = cta[P.n_cta + 2 * c + 1] = make_int4(0, 0, 0, 0);
+    }
     long long mine = 0;
     int cnt = 0, most = 0;
     for (int it = b0; it < b1; ++it) {
@@ -1134,9 +1251,9 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
                 atomicMin(&cta[c].x, r + c);
                 atomicMax(&cta[c].y, r + c + 1);
             }
-            if (cb > ca) {
-                cta[ca + 1].z = it;
-                cta[ca + 1].w = cb - ca + 1;
+            for (int c = ca + 1; c <= cb; ++c) {
+                cta[c].z = ca;
+                cta[c].w = cb - ca + 1;
             }
         }
         off += nk + kStart;
@@ -1174,13 +1291,7 @@ __device__ __forceinline__ void load_slice(const float* src, int lane, float (&v
     }
 }
 template <int D, typename PartOf>
-__device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf part_of, int lane, uint16_t* out_row,
-                                          bool even = false) {
-    auto range = [even](int n_kt, int k, int n, int& a, int& b) {
-        a = 0;
-        b = 1;  // even mode: no piece is empty
-        if (!even) piece_range(n_kt, k, n, a, b);
-    };
+__device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf part_of, int lane, uint16_t* out_row) {
     constexpr int NV = D / 32;  // dims per lane: 4 or 2
     if (n_pieces <= 8) {
         float v[8][NV];
@@ -1188,7 +1299,7 @@ __device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf par
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             int a = 0, b = 0;
-            if (k < n_pieces) range(n_kt_all, k, n_pieces, a, b);
+            if (k < n_pieces) piece_range(n_kt_all, k, n_pieces, a, b);
             ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int e = 0; e < NV; ++e) v[k][e] = 0.f;
@@ -1215,7 +1326,7 @@ __device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf par
     float m_mine = -INFINITY, l_mine = 0.f;
     for (int k = lane; k < n_pieces; k += 32) {
         int a, b;
-        range(n_kt_all, k, n_pieces, a, b);
+        piece_range(n_kt_all, k, n_pieces, a, b);
         if (b > a) {
             const float2 ml = *reinterpret_cast<const float2*>(part_of(k) + kPartML);
             if (ml.x > m_mine) {  // keep the larger reference; rescale the other sum
@@ -1240,7 +1351,7 @@ __device__ __forceinline__ void merge_row(int n_pieces, int n_kt_all, PartOf par
         for (int u = 0; u < 8; ++u) {
             const int k = k0 + u;
             int a = 0, b = 0;
-            if (k < n_pieces) range(n_kt_all, k, n_pieces, a, b);
+            if (k < n_pieces) piece_range(n_kt_all, k, n_pieces, a, b);
             f[u] = 0.f;
 #pragma unroll
             for (int e = 0; e < NV; ++e) v[u][e] = 0.f;
@@ -1312,29 +1423,6 @@ __global__ void __launch_bounds__(128) pa_prefill_merge_cut_kernel(const Prefill
                  lane, P.out + ((size_t)(q0 + i) * P.n_heads + kvh * G + r % G) * D);
 }
 
-// Even mode: one warp per (row, head) of the cut items, found at the CTA that
-// holds an item's second piece.
-template <int G, int D>
-__global__ void __launch_bounds__(128) pa_prefill_merge_even_kernel(const PrefillParams P) {
-    constexpr int QT = kRows / G;
-    pa::grid_dependency_wait();  // every piece's partial is written
-    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int c = w >> 8, x = (w >> 7) & 1, r = w & 127;
-    const int4 e = P.work[P.n_items + P.n_cta + c];
-    if (e.z < 0) return;
-    const int item = e.z, Hk = P.n_kv_heads;
-    const int s = item / (Hk * P.n_qp), kvh = (item / P.n_qp) % Hk, qp = item % P.n_qp;
-    const int q0 = P.qsl[s], L = P.qsl[s + 1] - q0;
-    const int i = qp * 2 * QT + x * QT + r / G;
-    if (i >= L) return;
-    merge_row<D>(e.w, 0,
-                 [&](int k) {
-                     const size_t slot = k == 0 ? 2 * c - 1 : 2 * (c - 1 + k);
-                     return P.part + ((slot * 2 + x) * 128 + r) * kPartStride;
-                 },
-                 lane, P.out + ((size_t)(q0 + i) * P.n_heads + kvh * G + r % G) * D, true);
-}
-
 template <int G, int D, int EB, bool WIN>
 int launch_prefill(const PrefillParams& Pp, const CUtensorMap& tk, const CUtensorMap& tv, int n_seqs,
                    int max_chunk_len, int n_rows, cudaStream_t stream) {
@@ -1351,12 +1439,10 @@ int launch_prefill(const PrefillParams& Pp, const CUtensorMap& tk, const CUtenso
     }
     constexpr int QT = kRows / G;
     const int n_qp = (max_chunk_len + 2 * QT - 1) / (2 * QT);
-    if (WIN && Pp.work) {  // even mode: plan, one CTA per SM, merge; each launched ahead of the one before's end
-        int st = pa_launch_pdl(pa_prefill_plan_even_kernel<G>, dim3(1), dim3(1024), 0, stream, Pp);
-        if (st == PA_OK) st = pa_launch_pdl(kern, dim3((unsigned)Pp.n_cta), dim3(kThreads), kSmemBytes, stream, Pp, tk, tv);
-        if (st == PA_OK)
-            st = pa_launch_pdl(pa_prefill_merge_even_kernel<G, D>, dim3((unsigned)Pp.n_cta * 64), dim3(128), 0, stream, Pp);
-        return st;
+    if (WIN && Pp.work) {  // even mode: plan, then one CTA per SM, launched ahead of the plan's end
+        const int st = pa_launch_pdl(pa_prefill_plan_even_kernel<G>, dim3(1), dim3(1024), 0, stream, Pp);
+        if (st != PA_OK) return st;
+        return pa_launch_pdl(kern, dim3((unsigned)Pp.n_cta), dim3(kThreads), kSmemBytes, stream, Pp, tk, tv);
     }
     if (Pp.work) {  // balanced mode: plan, then one CTA per SM taking work-list entries
         pa_prefill_plan_kernel<G><<<1, 1024, 0, stream>>>(Pp);
