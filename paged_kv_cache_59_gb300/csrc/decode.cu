@@ -1092,6 +1092,28 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
 
 namespace {
 
+// The maximum M and the sum L of a row's partitions (a warp; lane p reads those
+// of partitions p, p + 32, ...).
+__device__ __forceinline__ void merge_stats(const DecodeParams& P, size_t slot0, int nparts, int lane, float& M,
+                                            float& L) {
+    float m_mine = -INFINITY, l_mine = 0.f;  // this lane's partitions, relative to m_mine
+    for (int p = lane; p < nparts; p += 32) {
+        const float2 ml = *reinterpret_cast<const float2*>(P.ws_ml + (slot0 + p) * 2);
+        if (ml.x > m_mine) {
+            l_mine = (m_mine == -INFINITY ? 0.f : l_mine * pa::fast_exp2(m_mine - ml.x)) + ml.y;
+            m_mine = ml.x;
+        } else if (ml.x != -INFINITY) {
+            l_mine += ml.y * pa::fast_exp2(ml.x - m_mine);
+        }
+    }
+    M = m_mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    L = m_mine == -INFINITY ? 0.f : l_mine * pa::fast_exp2(m_mine - M);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+}
+
 // Split-K merge: one warp per (sequence, query head) row. Lane p reads the
 // (m, l) of partitions p, p+32, ...; a warp reduction gives M and L; then the
 // partitions' output slices are loaded eight at a time, so a row costs two
@@ -1111,22 +1133,8 @@ pa_decode_merge_kernel(const DecodeParams P, int n_rows) {
     const int nparts = Span(P, ctx).nparts;
     if (nparts <= 1) return;  // the partition kernel wrote this row
     const size_t slot0 = (size_t)row * P.max_parts;
-    float m_mine = -INFINITY, l_mine = 0.f;  // this lane's partitions, relative to m_mine
-    for (int p = lane; p < nparts; p += 32) {
-        const float2 ml = *reinterpret_cast<const float2*>(P.ws_ml + (slot0 + p) * 2);
-        if (ml.x > m_mine) {
-            l_mine = (m_mine == -INFINITY ? 0.f : l_mine * pa::fast_exp2(m_mine - ml.x)) + ml.y;
-            m_mine = ml.x;
-        } else if (ml.x != -INFINITY) {
-            l_mine += ml.y * pa::fast_exp2(ml.x - m_mine);
-        }
-    }
-    float M = m_mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float L = m_mine == -INFINITY ? 0.f : l_mine * pa::fast_exp2(m_mine - M);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+    float M, L;
+    merge_stats(P, slot0, nparts, lane, M, L);
     float acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = 0.f;
@@ -1160,6 +1168,40 @@ pa_decode_merge_kernel(const DecodeParams P, int n_rows) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(P.out + (size_t)row * D + lane * PER);
 #pragma unroll
     for (int k = 0; k < PER; k += 2) dst[k / 2] = pa::float2_to_bf16x2(acc[k] * inv, acc[k + 1] * inv);
+}
+
+// The same for many partitions: D / 32 warps share a row, one dim a lane, and
+// 32 partitions' outputs are in flight at a time. The steps and their order are
+// those of the kernel above, so the bits are too. A few long sequences leave
+// that one short of loads: 4 sequences of 64 heads and 128 partitions took 22
+// us in it (256 warps, 16 rounds of memory latency each).
+template <int D>
+__global__ void __launch_bounds__(128)
+pa_decode_merge_wide_kernel(const DecodeParams P, int n_rows) {
+    constexpr int W = D / 32, U = 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x * (4 / W) + warp / W;  // (seq, head) row
+    const int d = (warp % W) * 32 + lane;
+    pa::grid_dependency_wait();  // every partition's partial is written
+    if (row >= n_rows) return;
+    const int ctx = P.ctx[row / P.n_heads];
+    if (ctx <= 0) return;
+    const int nparts = Span(P, ctx).nparts;
+    if (nparts <= 1) return;  // the partition kernel wrote this row
+    const size_t slot0 = (size_t)row * P.max_parts;
+    float M, L;
+    merge_stats(P, slot0, nparts, lane, M, L);
+    float acc = 0.f;
+    for (int p0 = 0; p0 < nparts; p0 += U) {
+        const float m = p0 + lane < nparts ? P.ws_ml[(slot0 + p0 + lane) * 2] : -INFINITY;
+        float v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = p0 + u < nparts ? P.ws_o[(slot0 + p0 + u) * D + d] : 0.f;
+        const float f = m == -INFINITY ? 0.f : pa::fast_exp2(m - M);
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc += v[u] * __shfl_sync(kFull, f, u);
+    }
+    P.out[(size_t)row * D + d] = (uint16_t)pa::float2_to_bf16x2(acc * (1.f / L), 0.f);
 }
 
 constexpr int kNW = 4;  // warps per CTA
@@ -1451,6 +1493,11 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     if (st != PA_OK || max_parts <= 1) return st;
     const int n_rows = n_seqs * n_heads;
     dim3 grid((n_rows + 3) / 4);
+    if (max_parts > 8) {  // more than one round of the kernel for few partitions
+        if (head_dim == 128)
+            return pa_launch_pdl(pa_decode_merge_wide_kernel<128>, dim3(n_rows), dim3(128), 0, s, P, n_rows);
+        return pa_launch_pdl(pa_decode_merge_wide_kernel<64>, dim3((n_rows + 1) / 2), dim3(128), 0, s, P, n_rows);
+    }
     if (head_dim == 128) return pa_launch_pdl(pa_decode_merge_kernel<128>, grid, dim3(128), 0, s, P, n_rows);
     return pa_launch_pdl(pa_decode_merge_kernel<64>, grid, dim3(128), 0, s, P, n_rows);
 }
