@@ -142,11 +142,11 @@ __device__ __forceinline__ void rotate16(float (&x)[16], const float (&cs)[8], c
 
 // Rows of q (and, in bf16 and per-head mode, of k and v). A CTA takes a tile
 // of kThreads / (D / 16) tokens and `rows_per_thread` head rows of each; a
-// thread keeps its token's eight angles in registers over its rows, four rows'
+// thread keeps its token's eight angles in registers over its rows, U rows'
 // loads in flight at a time.
-template <int D, int MODE>
+template <int D, int MODE, int U>
 __device__ __forceinline__ void rotate_rows(const RopeParams& P, int cta) {
-    constexpr int LPR = D / 16, TPC = kThreads / LPR, U = 4;
+    constexpr int LPR = D / 16, TPC = kThreads / LPR;
     const int c = threadIdx.x % LPR;
     const long long t64 = (long long)(cta / P.row_groups) * TPC + threadIdx.x / LPR;
     if (t64 >= P.n_tokens) return;
@@ -238,16 +238,14 @@ __device__ __forceinline__ float power_scale(float amax) {
 // K and V of a block-scaled cache. The scale of a (block, head) covers all of
 // its tokens, so the tokens of one call that go to one block - a run: tokens
 // next to each other in the call with consecutive slots of one block, up to
-// 16 - belong to one warp, which holds them in registers, finds their largest
-// magnitude and encodes them. A run that starts at the block's first slot
+// 16 - belong to one warp, which finds their largest magnitude and encodes them.
+// A run that starts at the block's first slot
 // gives the block its scale; any other run raises the scale if it must, and
 // then also encodes the block's other tokens again. As scales are powers of
 // two, that is exact for every code whose new value is not an E4M3 subnormal,
 // and off by at most 2^-10 of the new scale (half a subnormal step) there:
 // tokens do not lose a bit each time the block's scale grows.
-// One warp per (tokens_per_warp tokens, KV head, K or V): one token in small
-// batches (each is a run of its own, and latency counts), sixteen in large
-// ones (a prompt's run is found by one warp of sixteen, not by sixteen).
+// One warp per (tokens_per_warp tokens, KV head, K or V).
 template <int D>
 __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta) {
     constexpr int LPR = D / 16, TPP = 32 / LPR, NP = kBS / TPP;  // lanes per row, rows per pass, passes
@@ -293,36 +291,37 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
         const int off0 = (int)(slot0 % kBS);
         const long long tile = slot0 / kBS * P.n_kv_heads + h;
         const float old = scales[tile];
-        uint4 raw[NP][2];
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int i = p * TPP + tg;
-            raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
-            if (i < n) {
-                const uint4* row = reinterpret_cast<const uint4*>(src + (t0 - 1 + l0 + i) * stride + h * D);
-                raw[p][0] = row[ca];
-                raw[p][1] = row[cb];
-            }
-        }
-        float x[NP][16];
-        float amax = 0.f;  // over finite values
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int i = p * TPP + tg;
+        // the run's rows are read twice, the second time from L1: holding 16 rotated
+        // rows in registers would halve the warps that hide the loads' latency
+        auto row_of = [&](int i) { return reinterpret_cast<const uint4*>(src + (t0 - 1 + l0 + i) * stride + h * D); };
+        auto rotated = [&](const uint4 a, const uint4 b, int i, float (&x)[16]) {  // lanes of a row: row i of the run
             const int at = __shfl_sync(kFull, pos, min(l0 + i, 31));
-            widen8(raw[p][0], x[p]);
-            widen8(raw[p][1], x[p] + 8);
+            widen8(a, x);
+            widen8(b, x + 8);
             if (turn && i < n) {
                 float cs[8], sn[8];
                 const float* row = P.cos_sin + (long long)at * P.rot;
                 load8(row + 8 * c, cs);
                 load8(row + P.rot / 2 + 8 * c, sn);
-                rotate16(x[p], cs, sn, il);
+                rotate16(x, cs, sn, il);
             }
+        };
+        float amax = 0.f;  // over finite values
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            if (p * TPP >= n) break;
+            const int i = p * TPP + tg;
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (i < n) {
+                a = row_of(i)[ca];
+                b = row_of(i)[cb];
+            }
+            float x[16];
+            rotated(a, b, i, x);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                const float a = fabsf(x[p][k]);
-                if (a < INFINITY) amax = fmaxf(amax, a);
+                const float v = fabsf(x[k]);
+                if (v < INFINITY) amax = fmaxf(amax, v);
             }
         }
 #pragma unroll
@@ -357,13 +356,21 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
+            if (p * TPP >= n) break;
             const int i = p * TPP + tg;
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (i < n) {
+                a = row_of(i)[ca];
+                b = row_of(i)[cb];
+            }
+            float x[16];
+            rotated(a, b, i, x);
             if (i < n) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[p][k] *= inv;
+                for (int k = 0; k < 16; ++k) x[k] *= inv;
                 uint2* row = reinterpret_cast<uint2*>(blk + (off0 + i) * D);
-                row[ca] = codes8(x[p]);
-                row[cb] = codes8(x[p] + 8);
+                row[ca] = codes8(x);
+                row[cb] = codes8(x + 8);
             }
         }
         if (lane == 0) scales[tile] = s;
@@ -371,8 +378,22 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
     }
 }
 
-template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeParams P) {
+// Two forms of each kernel. A small call is one wave of short-lived CTAs, where
+// spilled registers would only add latency: up to 102 registers a thread, four
+// rows in flight. A large one is bound by HBM (K/V warps: by latency) and wants
+// warps: 80 registers, or 64 and two rows in flight for the block-scaled
+// cache, whatever spills. Measured small / large (64 / 8,192 tokens of 64/8
+// heads of 128 in bf16; 64 tokens / 7,377 in ragged chunks of 32/8 heads in
+// E4M3): 2.2 / 54.1 us and 2.9 / 35.4 us in the first form, 2.4 / 52.6 and 3.8 /
+// 30.8 in the second.
+template <int MODE, bool LARGE>
+struct Form {
+    static constexpr int U = LARGE && MODE == kBlockScale ? 2 : 4;
+    static constexpr int kCtasPerSm = !LARGE ? 5 : MODE == kBlockScale ? 8 : 6;
+};
+
+template <int D, int MODE, bool LARGE>
+__global__ void __launch_bounds__(kThreads, Form<MODE, LARGE>::kCtasPerSm) rope_cache_kernel(const RopeParams P) {
     pa::launch_dependents();     // the next kernel (decode, prefill) may be scheduled
     pa::grid_dependency_wait();  // earlier readers and writers of q and the pool are complete
     int cta = blockIdx.x;
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeParams P
         }
         cta -= P.kv_ctas;
     }
-    rotate_rows<D, MODE>(P, cta);
+    rotate_rows<D, MODE, Form<MODE, LARGE>::U>(P, cta);
 }
 
 int sm_count() {
@@ -413,18 +434,26 @@ int launch(RopeParams& P, cudaStream_t stream) {
     const int n_rows = MODE == kBlockScale ? P.n_heads : P.n_heads + 2 * P.n_kv_heads;
     // one row a thread while that still fits in one wave of 16 CTAs per SM;
     // beyond it eight, which read a token's angles an eighth as often
-    P.rows_per_thread = tiles * n_rows <= 16LL * sms ? 1 : 8;
+    const bool large = tiles * n_rows > 16LL * sms;
+    P.rows_per_thread = large ? 8 : 1;
     P.row_groups = (n_rows + P.rows_per_thread - 1) / P.rows_per_thread;
     long long ctas = tiles * P.row_groups, kv = 0;
     if (MODE == kBlockScale) {
         const long long units = 2LL * P.n_kv_heads;
-        P.tokens_per_warp = P.n_tokens * units <= 16LL * kWarps * sms ? 1 : 16;
+        // K/V warps look at one token each while that is one wave of them. Beyond it a warp
+        // takes several: 16 suit prompt chunks (30.8 us against 34.2 with 4 for 7,377 tokens),
+        // where a warp finds one run, but a decode batch has a run per token and its warps
+        // would work through 16 (2,048 sequences: 39.9 us against 22.6), so calls that can
+        // still be one take 4.
+        P.tokens_per_warp = P.n_tokens * units <= 16LL * kWarps * sms ? 1 : P.n_tokens <= 4096 ? 4 : 16;
         const long long warps = ((long long)P.n_tokens + P.tokens_per_warp - 1) / P.tokens_per_warp * units;
         kv = (warps + kWarps - 1) / kWarps;
     }
     if (ctas + kv > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     P.kv_ctas = (int)kv;
-    return pa_launch_pdl(rope_cache_kernel<D, MODE>, dim3((unsigned)(ctas + kv)), dim3(kThreads), 0, stream, P);
+    const dim3 grid((unsigned)(ctas + kv));
+    return large ? pa_launch_pdl(rope_cache_kernel<D, MODE, true>, grid, dim3(kThreads), 0, stream, P)
+                 : pa_launch_pdl(rope_cache_kernel<D, MODE, false>, grid, dim3(kThreads), 0, stream, P);
 }
 
 template <int MODE>
