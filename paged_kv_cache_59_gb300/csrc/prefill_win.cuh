@@ -33,9 +33,11 @@
 
 namespace {
 
-// 8 softmax warps, MMA warp (8), K producer (9), 4 converter warps (10..13), V
-// producer (14); four warps a scheduler at most, so 128 registers each.
-constexpr int kWinThreads = 480;
+// 8 softmax warps, MMA warp (8), producer (9; bf16: of K), 4 converter warps
+// (10..13), bf16: V producer (14); four warps a scheduler at most, so 128
+// registers each.
+template <int EB>
+constexpr int kWinThreads = EB == 2 ? 480 : 448;
 
 // Shared memory, as PfLay: EB = bytes per cached element. With an E4M3 cache the
 // codes of a K and of a V tile land in a buffer of their own (128 rows of D
@@ -54,8 +56,7 @@ struct WinLay {
     static constexpr uint32_t kRawTile = kKT * D;
     static constexpr uint32_t kBars = kRaw + (EB == 1 ? 2 * kRawTile : 0);  // mbarriers
     static constexpr uint32_t kMisc = kBars + 256;       // tmem slot, abort flag
-    static constexpr uint32_t kScales = kMisc + 64;      // E4M3: per softmax warp, the tile's 8 blocks' float4
-    static constexpr uint32_t kSmem = kScales + (EB == 1 ? 8 * kBPT * 16 : 0);
+    static constexpr uint32_t kSmem = kMisc + 64;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -169,13 +170,15 @@ __device__ __forceinline__ bool hides_rows(const PrefillParams& P, const KeyTile
 // so it nearly always is the last one and never writes.)
 // Partial of a slot's tile x: float4 [D / 4][128 rows] of O, then float2 [128]
 // of (m, l). `own(c, v)` gives columns 32 c .. 32 c + 31 of this row's O (warp-
-// collective); `put(c, v)` takes the joined ones, normalised.
+// collective); `put(c, v)` takes the joined ones, normalised, and put_row(rr, v)
+// columns 4 lane .. of the warp's row rr. `valid`: the row is in the chunk (the
+// valid rows of a warp are its first).
 __device__ __forceinline__ float* slot_part(const PrefillParams& P, int slot, int x) {
     return P.part + ((size_t)slot * 2 + x) * 128 * kPartStride;
 }
-template <int D, typename Own, typename Put>
-__device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, int x, int r, int warp, int lane, float m,
-                                            float l, Own own, Put put) {
+template <int D, typename Own, typename Put, typename PutRow>
+__device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, int x, int r, int warp, int lane, bool valid,
+                                            float m, float l, Own own, Put put, PutRow put_row) {
     const int4* cta = P.work + P.n_items + P.n_cta;
     const int c = slot >> 1;
     const int4 info = cta[slot & 1 ? c + 1 : c];
@@ -186,7 +189,13 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
         return v;
     };
-    bool last = __all_sync(kFull, counted() == n - 1);
+    auto piece_part = [&](int k) { return slot_part(P, k == 0 ? 2 * ca + 1 : 2 * (ca + k), x); };
+    // A few rows in many pieces (a chunk of a token or two behind a long context) are joined row by
+    // row, the lanes along the columns and eight pieces' loads in flight, when that takes fewer
+    // rounds of memory latency than 32 columns of a piece at a time.
+    const int rows = __popc(__ballot_sync(kFull, valid));
+    const bool by_row = rows * ((n + 7) / 8) < D / 32 * (n - 1);
+    bool last = !by_row && __all_sync(kFull, counted() == n - 1);
     if (!last) {
         float* dst = slot_part(P, slot, x);
 #pragma unroll 1
@@ -206,9 +215,47 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
         if (last) last = __all_sync(kFull, counted() == n);  // (always: all have been counted)
     }
     if (!last) return;
+    if (by_row) {
+        for (int rr = 0; rr < rows; ++rr) {
+            const int row = (r & ~31) + rr;
+            auto row_ml = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(piece_part(k) + 128 * D) + row); };
+            float M = -INFINITY, sum = 0.f;
+            for (int k = lane; k < n; k += 32) M = fmaxf(M, row_ml(k).x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+            for (int k = lane; k < n; k += 32) {
+                const float2 p = row_ml(k);
+                sum += p.x == -INFINITY ? 0.f : p.y * pa::fast_exp2(p.x - M);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < n; k0 += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    v[u] = k0 + u < n && lane < D / 4
+                               ? __ldcg(reinterpret_cast<const float4*>(piece_part(k0 + u)) + lane * 128 + row)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                const int k = k0 + (lane & 7);
+                const float m_k = k < n ? row_ml(k).x : -INFINITY, f = m_k == -INFINITY ? 0.f : pa::fast_exp2(m_k - M);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float fu = __shfl_sync(kFull, f, u);
+                    acc.x += v[u].x * fu;
+                    acc.y += v[u].y * fu;
+                    acc.z += v[u].z * fu;
+                    acc.w += v[u].w * fu;
+                }
+            }
+            const float inv = 1.f / sum;
+            put_row(rr, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        }
+        return;
+    }
     auto ml = [&](int k) {
         return k == me ? make_float2(m, l)
-                       : __ldcg(reinterpret_cast<const float2*>(slot_part(P, k == 0 ? 2 * ca + 1 : 2 * (ca + k), x) + 128 * D) + r);
+                       : __ldcg(reinterpret_cast<const float2*>(piece_part(k) + 128 * D) + r);
     };
     float M = -INFINITY, sum = 0.f;
     for (int k = 0; k < n; ++k) M = fmaxf(M, ml(k).x);
@@ -228,7 +275,7 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
             if (k == me) {  // warp-uniform
                 own(q, v);
             } else {
-                const float4* src = reinterpret_cast<const float4*>(slot_part(P, k == 0 ? 2 * ca + 1 : 2 * (ca + k), x));
+                const float4* src = reinterpret_cast<const float4*>(piece_part(k));
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const float4 w = __ldcg(src + (8 * q + u) * 128 + r);
@@ -248,7 +295,7 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
 }
 
 template <int G, int D, int EB>
-__global__ void __launch_bounds__(kWinThreads, 1)
+__global__ void __launch_bounds__(kWinThreads<EB>, 1)
 pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
     using L_ = WinLay<D, EB>;
@@ -291,40 +338,50 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
     int J0 = 0;      // tiles of the segments before
 
     if (warp == 9 || warp == 14) {
-        // ---------------------------------------------------- TMA producers, K and V
-        // A stage is refilled as soon as its last reader is done: when a tile's load waits in line
-        // behind the other operand's, or behind its own address arithmetic, the tensor core waits
-        // for it (bf16, a warp for both: 1.86 us a tile instead of WIN_TILE). E4M3: K(J)'s codes
-        // replace K(J-1)'s once those are widened, V's likewise.
-        const int x = warp == 14;
-        const CUtensorMap* map = x ? &tmV : &tmK;
-        constexpr int kKN = EB == 2 ? kKS : 1, kVN = EB == 2 ? kVS : 1;
-        const int n_stages = x ? kVN : kKN;
-        uint64_t* full = x ? bars.v_full(0) : bars.k_full(0);
-        uint64_t* free = EB == 1 ? bars.raw_free(x) : x ? bars.v_free(0) : bars.k_free(0);
+        // ----------------------------------------------------------- TMA producers
+        // A stage is refilled as soon as its last reader is done. bf16: K and V have a warp each:
+        // when a tile's load waits in line behind the other operand's, the tensor core waits for it
+        // (1.86 us a tile with one warp, 1.67 with two). E4M3, half the bytes and boxes: one warp
+        // for both (1.75 us a tile; 1.83 with a second one, which takes issue slots from the
+        // softmax); K(J)'s codes replace K(J-1)'s once those are widened, V's likewise.
+        constexpr int kBoth = EB == 1;
         constexpr uint32_t kBytes = EB == 2 ? kTile : L_::kRawTile;
-        unsigned char* ring = sm + (EB == 1 ? L_::kRaw + x * L_::kRawTile : x ? L_::kV0 : L_::kK0);
-        // the next stage; the parity of the phase that frees it (for a first fill: of the phase
-        // before the barrier's first, which passes)
-        int st = 0, ph = 1;
+        // bf16: lane l < 8 kNH moves box (block l / kNH, dims 64 g .., g = l % kNH); E4M3: lane
+        // l < 8 block l's 16 x D codes
+        constexpr int NB = EB == 2 ? kNH : 1;
+        const int b = (lane / NB) & (kBPT - 1), half = lane % NB;
+        const uint32_t box = EB == 2 ? half * 16384 + b * 2048 : b * (kBS * D);
+        struct Ring {  // one operand's
+            const CUtensorMap* map;
+            unsigned char* mem;
+            uint64_t *full, *free;
+            int n_stages;
+            int st = 0, ph = 1;  // the next stage; the parity of the phase that frees it (for a first fill: of
+                                 // the phase before the barrier's first, which passes)
+            int ids, group;      // block ids of key tiles 4 group .. + 3, one per lane
+        };
+        auto ring = [&](int x) {
+            Ring r;
+            r.map = x ? &tmV : &tmK;
+            r.mem = sm + (EB == 1 ? L_::kRaw + x * L_::kRawTile : x ? L_::kV0 : L_::kK0);
+            r.full = x ? bars.v_full(0) : bars.k_full(0);
+            r.free = EB == 1 ? bars.raw_free(x) : x ? bars.v_free(0) : bars.k_free(0);
+            r.n_stages = EB == 1 ? 1 : x ? kVS : kKS;
+            return r;
+        };
+        Ring first = ring(warp == 14), second = ring(1);
         while (ok && segments.next(g)) {
             const KeyTiles keys = segments.keys(g);
             const int nblk = min((g.ctx + kBS - 1) / kBS, P.max_blocks);
             const int32_t* trow = P.tables + (size_t)g.s * P.max_blocks;
-            // bf16: lane l < 8 kNH moves box (block l / kNH, dims 64 g .., g = l % kNH); E4M3: lane
-            // l < 8 block l's 16 x D codes
-            constexpr int NB = EB == 2 ? kNH : 1;
-            const int b = (lane / NB) & (kBPT - 1), half = lane % NB;
-            const uint32_t box = EB == 2 ? half * 16384 + b * 2048 : b * (kBS * D);
-            int ids = -1, group = -1;  // block ids of key tiles 4 group .. + 3, one per lane
-            for (int j = 0; j < g.n_kt; ++j) {
-                const int tile = keys.tile(g.kt0 + j);
-                if ((tile >> 2) != group) {  // warp-collective
-                    group = tile >> 2;
-                    const int blk = group * 32 + lane;
-                    ids = blk < nblk ? trow[blk] : -1;
+            first.group = second.group = -1;
+            auto load = [&](Ring& r, int tile) {
+                if ((tile >> 2) != r.group) {  // warp-collective
+                    r.group = tile >> 2;
+                    const int blk = r.group * 32 + lane;
+                    r.ids = blk < nblk ? trow[blk] : -1;
                 }
-                const int bid = __shfl_sync(kFull, ids, (tile & 3) * kBPT + b);
+                const int bid = __shfl_sync(kFull, r.ids, (tile & 3) * kBPT + b);
                 const int blk = tile * kBPT + b;
                 // blocks past the context, or between the sinks and the window (they may be released): zeros
                 bool in = blk < nblk && keys.seen(P, blk * kBS, blk * kBS + kBS);
@@ -333,17 +390,22 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     in = false;
                 }
                 const int y = in ? (bid * Hk + g.kvh) * kBS : P.oob_row;  // out of range: zero fill
-                ok = wait_bar(free + st, (uint32_t)ph, P.err, abort_flag);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                if (lane == 0) pa::mbar_arrive_expect_tx(full + st, kBytes);
+                ok = __all_sync(kFull, wait_bar(r.free + r.st, (uint32_t)r.ph, P.err, abort_flag));
+                if (!ok) return;
+                if (lane == 0) pa::mbar_arrive_expect_tx(r.full + r.st, kBytes);
                 __syncwarp();
-                if (lane < NB * kBPT) tc::tma_load_2d(ring + st * kBytes + box, map, half * 64, y, full + st);
+                if (lane < NB * kBPT)
+                    tc::tma_load_2d(r.mem + r.st * kBytes + box, r.map, half * 64, y, r.full + r.st);
                 __syncwarp();
-                if (++st == n_stages) {
-                    st = 0;
-                    ph ^= 1;
+                if (++r.st == r.n_stages) {
+                    r.st = 0;
+                    r.ph ^= 1;
                 }
+            };
+            for (int j = 0; ok && j < g.n_kt; ++j) {
+                const int tile = keys.tile(g.kt0 + j);
+                load(first, tile);
+                if (kBoth && ok) load(second, tile);
             }
         }
         // Every issued copy lands before the CTA exits: normally the converters and the tensor
@@ -613,9 +675,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             float m_used = -INFINITY, l = 0.f;
             // E4M3: lane l holds the scales of block l % 8 of a key tile; those of
             // tile j + 1 and the block id of tile j + 2 are loaded while tile j is
-            // worked on. A tile's, as (K scale times `scale`, log2 and inverse of V's), are handed to
-            // the warp's lanes through shared memory.
-            float4* my_scales = reinterpret_cast<float4*>(sm + L_::kScales) + warp * kBPT;
+            // worked on.
             const int nblk = min((g.ctx + kBS - 1) / kBS, P.max_blocks);
             auto block_id = [&](int j) {
                 const int blk = j < g.n_kt ? keys.tile(g.kt0 + j) * kBPT + (lane & (kBPT - 1)) : nblk;
@@ -634,11 +694,12 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             }
             for (int j = 0; j < g.n_kt; ++j) {
                 const int J = J0 + j;
+                float my_k = 0.f, my_e = 0.f, my_inv = 0.f;
                 if constexpr (EB == 1) {  // the approximate log2 and reciprocal are off by 2^-22, far below w's rounding
                     const float vs = clamp_scale(vs_next);
-                    __syncwarp();  // the last tile's are read
-                    if (lane < kBPT) my_scales[lane] = make_float4(clamp_scale(ks_next) * sc, __log2f(vs), __fdividef(1.f, vs), 0.f);
-                    __syncwarp();
+                    my_k = clamp_scale(ks_next) * sc;
+                    my_e = __log2f(vs);
+                    my_inv = __fdividef(1.f, vs);
                     ks_next = scale_of(P.k_scale, bid_next);
                     vs_next = scale_of(P.v_scale, bid_next);
                     bid_next = block_id(j + 2);
@@ -698,10 +759,9 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         if constexpr (EB == 1) {
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
-                                const float4 f = my_scales[2 * qd + b];
-                                qk[b] = f.x;
-                                qe[b] = f.y;
-                                qi[b] = f.z;
+                                qk[b] = __shfl_sync(kFull, my_k, 2 * qd + b);
+                                qe[b] = __shfl_sync(kFull, my_e, 2 * qd + b);
+                                qi[b] = __shfl_sync(kFull, my_inv, 2 * qd + b);
                             }
                         }
                         uint32_t ph[16];
@@ -804,8 +864,17 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         make_uint4(pa::float2_to_bf16x2(v[k], v[k + 1]), pa::float2_to_bf16x2(v[k + 2], v[k + 3]),
                                    pa::float2_to_bf16x2(v[k + 4], v[k + 5]), pa::float2_to_bf16x2(v[k + 6], v[k + 7]));
             };
-            if (g.slot >= 0) {
-                join_pieces<D>(P, g.slot, x, r, warp, lane, m_used, l, own, put);
+            if (g.slot >= 0 && !__any_sync(kFull, i < g.L)) {
+                // no row of this warp is in the chunk: nothing to keep, here and in the other pieces
+            } else if (g.slot >= 0) {
+                join_pieces<D>(P, g.slot, x, r, warp, lane, i < g.L, m_used, l, own, put, [&](int rr, float4 v) {
+                    uint16_t* row = reinterpret_cast<uint16_t*>(
+                        __shfl_sync(kFull, (unsigned long long)reinterpret_cast<uintptr_t>(dst), rr));
+                    if (lane >= D / 4) return;
+                    finite &= fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY;
+                    reinterpret_cast<uint2*>(row)[lane] =
+                        make_uint2(pa::float2_to_bf16x2(v.x, v.y), pa::float2_to_bf16x2(v.z, v.w));
+                });
             } else if (P.work || P.splits <= 1) {
                 const float inv = 1.f / l;
 #pragma unroll 1
@@ -972,9 +1041,9 @@ int launch_prefill_win(const PrefillParams& Pp, const CUtensorMap& tk, const CUt
     if (Pp.work) {  // even mode: plan, then one CTA per SM, launched ahead of the plan's end
         const int st = pa_launch_pdl(pa_prefill_plan_even_kernel<G>, dim3(1), dim3(1024), 0, stream, Pp);
         if (st != PA_OK) return st;
-        return pa_launch_pdl(kern, dim3((unsigned)Pp.n_cta), dim3(kWinThreads), kSmemBytes, stream, Pp, tk, tv);
+        return pa_launch_pdl(kern, dim3((unsigned)Pp.n_cta), dim3(kWinThreads<EB>), kSmemBytes, stream, Pp, tk, tv);
     }
-    const int st = pa_launch_pdl(kern, dim3(Pp.n_qp * Pp.splits, Pp.n_kv_heads, n_seqs), dim3(kWinThreads), kSmemBytes, stream,
+    const int st = pa_launch_pdl(kern, dim3(Pp.n_qp * Pp.splits, Pp.n_kv_heads, n_seqs), dim3(kWinThreads<EB>), kSmemBytes, stream,
                                  Pp, tk, tv);
     if (st != PA_OK || Pp.splits <= 1) return st;
     // rows of all chunks: the merge finds each row's sequence in q_start_loc

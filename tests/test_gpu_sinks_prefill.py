@@ -146,6 +146,19 @@ def test_a_long_window(pk):
     check_device_error(0)
 
 
+@pytest.mark.parametrize("D,H,Hk", [(128, 4, 1), (64, 2, 2), (128, 8, 1), (64, 1, 1)])
+def test_short_chunks_behind_long_contexts(pk, D, H, Hk):
+    """One to forty rows behind up to 9,000 tokens: many pieces of few rows, joined
+    by row, and of many, joined by column; twice, with the same bits."""
+    for chunk, ctx in (([1], [9000]), ([3, 1], [5000, 200]), ([40], [9000]), ([1, 17], [3000, 6001])):
+        for kind, window, sinks in (("bf16", 2 ** 30, 0), ("block", -1, 0), ("bf16", 4000, 5)):
+            c = Cache(9, kind, ctx, Hk, D, window if window < 2 ** 30 else -1, sinks, chunk)
+            c.window = window
+            check(pk, c, H, D, chunk, 0, f"{kind} {chunk}")
+            q = f32_to_bf16_bits(np.random.default_rng(1).standard_normal((sum(chunk), H, D)).astype(np.float32))
+            assert np.array_equal(run(pk, c, q, chunk, 0), run(pk, c, q, chunk, 0))
+
+
 def test_rows_behind_the_last_chunk_and_a_loose_bound(pk):
     """q and out longer than the chunks, max_chunk_len above every chunk: the
     rows behind the last one stay as they were."""
