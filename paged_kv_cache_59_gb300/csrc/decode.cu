@@ -106,6 +106,8 @@ __device__ __forceinline__ bool cta_item(const DecodeParams& P, int& p, int& kvh
 // first position on (all of them without a window). Blocks between are never
 // read (their table entries may be released). The `total` blocks are numbered
 // 0 .. total-1 and cut into nparts partitions.
+// SINKS false: the call has none (those kernels carry no trace of them).
+template <bool SINKS>
 struct Span {
     int first_pos, blk_first, nblk, n_sink_blk, total, nparts;
     bool over;  // the context or its partitions exceed the call's bounds (clamped)
@@ -113,7 +115,7 @@ struct Span {
         nblk = (ctx + kBS - 1) / kBS;
         first_pos = P.window >= 0 ? max(0, ctx - 1 - P.window) : 0;
         blk_first = first_pos / kBS;
-        n_sink_blk = min((P.n_sinks + kBS - 1) / kBS, blk_first);
+        n_sink_blk = SINKS ? min((P.n_sinks + kBS - 1) / kBS, blk_first) : 0;
         total = n_sink_blk + nblk - blk_first;
         nparts = (total + P.part_blocks - 1) / P.part_blocks;
         over = nblk > P.max_blocks || nparts > P.max_parts;
@@ -127,12 +129,15 @@ struct Span {
         }
     }
     // the logical block of number i
-    __device__ __forceinline__ int block(int i) const { return i < n_sink_blk ? i : i - n_sink_blk + blk_first; }
+    __device__ __forceinline__ int block(int i) const {
+        return SINKS && i < n_sink_blk ? i : i - n_sink_blk + blk_first;
+    }
 };
 
 // Whether the query attends to position pos.
+template <bool SINKS>
 __device__ __forceinline__ bool visible(int pos, int ctx, int first_pos, int n_sinks) {
-    return pos < ctx && (pos >= first_pos || pos < n_sinks);
+    return pos < ctx && (pos >= first_pos || (SINKS && pos < n_sinks));
 }
 
 // A block-scaled cache's scale, within the range the library works with.
@@ -266,7 +271,7 @@ struct Chunk8<1> {
 // so the P.V product runs on the codes with one running reference m for loud
 // and quiet blocks alike, no output is ever rescaled for a scale, and the only
 // extra work is one multiply-add per score and one multiply per block.
-template <int D, int G, int LPT, int EB, bool BSC, int NW, int S, int MINB>
+template <int D, int G, int LPT, int EB, bool BSC, bool SINKS, int NW, int S, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB)
 pa_decode_partition_kernel(const DecodeParams P) {
     using SH = Shape<D, G, LPT, EB>;
@@ -300,7 +305,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
         }
         return;
     }
-    const Span sp(P, ctx);
+    const Span<SINKS> sp(P, ctx);
     if (sp.over && p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
     if (p >= sp.nparts) return;
     const int first_pos = sp.first_pos;
@@ -442,7 +447,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
 #pragma unroll
             for (int k = 0; k < NKEEP; ++k) {
                 const int t = (ip0 + k) * TPP + tg;
-                sc[k] = visible(tok0 + t, ctx, first_pos, P.n_sinks) ? scales.score(sc[k]) : -INFINITY;
+                sc[k] = visible<SINKS>(tok0 + t, ctx, first_pos, P.n_sinks) ? scales.score(sc[k]) : -INFINITY;
                 tmax = fmaxf(tmax, sc[k]);
             }
 #pragma unroll
@@ -490,7 +495,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
 #pragma unroll
             for (int ip = 0; ip < NPASS; ++ip) {
                 const int t = ip * TPP + tg;
-                if (visible(tok0 + t, ctx, first_pos, P.n_sinks)) {
+                if (visible<SINKS>(tok0 + t, ctx, first_pos, P.n_sinks)) {
 #pragma unroll
                     for (int j = 0; j < NCH; ++j) {
                         float2 vf[4];
@@ -692,7 +697,7 @@ __device__ __forceinline__ uint32_t sw_off(int row, int dims8) {
 
 }  // namespace mma
 
-template <int G, int EB, bool BSC>
+template <int G, int EB, bool BSC, bool SINKS>
 __global__ void __launch_bounds__(mma::kNW * 32, EB == 1 ? 4 : 3)
 pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
@@ -726,7 +731,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
         }
         return;
     }
-    const Span sp(P, ctx);
+    const Span<SINKS> sp(P, ctx);
     if (sp.over && p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
     if (p >= sp.nparts) return;
     const int first_pos = sp.first_pos;
@@ -869,7 +874,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
                 for (int u = 0; u < 4; ++u) {
                     const int pos = tok0 + g + 8 * (u >> 1);
                     const float s2 = BSC ? scales.score(sT[u]) : sT[u] * sc;
-                    sv[u] = visible(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
+                    sv[u] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
                 }
                 auto exps = [&]() {
 #pragma unroll
@@ -920,7 +925,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int pos = tok0 + 8 * n + 2 * t + k;
-                        sv[2 * n + k] = visible(pos, ctx, first_pos, P.n_sinks) ? s_acc[n][k] * sc : -INFINITY;
+                        sv[2 * n + k] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s_acc[n][k] * sc : -INFINITY;
                     }
                 float tmax = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
                 tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 1));
@@ -962,10 +967,10 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
             // V rows that the query does not see (past the context, before the
             // window) hold whatever the pool has there, and p = 0 must not meet
             // a NaN: zero them (E4M3: in registers, below)
-            if (EB == 2 && (ctx < tok0 + kBS || (tok0 < first_pos && tok0 + kBS > P.n_sinks))) {
+            if (EB == 2 && (ctx < tok0 + kBS || (tok0 < first_pos && (!SINKS || tok0 + kBS > P.n_sinks)))) {
                 unsigned char* vt = my_stages + (size_t)st * kStage + 4096;
                 for (int r = 0; r < kBS; ++r)
-                    if (!visible(tok0 + r, ctx, first_pos, P.n_sinks))  // a row: 2 boxes x 128 B
+                    if (!visible<SINKS>(tok0 + r, ctx, first_pos, P.n_sinks))  // a row: 2 boxes x 128 B
                         *reinterpret_cast<uint2*>(vt + (lane >> 4) * 2048 + r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
                 tc::fence_async_smem();  // before the stage's next TMA fill
                 __syncwarp();
@@ -991,8 +996,8 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
                 // the matching block of V^T, the A operand. Token rows that the
                 // query does not see are zero (p = 0 must not meet a NaN).
                 const unsigned char* rv = my_stages + (size_t)st * kStage + 2048;
-                const bool lo_ok = visible(tok0 + g, ctx, first_pos, P.n_sinks);
-                const bool hi_ok = visible(tok0 + g + 8, ctx, first_pos, P.n_sinks);
+                const bool lo_ok = visible<SINKS>(tok0 + g, ctx, first_pos, P.n_sinks);
+                const bool hi_ok = visible<SINKS>(tok0 + g + 8, ctx, first_pos, P.n_sinks);
 #pragma unroll
                 for (int mt = 0; mt < 8; ++mt) {
                     const int off = ((mt ^ (g & 7)) << 4) + 4 * t;  // rows g and g + 8 share the swizzle
@@ -1130,7 +1135,7 @@ pa_decode_merge_kernel(const DecodeParams P, int n_rows) {
     const int b = row / H;
     const int ctx = P.ctx[b];
     if (ctx <= 0) return;
-    const int nparts = Span(P, ctx).nparts;
+    const int nparts = Span<true>(P, ctx).nparts;
     if (nparts <= 1) return;  // the partition kernel wrote this row
     const size_t slot0 = (size_t)row * P.max_parts;
     float M, L;
@@ -1173,8 +1178,10 @@ pa_decode_merge_kernel(const DecodeParams P, int n_rows) {
 // The same for many partitions: D / 32 warps share a row, one dim a lane, and
 // 32 partitions' outputs are in flight at a time. The steps and their order are
 // those of the kernel above, so the bits are too. A few long sequences leave
-// that one short of loads: 4 sequences of 64 heads and 128 partitions took 22
-// us in it (256 warps, 16 rounds of memory latency each).
+// that one short of loads (4 sequences of 64 heads and 128 partitions: 256
+// warps, 16 rounds of memory latency each; decode and merge took 174 us, 164
+// with this one). Up to 16 partitions that one is as fast or faster (64
+// sequences of 32 heads: 0.4 us of 177).
 template <int D>
 __global__ void __launch_bounds__(128)
 pa_decode_merge_wide_kernel(const DecodeParams P, int n_rows) {
@@ -1186,7 +1193,7 @@ pa_decode_merge_wide_kernel(const DecodeParams P, int n_rows) {
     if (row >= n_rows) return;
     const int ctx = P.ctx[row / P.n_heads];
     if (ctx <= 0) return;
-    const int nparts = Span(P, ctx).nparts;
+    const int nparts = Span<true>(P, ctx).nparts;
     if (nparts <= 1) return;  // the partition kernel wrote this row
     const size_t slot0 = (size_t)row * P.max_parts;
     float M, L;
@@ -1227,11 +1234,11 @@ struct Launch {
     static constexpr int S = FP8_WIDE ? 2 : (D == 128 ? 2 : 4) * (MINB == 3 ? 1 : 3) / (MINB == 3 ? 1 : 2) * (2 / EB);
 };
 
-template <int D, int G, int EB, bool BSC>
+template <int D, int G, int EB, bool BSC, bool SINKS>
 int launch_partition(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     using LC = Launch<D, G, EB>;
     using SM = Smem<D, G, LC::LPT, EB, kNW, LC::S>;
-    auto kern = pa_decode_partition_kernel<D, G, LC::LPT, EB, BSC, kNW, LC::S, LC::MINB>;
+    auto kern = pa_decode_partition_kernel<D, G, LC::LPT, EB, BSC, SINKS, kNW, LC::S, LC::MINB>;
     static bool attr_done[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1245,22 +1252,22 @@ int launch_partition(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     return pa_launch_pdl(kern, grid, dim3(kNW * 32), SM::TOTAL, stream, P);
 }
 
-template <int D, int EB, bool BSC = false>
+template <int D, int EB, bool BSC, bool SINKS>
 int dispatch_group(int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_partition<D, 1, EB, BSC>(P, n_seqs, stream);
-        case 2: return launch_partition<D, 2, EB, BSC>(P, n_seqs, stream);
-        case 4: return launch_partition<D, 4, EB, BSC>(P, n_seqs, stream);
-        case 8: return launch_partition<D, 8, EB, BSC>(P, n_seqs, stream);
+        case 1: return launch_partition<D, 1, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 2: return launch_partition<D, 2, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 4: return launch_partition<D, 4, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 8: return launch_partition<D, 8, EB, BSC, SINKS>(P, n_seqs, stream);
         default: return PA_ERR_UNSUPPORTED;
     }
 }
 
 // The tensor-core partition kernel (head_dim 128, bf16 cache): K and V pools
 // as 2-D TMA maps of [num_blocks * n_kv_heads * 16 rows][128 dims].
-template <int G, int EB, bool BSC>
+template <int G, int EB, bool BSC, bool SINKS>
 int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
-    auto kern = pa_decode_mma_kernel<G, EB, BSC>;
+    auto kern = pa_decode_mma_kernel<G, EB, BSC, SINKS>;
     constexpr int kSmem = mma::Lay<EB>::kSmem;
     static bool attr_done[64] = {false};
     int dev = 0;
@@ -1281,15 +1288,22 @@ int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream)
     return pa_launch_pdl(kern, grid, dim3(mma::kNW * 32), kSmem, stream, P, tk, tv);
 }
 
-template <int EB, bool BSC = false>
+template <int EB, bool BSC, bool SINKS>
 int dispatch_group_mma(int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_partition_mma<1, EB, BSC>(P, n_seqs, stream);
-        case 2: return launch_partition_mma<2, EB, BSC>(P, n_seqs, stream);
-        case 4: return launch_partition_mma<4, EB, BSC>(P, n_seqs, stream);
-        case 8: return launch_partition_mma<8, EB, BSC>(P, n_seqs, stream);
+        case 1: return launch_partition_mma<1, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 2: return launch_partition_mma<2, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 4: return launch_partition_mma<4, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 8: return launch_partition_mma<8, EB, BSC, SINKS>(P, n_seqs, stream);
         default: return PA_ERR_UNSUPPORTED;
     }
+}
+
+template <int EB, bool BSC, bool SINKS>
+int dispatch_kernel(bool tensor, int head_dim, int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
+    if (tensor) return dispatch_group_mma<EB, BSC, SINKS>(G, P, n_seqs, stream);
+    return head_dim == 128 ? dispatch_group<128, EB, BSC, SINKS>(G, P, n_seqs, stream)
+                           : dispatch_group<64, EB, BSC, SINKS>(G, P, n_seqs, stream);
 }
 
 constexpr int kDefaultPartitionTokens = 512;
@@ -1478,22 +1492,18 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int st;
-    if (tensor) {
-        st = eb == 2 ? dispatch_group_mma<2>(G, P, n_seqs, s)
-             : block_scaled ? dispatch_group_mma<1, true>(G, P, n_seqs, s)
-                            : dispatch_group_mma<1>(G, P, n_seqs, s);
-    } else if (eb == 1 && block_scaled) {
-        st = head_dim == 128 ? dispatch_group<128, 1, true>(G, P, n_seqs, s)
-                             : dispatch_group<64, 1, true>(G, P, n_seqs, s);
-    } else if (eb == 1) {
-        st = head_dim == 128 ? dispatch_group<128, 1>(G, P, n_seqs, s) : dispatch_group<64, 1>(G, P, n_seqs, s);
-    } else {
-        st = head_dim == 128 ? dispatch_group<128, 2>(G, P, n_seqs, s) : dispatch_group<64, 2>(G, P, n_seqs, s);
-    }
+    if (block_scaled)  // one instantiation, with sinks
+        st = dispatch_kernel<1, true, true>(tensor, head_dim, G, P, n_seqs, s);
+    else if (n_sinks > 0)
+        st = eb == 2 ? dispatch_kernel<2, false, true>(tensor, head_dim, G, P, n_seqs, s)
+                     : dispatch_kernel<1, false, true>(tensor, head_dim, G, P, n_seqs, s);
+    else
+        st = eb == 2 ? dispatch_kernel<2, false, false>(tensor, head_dim, G, P, n_seqs, s)
+                     : dispatch_kernel<1, false, false>(tensor, head_dim, G, P, n_seqs, s);
     if (st != PA_OK || max_parts <= 1) return st;
     const int n_rows = n_seqs * n_heads;
     dim3 grid((n_rows + 3) / 4);
-    if (max_parts > 8) {  // more than one round of the kernel for few partitions
+    if (max_parts > 16) {  // more than two rounds of the kernel for few partitions
         if (head_dim == 128)
             return pa_launch_pdl(pa_decode_merge_wide_kernel<128>, dim3(n_rows), dim3(128), 0, s, P, n_rows);
         return pa_launch_pdl(pa_decode_merge_wide_kernel<64>, dim3((n_rows + 1) / 2), dim3(128), 0, s, P, n_rows);
