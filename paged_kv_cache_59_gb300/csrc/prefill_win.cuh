@@ -708,15 +708,19 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 ok = __all_sync(kFull, ok);
                 tc::fence_after_sync();
                 const int kb = keys.tile(g.kt0 + j) * kKT;
-                // Keys beyond a row's position are masked. Only the tiles on the
-                // diagonal have such keys; a warp takes the masking code only when
-                // one of its rows needs it (a warp-uniform branch), so the other
-                // tiles run the plain loop.
+                // A row does not see keys beyond its position or, sinks apart, before its window. A warp
+                // takes the masking code only for a tile where that hides a key from one of its rows (a
+                // warp-uniform branch): a tile or two at either end of a window, and that of the sinks.
+                // Key k of a quarter is bit k of the quarter's mask: two instructions an element (as
+                // three comparisons, a masked tile took twice a plain one's time).
                 const int lim0 = pos - kb;  // keys k > lim0 of the tile are not visible
-                // nor keys k < lim1, sinks (k < sink1) apart
-                const int lim1 = P.window >= 0 ? lim0 - P.window : 0, sink1 = P.n_sinks - kb;
+                const int lim1 = P.window >= 0 ? lim0 - P.window : 0, sink1 = P.n_sinks - kb;  // nor k < lim1, k >= sink1
                 const bool mask_warp = __any_sync(kFull, lim0 < kKT - 1 || (lim1 > 0 && sink1 < kKT));
-                auto is_visible = [&](int k) { return k <= lim0 && (k >= lim1 || k < sink1); };
+                auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };  // bits 0 .. n-1
+                auto visible_of = [&](int qd) {
+                    const int k0 = 32 * qd;
+                    return below(lim0 + 1 - k0) & (~below(lim1 - k0) | below(sink1 - k0));
+                };
                 float2 psum2 = make_float2(0.f, 0.f);  // this tile's sum of p against m_used
                 float alpha = 1.f;                     // this tile's rescale of l and O
                 const float2 sc2 = make_float2(sc, sc);
@@ -726,7 +730,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 // Returns the quarter's sum of p; `add` is what it adds to the row's sum
                 // (E4M3: each block's sum over its V scale).
                 float qk[2] = {sc, sc}, qe[2] = {0.f, 0.f}, qi[2] = {1.f, 1.f};  // E4M3: the quarter's two blocks
-                auto exps = [&](auto masked, const uint32_t (&raw)[32], int qd, uint32_t (&ph)[16], float& add) {
+                auto exps = [&](auto masked, const uint32_t (&raw)[32], uint32_t visible, uint32_t (&ph)[16], float& add) {
                     float2 qs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
@@ -735,9 +739,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])),
                                               EB == 1 ? make_float2(qk[b], qk[b]) : sc2, make_float2(nm, nm));
                         if constexpr (decltype(masked)::value) {  // masked keys give p = 0 (also for a zero scale)
-                            const int k = 32 * qd + 2 * w;
-                            if (!is_visible(k)) e.x = -INFINITY;
-                            if (!is_visible(k + 1)) e.y = -INFINITY;
+                            if (!(visible & (1u << (2 * w)))) e.x = -INFINITY;
+                            if (!(visible & (1u << (2 * w + 1)))) e.y = -INFINITY;
                         }
                         e.x = pa::fast_exp2(e.x);
                         e.y = pa::fast_exp2(e.y);
@@ -764,9 +767,10 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                 qi[b] = __shfl_sync(kFull, my_inv, 2 * qd + b);
                             }
                         }
+                        const uint32_t visible = decltype(masked)::value ? visible_of(qd) : 0xffffffffu;
                         uint32_t ph[16];
                         float add;
-                        const float qs = exps(masked, raw, qd, ph, add);
+                        const float qs = exps(masked, raw, visible, ph, add);
                         const bool big = !(qs <= 32768.f);  // also inf (no reference yet) and NaN
                         if (__any_sync(kFull, big)) {
                             // rare: a new reference for the rows that need one
@@ -775,7 +779,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                 float qmax = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
-                                    const bool vis = !decltype(masked)::value || is_visible(32 * qd + k);
+                                    const bool vis = !decltype(masked)::value || (visible & (1u << k));
                                     const float r = __uint_as_float(raw[k]);
                                     if (vis) qmax = fmaxf(qmax, EB == 1 ? fmaf(r, qk[k >> 4], qe[k >> 4]) : r);
                                 }
@@ -785,7 +789,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                     const float d = m_used - mq;
                                     a = d < -126.f ? 0.f : __int_as_float(((int)d + 127) << 23);
                                     m_used = mq;
-                                    exps(masked, raw, qd, ph, add);
+                                    exps(masked, raw, visible, ph, add);
                                 }
                             }
                             psum2.x *= a;
