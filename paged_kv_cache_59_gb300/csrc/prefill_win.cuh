@@ -694,12 +694,11 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             }
             for (int j = 0; j < g.n_kt; ++j) {
                 const int J = J0 + j;
-                float my_k = 0.f, my_e = 0.f, my_inv = 0.f;
+                float my_k = 0.f, my_e = 0.f;
                 if constexpr (EB == 1) {  // the approximate log2 and reciprocal are off by 2^-22, far below w's rounding
                     const float vs = clamp_scale(vs_next);
                     my_k = clamp_scale(ks_next) * sc;
                     my_e = __log2f(vs);
-                    my_inv = __fdividef(1.f, vs);
                     ks_next = scale_of(P.k_scale, bid_next);
                     vs_next = scale_of(P.v_scale, bid_next);
                     bid_next = block_id(j + 2);
@@ -764,7 +763,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             for (int b = 0; b < 2; ++b) {
                                 qk[b] = __shfl_sync(kFull, my_k, 2 * qd + b);
                                 qe[b] = __shfl_sync(kFull, my_e, 2 * qd + b);
-                                qi[b] = __shfl_sync(kFull, my_inv, 2 * qd + b);
+                                qi[b] = pa::fast_exp2(-qe[b]);
                             }
                         }
                         const uint32_t visible = decltype(masked)::value ? visible_of(qd) : 0xffffffffu;
