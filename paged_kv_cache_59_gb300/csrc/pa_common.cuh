@@ -134,6 +134,28 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
     }
 }
 
+// The same for one role of several in a kernel: it also gives up once another
+// role has (*abort_flag), tells the others when its own time is up, and sleeps
+// between polls (up to 20 us a poll, woken when the phase completes), so that
+// waiting warps take no issue slots from busy ones.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsigned int* err,
+                                          volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+        if ((it & 15u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > PA_WAIT_LIMIT_NS) {
+                set_error(err, PA_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------- bulk async copies
 // 1-D bulk copy global -> shared (this CTA), completion signalled on `bar`
 // as transaction bytes. dst/src 16-byte aligned, bytes a multiple of 16.

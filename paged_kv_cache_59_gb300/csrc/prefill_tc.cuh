@@ -1,5 +1,5 @@
-// What the chunked prefill's kernels share: parameters, shared-memory layout,
-// key tiles, waits, and the merge of a query-tile pair's pieces. The kernel for
+// What the chunked prefill's kernels share: parameters, key tiles and the merge
+// of a query-tile pair's pieces. The kernel for
 // a bf16 cache without a window is in prefill.cu, with its design; those for a
 // window with sinks and for a block-scaled E4M3 cache are in prefill_win.cuh.
 #pragma once
@@ -57,29 +57,6 @@ constexpr int kKT = 128;         // keys per key tile
 constexpr int kBPT = kKT / kBS;  // blocks per key tile
 constexpr int kRows = 128;       // MMA M
 constexpr unsigned kFull = 0xffffffffu;
-
-constexpr int kKS = 2;  // K tile stages
-constexpr int kVS = 3;  // V tile stages
-constexpr int kThreads = 448;  // 8 softmax warps, MMA warp (8), producer (9), 4 converter warps (10..13)
-// Shared memory map for head_dim D (64 or 128): a Q tile (128 rows) and a
-// K or V tile (128 keys) are 128 x D bf16 values each, stored as D / 64
-// 128B-swizzled halves of 64 dims (16 KiB each). The dynamic shared memory
-// base must be 1024-byte aligned (swizzle atoms of TMA and of the matrix
-// descriptors): checked.
-template <int D>
-struct PfLay {
-    static_assert(D == 64 || D == 128, "head_dim 64 or 128");
-    static constexpr int kHalves = D / 64;               // 64-dim halves of a row
-    static constexpr uint32_t kTile = kKT * D * 2;       // K or V tile bytes
-    static constexpr uint32_t kQTile = kRows * D * 2;    // Q tile bytes
-    static constexpr uint32_t kQ = 0;                    // Q_A, Q_B
-    static constexpr uint32_t kK0 = 2 * kQTile;          // K stages
-    static constexpr uint32_t kV0 = kK0 + kKS * kTile;   // V stages
-    static constexpr uint32_t kBars = kV0 + kVS * kTile; // mbarriers
-    static constexpr uint32_t kMisc = kBars + 256;       // tmem slot, abort flag, segment entries
-    static constexpr uint32_t kSmem = kMisc + 64;
-    static_assert(kSmem <= 227 * 1024, "shared memory budget");
-};
 constexpr uint32_t kTmemCols = 512;  // tile X: S at 256X, O at 256X + 128 (D columns)
 
 using PrefillParams = PaPrefillParams;
@@ -140,27 +117,6 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
     return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// Bounded wait (1 s) that also gives up once another role has aborted. A
-// waiting thread sleeps inside try_wait (up to 20 us per try, woken when the
-// phase completes), so idle roles take no issue slots from busy ones.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, unsigned int* err,
-                                         volatile int* abort_flag) {
-    if (pa::mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    const uint64_t t0 = pa::globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (pa::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-        if ((it & 15u) == 0) {
-            if (*abort_flag) return false;
-            if (pa::globaltimer_ns() - t0 > PA_WAIT_LIMIT_NS) {
-                pa::set_error(err, PA_DEVERR_TIMEOUT);
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
 }
 
 // Key tiles of item it = (sequence * n_kv_heads + kv head) * n_qp + pair:

@@ -16,9 +16,18 @@
 // phases go on from one segment to the next. While the softmax warps work on a
 // segment's last tile and write its output, the producer loads the next
 // segment's K and V, and the converter warps its Q as soon as the last Q.K^T has
-// read the old one; the tensor core then starts on it at once. Measured (2,048
-// rows, 32/8 heads of 128, window 4,096 + 4 sinks, 256 items of 35 tiles):
-// WIN_FIGURES
+// read the old one; the tensor core then starts on it at once.
+//
+// Measured (32/8 heads of 128, 19 pairs a KV head, so one item a CTA): 1.67 us a
+// key tile in bf16 (1,530 TFLOP/s of its two tiles' four products over 152 SMs,
+// 0.79 of a cuBLAS burst) and 1.78 with E4M3, and 14 us a call beside the tiles:
+// the plan and launches 7, the first tile's loads, softmax and the epilogue 7.
+// What bounds the tile loop: S and P share 128 of the 512 tensor-memory columns
+// for each of the two query tiles, so a tile's Q.K^T cannot start before its
+// last P.V, and the tensor core waits for a softmax about a fifth of the time.
+// 2,048 rows, window 4,096 + 4 sinks (256 items of 35 tiles on 152 SMs): 129 us,
+// 1,065 TFLOP/s of visible pairs; 179 us with whole waves, cut tails and a
+// block-wide barrier between segments.
 //
 // E4M3 (EB = 1). The codes of a K and of a V tile (half the bytes) land in a
 // buffer each, and the converter warps widen both to fp16, exactly; Q is
@@ -322,7 +331,9 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
         }
         pa::fence_mbar_init();
     }
-    if (warp == 0) {
+    pa::launch_dependents();     // the next kernel may be scheduled
+    pa::grid_dependency_wait();  // the plan, and whatever wrote q and the cache, is complete
+    if (warp == 0) {  // only now: tensor memory is not held while waiting for another kernel
         tc::tmem_alloc(tslot, kTmemCols);
         tc::tmem_relinquish();
     }
@@ -330,8 +341,6 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tbase = *tslot;
-    pa::launch_dependents();     // the next kernel may be scheduled
-    pa::grid_dependency_wait();  // the plan, and whatever wrote q and the cache, is complete
     Segments<G> segments(P);
     Segment g;
     bool ok = true;  // after a failed wait a role goes on without waiting, so that no other role is left alone
@@ -390,7 +399,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     in = false;
                 }
                 const int y = in ? (bid * Hk + g.kvh) * kBS : P.oob_row;  // out of range: zero fill
-                ok = __all_sync(kFull, wait_bar(r.free + r.st, (uint32_t)r.ph, P.err, abort_flag));
+                ok = __all_sync(kFull, pa::mbar_wait(r.free + r.st, (uint32_t)r.ph, P.err, abort_flag));
                 if (!ok) return;
                 if (lane == 0) pa::mbar_arrive_expect_tx(r.full + r.st, kBytes);
                 __syncwarp();
@@ -451,7 +460,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
         };
         int kst = 0, kph = 0, vst = 0, vph = 0;  // next K and V stage, phase parity
         auto k_ready = [&]() {
-            return wait_bar(EB == 2 ? bars.k_full(kst) : bars.k_conv(kst), (uint32_t)kph, P.err, abort_flag);
+            return pa::mbar_wait(EB == 2 ? bars.k_full(kst) : bars.k_conv(kst), (uint32_t)kph, P.err, abort_flag);
         };
         auto k_next = [&]() {
             if (++kst == kKS) {
@@ -460,7 +469,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             }
         };
         for (int n_seg = 0; segments.next(g); ++n_seg) {
-            if (ok) ok = wait_bar(bars.q_full(), (uint32_t)(n_seg & 1), P.err, abort_flag);
+            if (ok) ok = pa::mbar_wait(bars.q_full(), (uint32_t)(n_seg & 1), P.err, abort_flag);
             if (ok) ok = k_ready();
             ok = __all_sync(kFull, ok);
             if (ok && lane == 0) {
@@ -473,7 +482,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             k_next();
             for (int j = 0; j < g.n_kt; ++j) {
                 const bool more = j + 1 < g.n_kt;
-                if (ok) ok = wait_bar(bars.v_conv(vst), (uint32_t)vph, P.err, abort_flag);
+                if (ok) ok = pa::mbar_wait(bars.v_conv(vst), (uint32_t)vph, P.err, abort_flag);
                 if (ok && more) ok = k_ready();
                 ok = __all_sync(kFull, ok);
                 asm volatile("bar.sync 1, 160;" ::: "memory");  // tile A's P is in tensor memory
@@ -550,7 +559,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 uint4 v[8];
 #pragma unroll
                 for (int p = 0; p < 8; ++p) v[p] = fetch(0, p);
-                if (n_seg > 0) ok = wait_bar(bars.q_free(), (uint32_t)((n_seg - 1) & 1), P.err, abort_flag);
+                if (n_seg > 0) ok = pa::mbar_wait(bars.q_free(), (uint32_t)((n_seg - 1) & 1), P.err, abort_flag);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
 #pragma unroll
@@ -572,7 +581,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 };
                 for (int j = 0; j < g.n_kt; ++j) {
                     const int J = J0 + j, st = J % kVS, kb = keys.tile(g.kt0 + j) * kKT;
-                    ok = wait_bar(bars.v_full(st), (uint32_t)((J / kVS) & 1), P.err, abort_flag);
+                    ok = pa::mbar_wait(bars.v_full(st), (uint32_t)((J / kVS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     uint4* vs = reinterpret_cast<uint4*>(sm + L_::kV0 + st * kTile);
@@ -642,14 +651,14 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 };
                 for (int j = 0; j < g.n_kt; ++j) {
                     const int J = J0 + j, kb = keys.tile(g.kt0 + j) * kKT, ks = J % kKS, vs = J % kVS;
-                    ok = wait_bar(bars.k_full(0), (uint32_t)(J & 1), P.err, abort_flag);
-                    if (ok && J >= kKS) ok = wait_bar(bars.k_free(ks), (uint32_t)(((J - kKS) / kKS) & 1), P.err, abort_flag);
+                    ok = pa::mbar_wait(bars.k_full(0), (uint32_t)(J & 1), P.err, abort_flag);
+                    if (ok && J >= kKS) ok = pa::mbar_wait(bars.k_free(ks), (uint32_t)(((J - kKS) / kKS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     widen(0, sm + L_::kK0 + ks * kTile, kb);
                     if (lane == 0) pa::mbar_arrive(bars.k_conv(ks));
-                    ok = wait_bar(bars.v_full(0), (uint32_t)(J & 1), P.err, abort_flag);
-                    if (ok && J >= kVS) ok = wait_bar(bars.v_free(vs), (uint32_t)(((J - kVS) / kVS) & 1), P.err, abort_flag);
+                    ok = pa::mbar_wait(bars.v_full(0), (uint32_t)(J & 1), P.err, abort_flag);
+                    if (ok && J >= kVS) ok = pa::mbar_wait(bars.v_free(vs), (uint32_t)(((J - kVS) / kVS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     widen(1, sm + L_::kV0 + vs * kTile, kb);
@@ -703,7 +712,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     vs_next = scale_of(P.v_scale, bid_next);
                     bid_next = block_id(j + 2);
                 }
-                if (ok) ok = wait_bar(bars.s_full(x), (uint32_t)(J & 1), P.err, abort_flag);
+                if (ok) ok = pa::mbar_wait(bars.s_full(x), (uint32_t)(J & 1), P.err, abort_flag);
                 ok = __all_sync(kFull, ok);
                 tc::fence_after_sync();
                 const int kb = keys.tile(g.kt0 + j) * kKT;
@@ -780,9 +789,9 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                 for (int k = 0; k < 32; ++k) {
                                     const bool vis = !decltype(masked)::value || (visible & (1u << k));
                                     const float r = __uint_as_float(raw[k]);
-                                    if (vis) qmax = fmaxf(qmax, EB == 1 ? fmaf(r, qk[k >> 4], qe[k >> 4]) : r);
+                                    if (vis) qmax = fmaxf(qmax, EB == 1 ? fmaf(r, qk[k >> 4], qe[k >> 4]) : r * sc);
                                 }
-                                const float mq = ceilf(EB == 1 ? qmax : qmax * sc);
+                                const float mq = ceilf(qmax);
                                 if (mq > m_used) {
                                     // 2^(m_used - mq) built from its exponent bits (0 below 2^-126)
                                     const float d = m_used - mq;
@@ -822,7 +831,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 l = l * alpha + (psum2.x + psum2.y);
                 // a new reference rescales O_x: PV_x(j-1) must have landed first
                 if (j > 0 && __any_sync(kFull, alpha != 1.f)) {
-                    if (ok) ok = wait_bar(bars.pv_done(x), (uint32_t)((J - 1) & 1), P.err, abort_flag);
+                    if (ok) ok = pa::mbar_wait(bars.pv_done(x), (uint32_t)((J - 1) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     tc::fence_after_sync();
 #pragma unroll 1
@@ -842,7 +851,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             }
             tc::tmem_wait_st();  // no store may be pending when the columns are released
             more = segments.next(after);
-            if (ok) ok = wait_bar(bars.pv_done(x), (uint32_t)((J0 + g.n_kt - 1) & 1), P.err, abort_flag);
+            if (ok) ok = pa::mbar_wait(bars.pv_done(x), (uint32_t)((J0 + g.n_kt - 1) & 1), P.err, abort_flag);
             ok = __all_sync(kFull, ok);
             J0 += g.n_kt;
             if (!ok) continue;

@@ -434,7 +434,7 @@ int launch(RopeParams& P, cudaStream_t stream) {
     const int n_rows = MODE == kBlockScale ? P.n_heads : P.n_heads + 2 * P.n_kv_heads;
     // one row a thread while that still fits in one wave of 16 CTAs per SM;
     // beyond it eight, which read a token's angles an eighth as often
-    const bool large = tiles * n_rows > 16LL * sms;
+    const bool large = tiles * (P.n_heads + 2LL * P.n_kv_heads) > 16LL * sms;
     P.rows_per_thread = large ? 8 : 1;
     P.row_groups = (n_rows + P.rows_per_thread - 1) / P.rows_per_thread;
     long long ctas = tiles * P.row_groups, kv = 0;

@@ -57,8 +57,8 @@ def run(pk, c, q, pt=0, stream=None):
     return host_bits(out)
 
 
-def check(pk, c, H, D, seed, pt=0, what=""):
-    c.scale = D ** -0.5
+def check(pk, c, H, D, seed, pt=0, what="", scale=None):
+    c.scale = D ** -0.5 if scale is None else scale
     q = f32_to_bf16_bits(np.random.default_rng(seed).standard_normal((len(c.ctx), H, D)).astype(np.float32))
     ref = paged_decode(q, c.k, c.v, c.tables, c.ctx, c.scale, c.window, c.n_sinks, **c.scales())
     got = run(pk, c, q, pt)
@@ -96,6 +96,27 @@ def test_extreme_block_scales(pk, D, H, Hk):
     c.v_scale = np.exp2(rng.integers(-20, 21, (nb, Hk))).astype(np.float32)
     c.k_scale = (c.k_scale * np.exp2(rng.integers(-12, 1, (nb, Hk)))).astype(np.float32)
     check(pk, c, H, D, 6)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0884])
+def test_zero_and_negative_softmax_scales(pk, scale):
+    for kind in ("bf16", "head", "block"):
+        for D, H, Hk in [(128, 8, 2), (64, 8, 8), (128, 8, 1)]:
+            check(pk, Cache(4, kind, [300, 90, 1], Hk, D, 100, 5), H, D, 8, 64, kind, scale)
+
+
+def test_float8_pools_are_taken_as_they_are(pk):
+    torch = torch_cuda()
+    c = Cache(18, "block", [100, 700], 2, 128)
+    c.scale = 128 ** -0.5
+    q = f32_to_bf16_bits(np.random.default_rng(2).standard_normal((2, 8, 128)).astype(np.float32))
+    want = run(pk, c, q)
+    k, v = (dev(x).view(torch.float8_e4m3fn) for x in (c.k, c.v))
+    qd = dev(q).view(torch.bfloat16)
+    out = torch.empty_like(qd)
+    pk.pa_decode_fp8_block(out, qd, k, v, dev(c.k_scale), dev(c.v_scale), dev(c.tables), dev(c.ctx), c.scale, 700,
+                           workspace=pk.decode_workspace(qd, 700))
+    assert np.array_equal(host_bits(out), want)
 
 
 def test_uniform_scales_equal_head_scales_bit_for_bit(pk):

@@ -59,8 +59,8 @@ def run(pk, c, q, chunk, splits, max_chunk=None):
     return host_bits(out)
 
 
-def check(pk, c, H, D, chunk, splits, what=""):
-    c.scale = D ** -0.5
+def check(pk, c, H, D, chunk, splits, what="", scale=None):
+    c.scale = D ** -0.5 if scale is None else scale
     q = f32_to_bf16_bits(np.random.default_rng(H + D).standard_normal((sum(chunk), H, D)).astype(np.float32))
     ref = paged_prefill(q, c.k, c.v, c.tables, c.ctx, start_loc(chunk), c.scale, c.window, c.n_sinks, **c.scales())
     vm = max(np.nanmax(np.abs(dense_kv(c.v, c.v_scale, c.tables[b], int(n)))) for b, n in enumerate(c.ctx) if chunk[b] > 0)
@@ -96,6 +96,13 @@ def test_many_segments_per_cta(pk):
     for kind, window, sinks in (("bf16", 200, 4), ("block", -1, 0), ("block", 77, 130)):
         c = Cache(3, kind, [700, 257, 900, 400, 1000, 650], 16, 64, window, sinks, chunk)
         check(pk, c, 16, 64, chunk, 0, f"{kind}")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0884])
+def test_zero_and_negative_softmax_scales(pk, scale):
+    for kind, D in (("bf16", 128), ("block", 128), ("bf16", 64), ("block", 64)):
+        c = Cache(4, kind, [300, 90], 2, D, 100, 5, [70, 90])
+        check(pk, c, 4, D, [70, 90], 0, kind, scale)
 
 
 def test_extreme_block_scales(pk):
