@@ -310,8 +310,8 @@ def _decode_call(fn: str, per_block: bool, out, q, k_pool, v_pool, k_scale, v_sc
                  max_context_len, window, n_sinks, workspace, partition_tokens, stream) -> None:
     dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale, per_block,
                                                            block_tables, context_lens, q.shape[0])
-    _call(fn, dev, stream, *data, *tables, scale, *sizes, max_context_len, num_blocks, window, n_sinks,
-          partition_tokens, *_workspace(workspace, dev))
+    _call(fn, dev, stream, *data, *tables, float(scale), *sizes, int(max_context_len), num_blocks, int(window),
+          int(n_sinks), int(partition_tokens), *_workspace(workspace, dev))
 
 
 def pa_decode_sinks(out, q, k_pool, v_pool, block_tables, context_lens, scale: float, max_context_len: int,
@@ -614,7 +614,8 @@ def _prefill_call(fn: str, per_block: bool, out, q, k_pool, v_pool, k_scale, v_s
     dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale, per_block,
                                                            block_tables, context_lens, n_seqs)
     _call(fn, dev, stream, *(data if per_block else data[:4]), *tables, _at(q_start_loc, "q_start_loc", _Types.i32, dev),
-          scale, *sizes, max_chunk_len, num_blocks, window, n_sinks, splits, *_workspace(workspace, dev))
+          float(scale), *sizes, int(max_chunk_len), num_blocks, int(window), int(n_sinks), int(splits),
+          *_workspace(workspace, dev))
 
 
 def pa_prefill_sinks(out, q, k_pool, v_pool, block_tables, context_lens, q_start_loc, scale: float, max_chunk_len: int,
