@@ -78,7 +78,10 @@ enum pa_device_error {
     PA_DEVERR_PAIR = 8,     /* a copy_blocks pair outside the pool */
     PA_DEVERR_CONTEXT = 16, /* a context length beyond 16*max_blocks_per_seq or
                                max_context_len (the excess is not attended), or a
-                               prefill chunk longer than its context */
+                               prefill chunk longer than its context; under a
+                               window with sinks or over block-scaled E4M3 also a
+                               prefill context beyond its table or a chunk beyond
+                               max_chunk_len (the sequence is left out) */
     PA_DEVERR_LAYOUT = 32,  /* the shared-memory base was not 1024-byte aligned
                                (prefill; nothing computed) */
     PA_DEVERR_RANGE = 64,   /* a prefill output (or split partial) was not finite:

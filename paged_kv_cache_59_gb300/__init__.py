@@ -310,8 +310,9 @@ def _decode_call(fn: str, per_block: bool, out, q, k_pool, v_pool, k_scale, v_sc
                  max_context_len, window, n_sinks, workspace, partition_tokens, stream) -> None:
     dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale, per_block,
                                                            block_tables, context_lens, q.shape[0])
-    _call(fn, dev, stream, *data, *tables, float(scale), *sizes, int(max_context_len), num_blocks, int(window),
-          int(n_sinks), int(partition_tokens), *_workspace(workspace, dev))
+    longest, window, n_sinks, partition_tokens = _ints(max_context_len, window, n_sinks, partition_tokens)
+    _call(fn, dev, stream, *data, *tables, float(scale), *sizes, longest, num_blocks, window, n_sinks, partition_tokens,
+          *_workspace(workspace, dev))
 
 
 def pa_decode_sinks(out, q, k_pool, v_pool, block_tables, context_lens, scale: float, max_context_len: int,
@@ -451,6 +452,14 @@ def _call(fn: str, dev: int, stream, *args) -> None:
     st = getattr(_capi._lib or load(), fn)(*args, _Types.raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         check(fn, st)
+
+
+def _ints(*values):
+    """The values as C ints (a larger one would be cut to its low 32 bits)."""
+    values = [int(x) for x in values]
+    if max(values) >= 2 ** 31 or min(values) < -2 ** 31:
+        raise ValueError(f"a size, window or count does not fit 32 bits: {values}")
+    return values
 
 
 def _workspace(t, dev: int):
@@ -613,9 +622,9 @@ def _prefill_call(fn: str, per_block: bool, out, q, k_pool, v_pool, k_scale, v_s
         raise ValueError("q_start_loc must have n_seqs + 1 entries")
     dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale, per_block,
                                                            block_tables, context_lens, n_seqs)
+    longest, window, n_sinks, splits = _ints(max_chunk_len, window, n_sinks, splits)
     _call(fn, dev, stream, *(data if per_block else data[:4]), *tables, _at(q_start_loc, "q_start_loc", _Types.i32, dev),
-          float(scale), *sizes, int(max_chunk_len), num_blocks, int(window), int(n_sinks), int(splits),
-          *_workspace(workspace, dev))
+          float(scale), *sizes, longest, num_blocks, window, n_sinks, splits, *_workspace(workspace, dev))
 
 
 def pa_prefill_sinks(out, q, k_pool, v_pool, block_tables, context_lens, q_start_loc, scale: float, max_chunk_len: int,

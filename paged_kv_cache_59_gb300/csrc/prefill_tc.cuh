@@ -119,9 +119,19 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_majo
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Whether a sequence of L > 0 rows is left out and flagged: its chunk is not in
+// the cache yet, or (calls with a window or over E4M3) its context runs past its
+// table or its chunk past max_chunk_len.
+template <int G>
+__device__ __forceinline__ bool left_out(const PrefillParams& P, int L, int ctx) {
+    constexpr int QT = kRows / G;
+    if (ctx < L) return true;
+    return (P.window >= 0 || P.k_scale) && ((ctx - 1) / kBS >= P.max_blocks || (L - 1) / (2 * QT) >= P.n_qp);
+}
+
 // Key tiles of item it = (sequence * n_kv_heads + kv head) * n_qp + pair:
-// 0 if the pair has no rows. A chunk that is not in the cache (ctx < L) has
-// none either, and flags the device error once per sequence.
+// 0 if the pair has no rows. A sequence that is left out has none either, and
+// flags the device error once.
 template <int G>
 __device__ int item_tiles(const PrefillParams& P, int it) {
     constexpr int QT = kRows / G;
@@ -130,7 +140,7 @@ __device__ int item_tiles(const PrefillParams& P, int it) {
     const int q0 = P.qsl[s], L = P.qsl[s + 1] - q0, i0 = qp * 2 * QT;
     if (i0 >= L) return 0;
     const int ctx = P.ctx[s];
-    if (ctx < L) {
+    if (left_out<G>(P, L, ctx)) {
         if (it % per_seq == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
         return 0;
     }
@@ -266,8 +276,9 @@ pa_prefill_merge_kernel(const PrefillParams P, int n_seqs, int n_rows_total, int
     const int s = lo;
     const int q0 = P.qsl[s], L = P.qsl[s + 1] - q0, ctx = P.ctx[s];
     const int i = t - q0;
-    if (i < 0 || i >= L || ctx < L) return;
+    if (i < 0 || i >= L || left_out<G>(P, L, ctx)) return;
     const int qp = i / (2 * QT), x = (i % (2 * QT)) / QT, r = (i % QT) * G + h % G, kvh = h / G;
+    if (qp >= n_qp) return;  // a chunk beyond max_chunk_len: no partials
     const int i0 = qp * 2 * QT;
     const int n_kt_all = KeyTiles(P, ctx - L + i0, ctx - L + min(i0 + 2 * QT, L) - 1).n;
     const size_t item = ((size_t)s * Hk + kvh) * n_qp + qp;

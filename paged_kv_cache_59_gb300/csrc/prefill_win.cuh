@@ -111,7 +111,7 @@ struct Segments {
             if (!P.work) {
                 constexpr int QT = kRows / G;
                 if (g.qp * 2 * QT >= g.L) continue;
-                if (g.ctx < g.L) {  // the chunk must be in the cache already
+                if (left_out<G>(P, g.L, g.ctx)) {
                     if (threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
                     continue;
                 }

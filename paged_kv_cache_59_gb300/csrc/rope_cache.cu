@@ -383,7 +383,7 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
 // rows in flight. A large one is bound by HBM (K/V warps: by latency) and wants
 // warps: 80 registers, or 64 and two rows in flight for the block-scaled
 // cache, whatever spills. Measured small / large (64 / 8,192 tokens of 64/8
-// heads of 128 in bf16; 64 tokens / 7,377 in ragged chunks of 32/8 heads in
+// heads of 128 in bf16; 64 tokens / 6,742 in ragged chunks of 32/8 heads in
 // E4M3): 2.2 / 54.1 us and 2.9 / 35.4 us in the first form, 2.4 / 52.6 and 3.8 /
 // 30.8 in the second.
 template <int MODE, bool LARGE>
@@ -441,7 +441,7 @@ int launch(RopeParams& P, cudaStream_t stream) {
     if (MODE == kBlockScale) {
         const long long units = 2LL * P.n_kv_heads;
         // K/V warps look at one token each while that is one wave of them. Beyond it a warp
-        // takes several: 16 suit prompt chunks (30.8 us against 34.2 with 4 for 7,377 tokens),
+        // takes several: 16 suit prompt chunks (30.8 us against 34.2 with 4 for 6,742 tokens),
         // where a warp finds one run, but a decode batch has a run per token and its warps
         // would work through 16 (2,048 sequences: 39.9 us against 22.6), so calls that can
         // still be one take 4.

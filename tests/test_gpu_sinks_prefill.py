@@ -90,8 +90,8 @@ def test_block_scaled_full_context(pk, D, H, Hk, splits, spread):
 
 
 def test_many_segments_per_cta(pk):
-    """More query-tile pairs than SMs: the persistent CTAs run several segments
-    with their barriers re-initialised."""
+    """More query-tile pairs than SMs: the persistent CTAs run several segments,
+    barrier phases going on from one to the next."""
     chunk = [129, 257, 64, 300, 1, 500]
     for kind, window, sinks in (("bf16", 200, 4), ("block", -1, 0), ("block", 77, 130)):
         c = Cache(3, kind, [700, 257, 900, 400, 1000, 650], 16, 64, window, sinks, chunk)
@@ -200,6 +200,27 @@ def test_flags(pk):
     assert (got[20:] == 0x7FC0).all() and (got[:20] != 0x7FC0).any()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "block"])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_sequences_beyond_the_calls_bounds_are_left_out(pk, kind, splits):
+    """A context that its table does not hold, a chunk beyond max_chunk_len:
+    flagged, its rows left as they were, the others' unchanged."""
+    chunk = [20, 5, 70]
+    c = Cache(8, kind, [300, 40, 100], 2, 64, 120, 3, chunk)
+    c.scale = 0.125
+    q = f32_to_bf16_bits(np.random.default_rng(3).standard_normal((95, 16, 64)).astype(np.float32))
+    want = run(pk, c, q, chunk, splits)
+    check_device_error(0)
+    tables, c.tables = c.tables, c.tables[:, :18].copy()  # of 19 blocks
+    got = run(pk, c, q, chunk, splits)
+    check_device_error(16)
+    assert (got[:20] == 0x7FC0).all() and np.array_equal(got[20:], want[20:])
+    c.tables = tables
+    got = run(pk, c, q, chunk, splits, max_chunk=64)  # pairs of 32 rows: the third chunk has 70
+    check_device_error(16)
+    assert (got[25:] == 0x7FC0).all() and np.array_equal(got[:25], want[:25])
+
+
 def test_captured_and_replayed_and_two_streams(pk):
     torch = torch_cuda()
     chunk = [90, 200, 33]
@@ -229,6 +250,24 @@ def test_captured_and_replayed_and_two_streams(pk):
                     call(pk, c, qd, chunk, 0, outs[i], spaces[i], t)
         torch.cuda.synchronize()
         assert all(np.array_equal(host_bits(o), want) for o in outs)
+    check_device_error(0)
+
+
+def test_numbers_beyond_32_bits_are_refused(pk):
+    torch = torch_cuda()
+    chunk = [4]
+    c = Cache(17, "block", [100], 2, 128, chunk=chunk)
+    q = torch.zeros((4, 8, 128), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    k, v, ks, vs, tab, ctx, loc = tensors_of(c, chunk)
+    one = torch.zeros((1, 8, 128), dtype=torch.bfloat16, device="cuda")
+    for bad in (2 ** 32, 2 ** 31, -2 ** 31 - 1, 2 ** 32 + 5):
+        for over in (dict(window=bad), dict(window=5, n_sinks=bad), dict(splits=bad)):
+            with pytest.raises(ValueError):
+                pk.pa_prefill_fp8_block(out, q, k, v, ks, vs, tab, ctx, loc, 0.1, 4, **{"splits": 1, **over})
+        for over in (dict(window=bad), dict(window=5, n_sinks=bad), dict(partition_tokens=bad)):
+            with pytest.raises(ValueError):
+                pk.pa_decode_fp8_block(torch.empty_like(one), one, k, v, ks, vs, tab, ctx, 0.1, 100, **over)
     check_device_error(0)
 
 
