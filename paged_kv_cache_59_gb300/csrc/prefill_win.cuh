@@ -178,8 +178,8 @@ __device__ __forceinline__ bool hides_rows(const PrefillParams& P, const KeyTile
 // less: the piece a CTA passes on is its last, the rest its successor's first,
 // so it nearly always is the last one and never writes.)
 // Partial of a slot's tile x: float4 [D / 4][128 rows] of O, then float2 [128]
-// of (m, l). `own(c, v)` gives columns 32 c .. 32 c + 31 of this row's O (warp-
-// collective); `put(c, v)` takes the joined ones, normalised, and put_row(rr, v)
+// (m, l). `own(c, v)` gives columns 32 c .. 32 c + 31 of this row's O, `put(c, v)`
+// takes the joined ones, normalised (both warp-collective), and put_row(rr, v)
 // columns 4 lane .. of the warp's row rr. `valid`: the row is in the chunk (the
 // valid rows of a warp are its first).
 __device__ __forceinline__ float* slot_part(const PrefillParams& P, int slot, int x) {
@@ -204,7 +204,8 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
     // rounds of memory latency than 32 columns of a piece at a time.
     const int rows = __popc(__ballot_sync(kFull, valid));
     const bool by_row = rows * ((n + 7) / 8) < D / 32 * (n - 1);
-    bool last = !by_row && __all_sync(kFull, counted() == n - 1);
+    // only the item's first piece, its CTA's last segment, can expect the others to be complete
+    bool last = me == 0 && !by_row && __all_sync(kFull, counted() == n - 1);
     if (!last) {
         float* dst = slot_part(P, slot, x);
 #pragma unroll 1
@@ -262,10 +263,13 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
         }
         return;
     }
-    auto ml = [&](int k) {
-        return k == me ? make_float2(m, l)
-                       : __ldcg(reinterpret_cast<const float2*>(piece_part(k) + 128 * D) + r);
+    float2 ml01[2];  // (m, l) of the first two pieces (nearly always all of them)
+    auto load_ml = [&](int k) {
+        return k == me ? make_float2(m, l) : __ldcg(reinterpret_cast<const float2*>(piece_part(k) + 128 * D) + r);
     };
+    ml01[0] = load_ml(0);
+    ml01[1] = load_ml(1);
+    auto ml = [&](int k) { return k == 0 ? ml01[0] : k == 1 ? ml01[1] : load_ml(k); };
     float M = -INFINITY, sum = 0.f;
     for (int k = 0; k < n; ++k) M = fmaxf(M, ml(k).x);
     auto factor = [&](float mk) { return mk == -INFINITY ? 0.f : pa::fast_exp2(mk - M); };
@@ -279,7 +283,6 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
         float acc[32] = {};
 #pragma unroll 1
         for (int k = 0; k < n; ++k) {
-            const float f = factor(ml(k).x);
             float v[32];
             if (k == me) {  // warp-uniform
                 own(q, v);
@@ -294,6 +297,7 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
                     v[4 * u + 3] = w.w;
                 }
             }
+            const float f = factor(ml(k).x);
 #pragma unroll
             for (int u = 0; u < 32; ++u) acc[u] += v[u] * f;
         }
@@ -865,27 +869,49 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]) * kUndo;
             };
-            uint4* dst = reinterpret_cast<uint4*>(P.out + ((size_t)(g.q0 + i) * H + g.kvh * G + r % G) * D);
-            auto put = [&](int c, const float (&v)[32]) {  // the normalised output
-                if (i >= g.L) return;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) finite &= fabsf(v[k]) < INFINITY;
-#pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                    dst[(c * 32 + k) / 8] =
-                        make_uint4(pa::float2_to_bf16x2(v[k], v[k + 1]), pa::float2_to_bf16x2(v[k + 2], v[k + 3]),
-                                   pa::float2_to_bf16x2(v[k + 4], v[k + 5]), pa::float2_to_bf16x2(v[k + 6], v[k + 7]));
+            auto row_out = [&](int rr) {  // output row of matrix row rr
+                return reinterpret_cast<uint4*>(P.out + ((size_t)(g.q0 + i - r / G + rr / G) * H + g.kvh * G + rr % G) * D);
             };
-            if (g.slot >= 0 && !__any_sync(kFull, i < g.L)) {
-                // no row of this warp is in the chunk: nothing to keep, here and in the other pieces
+            // The normalised output: 32 columns, 64 bytes of each row. Four lanes exchange theirs
+            // so that each of their stores covers a row's 64 bytes: as 16 bytes a row, 32 rows an
+            // instruction, the stores took 2 us a segment.
+            auto put = [&](int c, const float (&v)[32]) {
+                if (i < g.L) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) finite &= fabsf(v[k]) < INFINITY;
+                }
+                uint32_t w[4][4];  // [16-byte chunk][word]
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k >> 2][k & 3] = pa::float2_to_bf16x2(v[2 * k], v[2 * k + 1]);
+#pragma unroll
+                for (int o = 1; o <= 2; o <<= 1) {  // transposes the 4 x 4 chunks of a lane quad
+                    const bool up = (lane & o) != 0;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        if (a & o) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t got = __shfl_xor_sync(kFull, up ? w[a][e] : w[a + o][e], o);
+                            if (up) w[a][e] = got;
+                            else w[a + o][e] = got;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {  // chunk lane % 4 of the quad's row a
+                    const int rr = (r & ~3) + a;
+                    if (i - r / G + rr / G < g.L)
+                        row_out(rr)[4 * c + (lane & 3)] = make_uint4(w[a][0], w[a][1], w[a][2], w[a][3]);
+                }
+            };
+            if (!__any_sync(kFull, i < g.L)) {
+                // no row of this warp is in the chunk: nothing to keep, here and in other pieces of the item
             } else if (g.slot >= 0) {
                 join_pieces<D>(P, g.slot, x, r, warp, lane, i < g.L, m_used, l, own, put, [&](int rr, float4 v) {
-                    uint16_t* row = reinterpret_cast<uint16_t*>(
-                        __shfl_sync(kFull, (unsigned long long)reinterpret_cast<uintptr_t>(dst), rr));
+                    uint2* row = reinterpret_cast<uint2*>(row_out((r & ~31) + rr));
                     if (lane >= D / 4) return;
                     finite &= fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY;
-                    reinterpret_cast<uint2*>(row)[lane] =
-                        make_uint2(pa::float2_to_bf16x2(v.x, v.y), pa::float2_to_bf16x2(v.z, v.w));
+                    row[lane] = make_uint2(pa::float2_to_bf16x2(v.x, v.y), pa::float2_to_bf16x2(v.z, v.w));
                 });
             } else if (P.work || P.splits <= 1) {
                 const float inv = 1.f / l;
@@ -924,8 +950,11 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 
 // Even mode: the work list. An item costs
 // its key tiles plus kStart, what starting and finishing a segment takes in
-// units of a tile (Q, the pipeline's fill, the epilogue: about 10 us against
-// 1.9). The costs of all non-empty items, in item order, are cut into C runs of
+// units of a tile (the pipeline's fill, the epilogue: 4 us for an item run whole
+// against 1.78 us a tile, 5 and 8 us for the two pieces of a cut one; 3 was the
+// best of 1, 2, 3 and 5 for chunks of several lengths together: 190, 188, 189
+// and 190 us for two of 1,024 rows, 231, 204, 202 and 207 us for four of 512
+// rows behind 700 .. 16,384 tokens). The costs of all non-empty items, in item order, are cut into C runs of
 // equal length, C the CTAs (fewer when a run would be shorter than kStart + 4),
 // so that all CTAs finish together: each has at most one piece of an item begun
 // by the CTA before, whole items, and one piece of an item that the next CTA
@@ -941,7 +970,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 // CTA c - 1 and c, its pieces or 0). Piece k of that item: slot 2 ca + 1 for
 // k = 0, else 2 (ca + k). Behind that table, 8 counters for each CTA (see
 // join_pieces), zeroed here.
-constexpr int kStart = 5, kLeast = 3;
+constexpr int kStart = 3, kLeast = 3;
 template <int G>
 __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const PrefillParams P) {
     __shared__ long long wsum[32];
