@@ -61,21 +61,22 @@ constexpr uint32_t kTmemCols = 512;  // tile X: S at 256X, O at 256X + 128 (D co
 
 using PrefillParams = PaPrefillParams;
 
-// The key tiles that the rows of a query-tile pair attend to, numbered 0 ..
-// n-1: the n_sink leading tiles that hold sinks, then tiles `first` .. from
-// the window of the pair's first row to its last row (all without a window).
-// `lo`: the first position in that row's window.
+// The key tiles that the rows of a query-tile pair attend to: the cache blocks
+// that some row sees, in order - the n_sink leading ones that hold sinks, then
+// those from `first` on, the block of `lo`, the first position in the window of
+// the pair's first row (all blocks without a window) - eight a tile, so that a
+// tile may hold sinks and the window's beginning. n tiles.
 struct KeyTiles {
     int lo, first, n_sink, n;
     __device__ __forceinline__ KeyTiles(const PrefillParams& P, int first_row_pos, int last_row_pos) {
         lo = P.window >= 0 ? max(0, first_row_pos - P.window) : 0;
-        first = lo / kKT;
-        n_sink = min((P.n_sinks + kKT - 1) / kKT, first);
-        n = n_sink + last_row_pos / kKT + 1 - first;
+        first = lo / kBS;
+        n_sink = min((P.n_sinks + kBS - 1) / kBS, first);
+        n = (n_sink + last_row_pos / kBS - first + kBPT) / kBPT;
     }
-    __device__ __forceinline__ int tile(int j) const { return j < n_sink ? j : j - n_sink + first; }
-    // whether some row of the pair sees one of the positions a .. b-1 (past the context aside)
-    __device__ __forceinline__ bool seen(const PrefillParams& P, int a, int b) const { return b > lo || a < P.n_sinks; }
+    __device__ __forceinline__ int block(int i) const { return i < n_sink ? i : i - n_sink + first; }
+    // position of key k of tile j
+    __device__ __forceinline__ int position(int j, int k) const { return block(j * kBPT + k / kBS) * kBS + k % kBS; }
 };
 
 // A block-scaled cache's scale, within the range the library works with.

@@ -160,12 +160,12 @@ struct Bars {
 };
 
 // Whether no query of the pair sees the position (its V row is zeroed), and
-// whether the key tile from position kb on has such a row.
+// whether tile j may have such a row.
 __device__ __forceinline__ bool hidden_row(const PrefillParams& P, const KeyTiles& keys, int ctx, int pos) {
-    return pos >= ctx || !keys.seen(P, pos, pos + 1);
+    return pos >= ctx || (pos < keys.lo && pos >= P.n_sinks);
 }
-__device__ __forceinline__ bool hides_rows(const PrefillParams& P, const KeyTiles& keys, int ctx, int kb) {
-    return kb + kKT > ctx || (kb < keys.lo && kb + kKT > P.n_sinks);
+__device__ __forceinline__ bool hides_rows(const KeyTiles& keys, int ctx, int j) {
+    return keys.position(j, kKT - 1) >= ctx || (keys.lo > 0 && j * kBPT <= keys.n_sink);
 }
 
 // Even mode: a warp's 32 rows (thread = row) of a cut item. There is no merge
@@ -391,13 +391,11 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             auto load = [&](Ring& r, int tile) {
                 if ((tile >> 2) != r.group) {  // warp-collective
                     r.group = tile >> 2;
-                    const int blk = r.group * 32 + lane;
+                    const int blk = keys.block(r.group * 32 + lane);
                     r.ids = blk < nblk ? trow[blk] : -1;
                 }
                 const int bid = __shfl_sync(kFull, r.ids, (tile & 3) * kBPT + b);
-                const int blk = tile * kBPT + b;
-                // blocks past the context, or between the sinks and the window (they may be released): zeros
-                bool in = blk < nblk && keys.seen(P, blk * kBS, blk * kBS + kBS);
+                bool in = keys.block(tile * kBPT + b) < nblk;  // blocks past the context: zeros
                 if (in && (bid < 0 || bid >= P.num_blocks)) {
                     if (lane < NB * kBPT && half == 0) pa::set_error(P.err, PA_DEVERR_BLOCK_ID);
                     in = false;
@@ -416,9 +414,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 }
             };
             for (int j = 0; ok && j < g.n_kt; ++j) {
-                const int tile = keys.tile(g.kt0 + j);
-                load(first, tile);
-                if (kBoth && ok) load(second, tile);
+                load(first, g.kt0 + j);
+                if (kBoth && ok) load(second, g.kt0 + j);
             }
         }
         // Every issued copy lands before the CTA exits: normally the converters and the tensor
@@ -584,7 +581,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     return float2_to_f16x2(f.x, f.y);
                 };
                 for (int j = 0; j < g.n_kt; ++j) {
-                    const int J = J0 + j, st = J % kVS, kb = keys.tile(g.kt0 + j) * kKT;
+                    const int J = J0 + j, st = J % kVS, tile = g.kt0 + j;
                     ok = pa::mbar_wait(bars.v_full(st), (uint32_t)((J / kVS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
@@ -596,7 +593,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             uint4 w = vs[e];
                             // rows that no query of the pair sees are zero (p = 0 must not meet a NaN)
                             if constexpr (decltype(partial)::value)
-                                if (hidden_row(P, keys, g.ctx, kb + ((e & 1023) >> 3))) w = make_uint4(0, 0, 0, 0);
+                                if (hidden_row(P, keys, g.ctx, keys.position(tile, (e & 1023) >> 3))) w = make_uint4(0, 0, 0, 0);
                             w.x = cvt(w.x);
                             w.y = cvt(w.y);
                             w.z = cvt(w.z);
@@ -604,7 +601,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             vs[e] = w;
                         }
                     };
-                    if (hides_rows(P, keys, g.ctx, kb)) convert(std::true_type{});
+                    if (hides_rows(keys, g.ctx, tile)) convert(std::true_type{});
                     else convert(std::false_type{});
                     arrive(bars.v_conv(st));
                 }
@@ -630,7 +627,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 const uint32_t src0 = row0 * D + (D == 64 ? c16 * 16 : ((c16 ^ (row0 & 7)) << 4));
                 const uint32_t half = (c16 >> 2) * 16384, ch = 2 * (c16 & 3);
                 const uint32_t dst0 = half + tc::sw128_offset(row0, ch), dst1 = half + tc::sw128_offset(row0, ch + 1);
-                auto widen = [&](int x, unsigned char* dst, int kb) {
+                auto widen = [&](int x, unsigned char* dst, int tile) {
                     const unsigned char* raw = sm + L_::kRaw + x * L_::kRawTile + src0;
                     auto pass = [&](auto partial) {
 #pragma unroll 4
@@ -638,7 +635,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             uint4 w = *reinterpret_cast<const uint4*>(raw + c * kStep * D);
                             // V rows that no query of the pair sees are zero (p = 0 must not meet a NaN)
                             if constexpr (decltype(partial)::value) {
-                                if (hidden_row(P, keys, g.ctx, kb + row0 + c * kStep)) w = make_uint4(0, 0, 0, 0);
+                                if (hidden_row(P, keys, g.ctx, keys.position(tile, row0 + c * kStep))) w = make_uint4(0, 0, 0, 0);
                             }
                             uint4 lo, hi;
                             e4m3x4_to_f16x4(w.x, lo.x, lo.y);
@@ -649,23 +646,23 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             *reinterpret_cast<uint4*>(dst + dst1 + c * kStep * 128) = hi;
                         }
                     };
-                    if (x == 1 && hides_rows(P, keys, g.ctx, kb)) pass(std::true_type{});
+                    if (x == 1 && hides_rows(keys, g.ctx, tile)) pass(std::true_type{});
                     else pass(std::false_type{});
                     arrive(bars.raw_free(x));
                 };
                 for (int j = 0; j < g.n_kt; ++j) {
-                    const int J = J0 + j, kb = keys.tile(g.kt0 + j) * kKT, ks = J % kKS, vs = J % kVS;
+                    const int J = J0 + j, tile = g.kt0 + j, ks = J % kKS, vs = J % kVS;
                     ok = pa::mbar_wait(bars.k_full(0), (uint32_t)(J & 1), P.err, abort_flag);
                     if (ok && J >= kKS) ok = pa::mbar_wait(bars.k_free(ks), (uint32_t)(((J - kKS) / kKS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
-                    widen(0, sm + L_::kK0 + ks * kTile, kb);
+                    widen(0, sm + L_::kK0 + ks * kTile, tile);
                     if (lane == 0) pa::mbar_arrive(bars.k_conv(ks));
                     ok = pa::mbar_wait(bars.v_full(0), (uint32_t)(J & 1), P.err, abort_flag);
                     if (ok && J >= kVS) ok = pa::mbar_wait(bars.v_free(vs), (uint32_t)(((J - kVS) / kVS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
-                    widen(1, sm + L_::kV0 + vs * kTile, kb);
+                    widen(1, sm + L_::kV0 + vs * kTile, tile);
                     if (lane == 0) pa::mbar_arrive(bars.v_conv(vs));
                 }
             }
@@ -686,13 +683,18 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             const int i = g.qp * 2 * QT + x * QT + r / G;
             const int pos = g.ctx - g.L + i;  // this row's position (padding rows: beyond the chunk)
             float m_used = -INFINITY, l = 0.f;
+            // Key k of tile j is at position 128 j + k + kb_sinks if it is a sink, else + kb_win. In tiles
+            // from j_win on, the limits below are those of the window's keys: where such a tile begins
+            // with sinks, they precede every row's window, so each row sees them by their number alone.
+            const int kb_sinks = g.kt0 * kKT, kb_win = kb_sinks + (keys.first - keys.n_sink) * kBS;
+            const int j_win = keys.n_sink / kBPT - g.kt0;
             // E4M3: lane l holds the scales of block l % 8 of a key tile; those of
             // tile j + 1 and the block id of tile j + 2 are loaded while tile j is
             // worked on.
             const int nblk = min((g.ctx + kBS - 1) / kBS, P.max_blocks);
             auto block_id = [&](int j) {
-                const int blk = j < g.n_kt ? keys.tile(g.kt0 + j) * kBPT + (lane & (kBPT - 1)) : nblk;
-                return blk < nblk && keys.seen(P, blk * kBS, blk * kBS + kBS) ? P.tables[(size_t)g.s * P.max_blocks + blk] : -1;
+                const int blk = j < g.n_kt ? keys.block((g.kt0 + j) * kBPT + (lane & (kBPT - 1))) : nblk;
+                return blk < nblk ? P.tables[(size_t)g.s * P.max_blocks + blk] : -1;
             };
             auto scale_of = [&](const float* scales, int bid) {
                 return bid >= 0 && bid < P.num_blocks ? scales[(size_t)bid * Hk + g.kvh] : 1.f;
@@ -719,14 +721,14 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 if (ok) ok = pa::mbar_wait(bars.s_full(x), (uint32_t)(J & 1), P.err, abort_flag);
                 ok = __all_sync(kFull, ok);
                 tc::fence_after_sync();
-                const int kb = keys.tile(g.kt0 + j) * kKT;
+                const int kb = j * kKT + (j < j_win ? kb_sinks : kb_win);
                 // A row does not see keys beyond its position or, sinks apart, before its window. A warp
                 // takes the masking code only for a tile where that hides a key from one of its rows (a
                 // warp-uniform branch): a tile or two at either end of a window, and that of the sinks.
                 // Key k of a quarter is bit k of the quarter's mask: two instructions an element (as
                 // three comparisons, a masked tile took twice a plain one's time).
                 const int lim0 = pos - kb;  // keys k > lim0 of the tile are not visible
-                const int lim1 = P.window >= 0 ? lim0 - P.window : 0, sink1 = P.n_sinks - kb;  // nor k < lim1, k >= sink1
+                const int lim1 = P.window >= 0 ? lim0 - P.window : 0, sink1 = P.n_sinks - kb_sinks - j * kKT;  // nor k < lim1, k >= sink1
                 const bool mask_warp = __any_sync(kFull, lim0 < kKT - 1 || (lim1 > 0 && sink1 < kKT));
                 auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };  // bits 0 .. n-1
                 auto visible_of = [&](int qd) {
