@@ -362,7 +362,9 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
  * rows of positions that are not visible may hold anything, NaN included.
  * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG; n_sinks = 0 is
  * pa_decode_window. bf16 pools (k_scale, v_scale NULL) or E4M3 pools with
- * per-head scales (both given); workspace as for pa_decode_ex.
+ * per-head scales (both given); workspace as for pa_decode_ex. partition_tokens
+ * 0: on the tensor-core kernel (E4M3 or sinks) 512 .. 1024, the least that the
+ * GPU takes in one wave, instead of pa_decode_partition_tokens.
  */
 int pa_decode_sinks(void* out, const void* q, const void* k_pool, const void* v_pool,
                     const float* k_scale, const float* v_scale, const int32_t* block_tables,
@@ -474,8 +476,8 @@ int pa_copy_blocks_fp8_block(void* k_pool, void* v_pool, float* k_scale, float* 
  * Decode over such a cache: pa_decode_fp8 with the scales of each block,
  *     K_b[t] = code * k_scale[block of t][kv head], V_b[t] likewise.
  * window -1: every position; window >= 0: as pa_decode_sinks, n_sinks too
- * (n_sinks is ignored without a window). Workspace, partitions and kernels as
- * for pa_decode_fp8. V's scale is folded into the softmax weight, w = p *
+ * (n_sinks is ignored without a window). Workspace and kernels as for
+ * pa_decode_fp8; default partitions as for pa_decode_sinks. V's scale is folded into the softmax weight, w = p *
  * v_scale = 2^(s + log2 v_scale - m), which enters the P.V product as one
  * fp16 term at head_dim 128: within 2^-11 of w, or 2^-25 of the reference weight.
  */

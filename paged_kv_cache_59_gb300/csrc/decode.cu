@@ -1360,11 +1360,26 @@ int wave_partition_tokens(int n_seqs, int n_kv_heads, int context, int sms, int 
     return best;
 }
 
+// The same for the tensor-core kernel in pa_decode_sinks (but for a bf16 window
+// without sinks) and pa_decode_fp8_block: 1024 tokens, or the size in [512, 1024] that gives the fullest slot of a
+// single wave the least to do. A call that leaves slots empty takes as long as
+// its longest partition: 1 sequence of 32/8 heads and 4,096 tokens (E4M3) took
+// 15.2 us with 1024 and 10.3 with 512, 2 of 16,384 tokens 18.8 and 15.7; with
+// several waves 512 costs more than it gives (1 of 131,072: 54.9 and 65.2).
+// Sizes above 1024 would suit some long contexts (49.1 us there, 1792), but a
+// bound far above the contexts' lengths would then cost (23 us at 4,096).
+int mma_partition_tokens(int eb, int n_seqs, int n_kv_heads, int span) {
+    const long long slots = (long long)sm_count() * (eb == 1 ? 4 : 3);  // CTAs per SM, see mma::Lay
+    for (int pt = kDefaultPartitionTokens; pt < 2 * kDefaultPartitionTokens; pt += 64)
+        if ((long long)n_seqs * n_kv_heads * ((span + pt - 1) / pt) <= slots) return pt;
+    return 2 * kDefaultPartitionTokens;
+}
+
 int default_partition_tokens(bool tensor, int eb, int n_seqs, int n_kv_heads, int G, int head_dim,
-                             int max_context_len, int window, int n_sinks = 0) {
-    if (tensor) return 2 * kDefaultPartitionTokens;
+                             int max_context_len, int window, int n_sinks = 0, bool spread = false) {
     const long long wide = (long long)window + n_sinks + (n_sinks > 0 ? 3 : 2) * kBS;  // a window and its sinks
     const int span = window >= 0 && wide < max_context_len ? (int)wide : max_context_len;
+    if (tensor) return spread ? mma_partition_tokens(eb, n_seqs, n_kv_heads, span) : 2 * kDefaultPartitionTokens;
     const int sms = sm_count();
     return wave_partition_tokens(n_seqs, n_kv_heads, span, sms, sms * k1_ctas_per_sm(head_dim, G, eb));
 }
@@ -1413,7 +1428,7 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
                 int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len, int num_blocks,
                 int window, int partition_tokens, void* workspace, size_t workspace_bytes,
                 pa_stream_t stream, bool force_tc = false, const int32_t* items = nullptr, int n_items = 0,
-                int n_sinks = 0, bool block_scaled = false) {
+                int n_sinks = 0, bool block_scaled = false, bool spread = false) {
     if (n_seqs < 0 || max_context_len < 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
         n_heads <= 0 || n_kv_heads <= 0)
         return PA_ERR_INVALID_ARG;
@@ -1438,7 +1453,7 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     // for 512 covers every one of them.
     const int pt = partition_tokens == 0
                        ? default_partition_tokens(tensor, eb, n_seqs, n_kv_heads, G, head_dim, max_context_len, window,
-                                                  n_sinks)
+                                                  n_sinks, spread)
                        : resolve_partition_tokens(partition_tokens);
     if (pt < 0) return PA_ERR_INVALID_ARG;
     if (pt / kBS > 32 * kNW) return PA_ERR_INVALID_ARG;  // one table entry per lane
@@ -1574,7 +1589,7 @@ extern "C" int pa_decode_sinks(void* out, const void* q, const void* k_pool, con
     return decode_impl(k_scale ? 1 : 2, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
                        n_heads, n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len,
                        num_blocks, window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0,
-                       n_sinks);
+                       n_sinks, false, k_scale || n_sinks > 0);
 }
 
 extern "C" int pa_decode_fp8_block(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -1588,7 +1603,8 @@ extern "C" int pa_decode_fp8_block(void* out, const void* q, const void* k_pool,
     if (n_sinks > max_context_len) n_sinks = max_context_len;
     return decode_impl(1, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, n_heads,
                        n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len, num_blocks,
-                       window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0, n_sinks, true);
+                       window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0, n_sinks, true,
+                       true);
 }
 
 extern "C" int pa_decode(void* out, const void* q, const void* k_pool, const void* v_pool,
