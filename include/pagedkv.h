@@ -363,8 +363,9 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
  * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG; n_sinks = 0 is
  * pa_decode_window. bf16 pools (k_scale, v_scale NULL) or E4M3 pools with
  * per-head scales (both given); workspace as for pa_decode_ex. partition_tokens
- * 0: on the tensor-core kernel (E4M3 or sinks) 512 .. 1024, the least that the
- * GPU takes in one wave, instead of pa_decode_partition_tokens.
+ * 0: on the tensor-core kernel (E4M3 or sinks) 512 .. 2048, by how the call
+ * fills the GPU, instead of pa_decode_partition_tokens; of up to 4 sequences,
+ * those far below max_context_len are cut into smaller partitions.
  */
 int pa_decode_sinks(void* out, const void* q, const void* k_pool, const void* v_pool,
                     const float* k_scale, const float* v_scale, const int32_t* block_tables,

@@ -69,6 +69,8 @@ struct DecodeParams {
     int max_blocks;
     int num_blocks;
     int part_blocks;
+    int part_least;  // less than part_blocks: sequences too short for max_parts partitions take smaller
+                     // ones, but none below this
     int max_parts;
     int window;  // >= 0: the query at position ctx-1 sees positions ctx-1-window .. ctx-1
     int n_sinks; // and, with a window, positions 0 .. n_sinks-1
@@ -105,11 +107,11 @@ __device__ __forceinline__ bool cta_item(const DecodeParams& P, int& p, int& kvh
 // blocks that hold sinks, then blocks blk_first .. nblk - 1 from the window's
 // first position on (all of them without a window). Blocks between are never
 // read (their table entries may be released). The `total` blocks are numbered
-// 0 .. total-1 and cut into nparts partitions.
+// 0 .. total-1 and cut into nparts partitions of `part` blocks.
 // SINKS false: the call has none (those kernels carry no trace of them).
 template <bool SINKS>
 struct Span {
-    int first_pos, blk_first, nblk, n_sink_blk, total, nparts;
+    int first_pos, blk_first, nblk, n_sink_blk, total, part, nparts;
     bool over;  // the context or its partitions exceed the call's bounds (clamped)
     __device__ __forceinline__ Span(const DecodeParams& P, int ctx) {
         nblk = (ctx + kBS - 1) / kBS;
@@ -117,15 +119,18 @@ struct Span {
         blk_first = first_pos / kBS;
         n_sink_blk = SINKS ? min((P.n_sinks + kBS - 1) / kBS, blk_first) : 0;
         total = n_sink_blk + nblk - blk_first;
-        nparts = (total + P.part_blocks - 1) / P.part_blocks;
+        part = P.part_blocks;
+        if (SINKS && P.part_least < part)  // in steps of 4 blocks, one a warp
+            part = min(part, max(P.part_least, ((total + P.max_parts - 1) / P.max_parts + 3) / 4 * 4));
+        nparts = (total + part - 1) / part;
         over = nblk > P.max_blocks || nparts > P.max_parts;
         if (over) {  // caller broke the bounds it passed
             nblk = min(nblk, P.max_blocks);
             blk_first = min(blk_first, nblk);
             n_sink_blk = min(n_sink_blk, blk_first);
             total = n_sink_blk + nblk - blk_first;
-            nparts = min((total + P.part_blocks - 1) / P.part_blocks, P.max_parts);
-            total = min(total, nparts * P.part_blocks);
+            nparts = min((total + part - 1) / part, P.max_parts);
+            total = min(total, nparts * part);
         }
     }
     // the logical block of number i
@@ -309,8 +314,8 @@ pa_decode_partition_kernel(const DecodeParams P) {
     if (sp.over && p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
     if (p >= sp.nparts) return;
     const int first_pos = sp.first_pos;
-    const int blk_begin = p * P.part_blocks;  // numbered as in Span
-    const int nb_local = min(blk_begin + P.part_blocks, sp.total) - blk_begin;
+    const int blk_begin = p * sp.part;  // numbered as in Span
+    const int nb_local = min(blk_begin + sp.part, sp.total) - blk_begin;
     const int my_n = nb_local > warp ? (nb_local - warp + NW - 1) / NW : 0;  // <= 32
 
     const int c = lane % LPT;   // chunk lane within a token row
@@ -735,8 +740,8 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
     if (sp.over && p == 0 && threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
     if (p >= sp.nparts) return;
     const int first_pos = sp.first_pos;
-    const int blk_begin = p * P.part_blocks;  // numbered as in Span
-    const int nb_local = min(blk_begin + P.part_blocks, sp.total) - blk_begin;
+    const int blk_begin = p * sp.part;  // numbered as in Span
+    const int nb_local = min(blk_begin + sp.part, sp.total) - blk_begin;
     const int my_n = nb_local > warp ? (nb_local - warp + NW - 1) / NW : 0;  // <= 32
 
     unsigned char* my_stages = stages + (size_t)warp * kWarp;
@@ -1361,18 +1366,31 @@ int wave_partition_tokens(int n_seqs, int n_kv_heads, int context, int sms, int 
 }
 
 // The same for the tensor-core kernel in pa_decode_sinks (but for a bf16 window
-// without sinks) and pa_decode_fp8_block: 1024 tokens, or the size in [512, 1024] that gives the fullest slot of a
-// single wave the least to do. A call that leaves slots empty takes as long as
-// its longest partition: 1 sequence of 32/8 heads and 4,096 tokens (E4M3) took
-// 15.2 us with 1024 and 10.3 with 512, 2 of 16,384 tokens 18.8 and 15.7; with
-// several waves 512 costs more than it gives (1 of 131,072: 54.9 and 65.2).
-// Sizes above 1024 would suit some long contexts (49.1 us there, 1792), but a
-// bound far above the contexts' lengths would then cost (23 us at 4,096).
+// without sinks) and pa_decode_fp8_block. A call that leaves CTA slots empty
+// takes as long as its longest partition, and one that fills them as many
+// rounds; a round costs its partition and about 128 tokens more. Measured with
+// 1024 tokens and with this rule (E4M3, 32/8 and 64/8 heads): 1 sequence of 4,096
+// tokens 15.2 and 10.2 us (512), 2 of 16,384 18.8 and 15.6, 1 of 131,072 54.9
+// and 49.3 (1792), 4 of 100,000 .. 121,596 166 and 157. Where max_context_len is
+// far above a sequence's length, the kernel cuts it smaller (Span). Batches
+// differ in their lengths, so rounds say little for them: more than 4 sequences
+// take 1024 tokens, or fewer when that still is a single round (24 of 1,100
+// tokens: 19.6 and 14.9 us).
+constexpr int kFewSeqs = 4;
 int mma_partition_tokens(int eb, int n_seqs, int n_kv_heads, int span) {
-    const long long slots = (long long)sm_count() * (eb == 1 ? 4 : 3);  // CTAs per SM, see mma::Lay
-    for (int pt = kDefaultPartitionTokens; pt < 2 * kDefaultPartitionTokens; pt += 64)
-        if ((long long)n_seqs * n_kv_heads * ((span + pt - 1) / pt) <= slots) return pt;
-    return 2 * kDefaultPartitionTokens;
+    const int sms = sm_count();
+    const long long slots = (long long)sms * (eb == 1 ? 4 : 3) - sms / 16;  // see mma::Lay; a few may be late
+    if (sms <= 0) return 2 * kDefaultPartitionTokens;
+    long long least = 0;
+    int best = 2 * kDefaultPartitionTokens;
+    for (int pt = kDefaultPartitionTokens; pt <= 4 * kDefaultPartitionTokens; pt += 64) {
+        const long long rounds = ((long long)n_seqs * n_kv_heads * ((span + pt - 1) / pt) + slots - 1) / slots;
+        const long long cost = rounds * (pt + 128);
+        if (n_seqs > kFewSeqs ? rounds > 1 || pt >= best : least > 0 && cost > least) continue;
+        least = cost;
+        best = pt;
+    }
+    return best;
 }
 
 int default_partition_tokens(bool tensor, int eb, int n_seqs, int n_kv_heads, int G, int head_dim,
@@ -1496,7 +1514,8 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     P.n_kv_heads = n_kv_heads;
     P.max_blocks = max_blocks_per_seq;
     P.num_blocks = num_blocks;
-    P.part_blocks = pt / kBS;
+    P.part_blocks = P.part_least = pt / kBS;
+    if (partition_tokens == 0 && tensor && spread && n_seqs <= kFewSeqs) P.part_least = kDefaultPartitionTokens / kBS;
     P.max_parts = max_parts;
     P.window = window;
     P.n_sinks = n_sinks;
@@ -1509,7 +1528,7 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     int st;
     if (block_scaled)  // one instantiation, with sinks
         st = dispatch_kernel<1, true, true>(tensor, head_dim, G, P, n_seqs, s);
-    else if (n_sinks > 0)
+    else if (spread)
         st = eb == 2 ? dispatch_kernel<2, false, true>(tensor, head_dim, G, P, n_seqs, s)
                      : dispatch_kernel<1, false, true>(tensor, head_dim, G, P, n_seqs, s);
     else
