@@ -18,15 +18,20 @@
 // segment's K and V, and the converter warps its Q as soon as the last Q.K^T has
 // read the old one; the tensor core then starts on it at once.
 //
-// Measured (32/8 heads of 128, 19 pairs a KV head, so one item a CTA): 1.67 us a
-// key tile in bf16 (1,530 TFLOP/s of its two tiles' four products over 152 SMs,
-// 0.79 of a cuBLAS burst) and 1.78 with E4M3, and 14 us a call beside the tiles:
-// the plan and launches 7, the first tile's loads, softmax and the epilogue 7.
-// What bounds the tile loop: S and P share 128 of the 512 tensor-memory columns
-// for each of the two query tiles, so a tile's Q.K^T cannot start before its
-// last P.V, and the tensor core waits for a softmax about a fifth of the time.
-// 2,048 rows, window 4,096 + 4 sinks (256 items of 35 tiles on 152 SMs): 129 us,
-// 1,065 TFLOP/s of visible pairs; 179 us with whole waves, cut tails and a
+// Measured (32/8 heads of 128, 19 pairs a KV head, so one item a CTA): 1.75 us a
+// key tile in bf16 (1,460 TFLOP/s of its two tiles' four products over 152 SMs,
+// 0.75 of a cuBLAS burst) and 1.80 with E4M3, and 11 us a call beside the tiles:
+// the plan and launches 6, the first tile's loads, softmax and the epilogue 5.
+// What bounds the tile loop is a chain: S and P share 128 of the 512 tensor-
+// memory columns for each of the two query tiles, so a tile's P.V and next
+// Q.K^T (1,350 cycles, the shared memory's bandwidth being shared with V's
+// conversion) and its softmax (1,650 to 1,900) follow each other. Without the
+// exponentials a tile takes 1.56 us, without V's conversion 1.61, without both
+// 1.47. Converters that load V (E4M3: K and V) themselves, a tile ahead in
+// registers instead of by TMA, took 1.82, and 270 us instead of 201 for four
+// chunks whose cache comes from HBM.
+// 2,048 rows, window 4,096 + 4 sinks (256 items of 33 tiles on 152 SMs): 127.5 us,
+// 1,079 TFLOP/s of visible pairs; 179 us with whole waves, cut tails and a
 // block-wide barrier between segments.
 //
 // E4M3 (EB = 1). The codes of a K and of a V tile (half the bytes) land in a
@@ -354,9 +359,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
         // ----------------------------------------------------------- TMA producers
         // A stage is refilled as soon as its last reader is done. bf16: K and V have a warp each:
         // when a tile's load waits in line behind the other operand's, the tensor core waits for it
-        // (1.86 us a tile with one warp, 1.67 with two). E4M3, half the bytes and boxes: one warp
-        // for both (1.75 us a tile; 1.83 with a second one, which takes issue slots from the
-        // softmax); K(J)'s codes replace K(J-1)'s once those are widened, V's likewise.
+        // (one warp for both: 11% more a tile). E4M3, half the bytes and boxes: one warp for both
+        // (a second one takes issue slots from the softmax: 5% more a tile); K(J)'s codes replace K(J-1)'s once those are widened, V's likewise.
         constexpr int kBoth = EB == 1;
         constexpr uint32_t kBytes = EB == 2 ? kTile : L_::kRawTile;
         // bf16: lane l < 8 kNH moves box (block l / kNH, dims 64 g .., g = l % kNH); E4M3: lane
@@ -956,12 +960,12 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 // against 1.78 us a tile, 5 and 8 us for the two pieces of a cut one; 3 was the
 // best of 1, 2, 3 and 5 for chunks of several lengths together: 190, 188, 189
 // and 190 us for two of 1,024 rows, 231, 204, 202 and 207 us for four of 512
-// rows behind 700 .. 16,384 tokens). The costs of all non-empty items, in item order, are cut into C runs of
-// equal length, C the CTAs (fewer when a run would be shorter than kStart + 4),
-// so that all CTAs finish together: each has at most one piece of an item begun
+// rows behind 700 .. 16,384 tokens). The costs of all non-empty items, in item
+// order, are cut into C runs of equal length, C the CTAs (fewer when a run would
+// be shorter than kStart + 4), so that all CTAs finish together: each has at most one piece of an item begun
 // by the CTA before, whole items, and one piece of an item that the next CTA
 // goes on with. (A window makes the items equally long and few waves deep: 256
-// items of 35 tiles on 152 CTAs take 4 segments on the busiest CTA with whole
+// items of 33 tiles on 152 CTAs take 4 segments on the busiest CTA with whole
 // waves and cut tails, 2 or 3 here, and no CTA idles.) A cut that would leave
 // fewer than kLeast tiles on one side moves to that end of the item. When the
 // items are at most the CTAs and none is much longer than the mean, each runs
