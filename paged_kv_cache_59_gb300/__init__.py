@@ -454,12 +454,13 @@ def _call(fn: str, dev: int, stream, *args) -> None:
         check(fn, st)
 
 
-def _ints(*values):
+def _ints(a, b, c, d):
     """The values as C ints (a larger one would be cut to its low 32 bits)."""
-    values = [int(x) for x in values]
-    if max(values) >= 2 ** 31 or min(values) < -2 ** 31:
-        raise ValueError(f"a size, window or count does not fit 32 bits: {values}")
-    return values
+    a, b, c, d = int(a), int(b), int(c), int(d)
+    if (a <= 0x7fffffff and b <= 0x7fffffff and c <= 0x7fffffff and d <= 0x7fffffff and
+            a >= -0x80000000 and b >= -0x80000000 and c >= -0x80000000 and d >= -0x80000000):
+        return a, b, c, d
+    raise ValueError(f"a size, window or count does not fit 32 bits: {(a, b, c, d)}")
 
 
 def _workspace(t, dev: int):
