@@ -366,6 +366,8 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
  * 0: on the tensor-core kernel (E4M3 or sinks) 512 .. 2048, by how the call
  * fills the GPU, instead of pa_decode_partition_tokens; of up to 4 sequences,
  * those far below max_context_len are cut into smaller partitions.
+ * A workspace serves one call at a time: calls, or captured graphs of them,
+ * whose kernels may overlap need one each.
  */
 int pa_decode_sinks(void* out, const void* q, const void* k_pool, const void* v_pool,
                     const float* k_scale, const float* v_scale, const int32_t* block_tables,
@@ -601,7 +603,8 @@ int pa_prefill_paged_ex(void* out, const void* q, const void* k_pool, const void
  * position spoils (and flags) the rows that share its key tile, also where it
  * is masked for them, as in pa_prefill_paged.
  * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG. splits and workspace
- * as for pa_prefill_paged_ex.
+ * as for pa_prefill_paged_ex; calls whose kernels may overlap need a workspace
+ * each.
  */
 int pa_prefill_sinks(void* out, const void* q, const void* k_pool, const void* v_pool,
                      const int32_t* block_tables, const int32_t* context_lens,
