@@ -80,12 +80,32 @@ struct DecodeParams {
     const int4* items;
     int n_items;
     int n_seqs;
+    int parts_last;  // the grid is (KV heads, sequences, partitions)
 };
+
+// The grid of a partition kernel. Under a window with sinks every sequence has as
+// many partitions, the last of them short: those run last, and fill the end of
+// the last wave (32 windows of 4,096 + 4, 32/8 heads: bf16 91.5 us with the
+// partitions of a sequence side by side, 87.8 so, E4M3 49.8 and 48.6; 16 with
+// 64/8 heads: E4M3 29.4 and 27.7, but bf16 51.3 and 52.6). Contexts of different
+// lengths are better off side by side (64 of 128 .. 4,096 tokens, E4M3: 46.0 us,
+// 47.2 otherwise).
+dim3 grid_of(const DecodeParams& P, int n_seqs) {
+    if (P.items) return dim3((unsigned)P.n_items);
+    return P.parts_last ? dim3(P.n_kv_heads, n_seqs, P.max_parts) : dim3(P.max_parts, P.n_kv_heads, n_seqs);
+}
 
 // The (partition, KV head, sequence) of this CTA: its grid position, or its
 // plan item. A plan item outside the call's bounds sets PA_DEVERR_PLAN and
-// the CTA does nothing.
+// the CTA does nothing. SINKS, under a window: partitions vary slowest (grid_of).
+template <bool SINKS>
 __device__ __forceinline__ bool cta_item(const DecodeParams& P, int& p, int& kvh, int& b) {
+    if (SINKS && P.parts_last) {
+        p = blockIdx.z;
+        kvh = blockIdx.x;
+        b = blockIdx.y;
+        return true;
+    }
     if (!P.items) {
         p = blockIdx.x;
         kvh = blockIdx.y;
@@ -297,7 +317,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
     pa::launch_dependents();     // the merge kernel may be scheduled now
     pa::grid_dependency_wait();  // the previous kernel (e.g. the cache write) is complete
     int p, kvh, b;
-    if (!cta_item(P, p, kvh, b)) return;
+    if (!cta_item<SINKS>(P, p, kvh, b)) return;
     const int h0 = kvh * G;
     const int ctx = P.ctx[b];
 
@@ -720,7 +740,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
     pa::launch_dependents();
     pa::grid_dependency_wait();
     int p, kvh, b;
-    if (!cta_item(P, p, kvh, b)) return;
+    if (!cta_item<SINKS>(P, p, kvh, b)) return;
     const int h0 = kvh * G;
     if (pa::smem_u32(smem_mma) & 1023u) {  // never expected; refuse rather than mis-swizzle
         if (threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_LAYOUT);
@@ -1253,7 +1273,7 @@ int launch_partition(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
             return PA_ERR_CUDA;
         attr_done[dev] = true;
     }
-    const dim3 grid = P.items ? dim3((unsigned)P.n_items) : dim3(P.max_parts, P.n_kv_heads, n_seqs);
+    const dim3 grid = grid_of(P, n_seqs);
     return pa_launch_pdl(kern, grid, dim3(kNW * 32), SM::TOTAL, stream, P);
 }
 
@@ -1289,7 +1309,7 @@ int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream)
                               : pa_make_tmap_2d_u8(&tk, P.k_pool, 128, rows, 128, 128, kBS) &&
                                     pa_make_tmap_2d_u8(&tv, P.v_pool, 128, rows, 128, 128, kBS);
     if (!maps) return PA_ERR_CUDA;
-    const dim3 grid = P.items ? dim3((unsigned)P.n_items) : dim3(P.max_parts, P.n_kv_heads, n_seqs);
+    const dim3 grid = grid_of(P, n_seqs);
     return pa_launch_pdl(kern, grid, dim3(mma::kNW * 32), kSmem, stream, P, tk, tv);
 }
 
@@ -1523,6 +1543,7 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     P.items = reinterpret_cast<const int4*>(items);
     P.n_items = n_items;
     P.n_seqs = n_seqs;
+    P.parts_last = n_sinks > 0 && window >= 0 && max_parts <= 65535;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int st;
