@@ -446,17 +446,19 @@ int pa_decode_fp8(void* out, const void* q, const void* k_pool, const void* v_po
 /*
  * pa_rope_and_cache into such a cache: element x of the rotated k (or of v)
  * is stored as the E4M3 code of x / scale (nearest even; beyond +-448
- * saturates, NaN stays NaN). The new tokens of a block in one call form a run:
- *  - a run that starts at the block's first slot gives the block its scale
+ * saturates, NaN stays NaN). The new tokens of a block in one call are encoded
+ * together:
+ *  - with the block's first slot among them they give the block its scale
  *    (what the block held is void: a block's first slot is written first);
- *  - any other run raises the block's scale where its own tokens need a
- *    larger one, and the block's other slots are then encoded again: exact,
- *    unless the new code is an E4M3 subnormal (off by at most 2^-10 of the
- *    new scale).
+ *  - else they raise the block's scale where they need a larger one, and the
+ *    block's other slots are then encoded again: exact, unless the new code is
+ *    an E4M3 subnormal (off by at most 2^-10 of the new scale).
  * Infinite and NaN elements do not enter the maximum. A call's tokens of one
- * block must be next to each other in slot_mapping with consecutive slots (as
- * pa_bm_append_tokens gives them); two runs of one block in one call race.
- * Tokens skipped by a negative position or slot end a run.
+ * block must lie within 16 consecutive entries of slot_mapping, in any order
+ * (pa_bm_append_tokens gives them so); skipped entries, and other blocks' tokens,
+ * may lie between them. A token further from the first of its block is not
+ * written and sets PA_DEVERR_SLOT when another one of the block precedes it by
+ * fewer than 16 entries; otherwise the block's two groups race.
  * Arguments as for pa_rope_and_cache, with rot_dim = 0 for a plain write.
  */
 int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const void* v, void* k_pool,

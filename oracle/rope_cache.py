@@ -55,32 +55,37 @@ def power_scale(amax: float) -> float:
     return 2.0 ** e
 
 
+def read_scale(s: float) -> float:
+    """A block's scale as the attention calls read it: in [2^-32, 2^32], NaN as 2^-32."""
+    return 2.0 ** -32 if s != s else min(max(float(s), 2.0 ** -32), 2.0 ** 32)
+
+
 def block_scaled_write(x, pool8, scales, slots):
     """x fp32 [T][Hk][D] (K already rotated); pool8 uint8 [nb][Hk][16][D],
     scales fp32 [nb][Hk]. Tokens with slot < 0 are skipped. The tokens of one
-    block are next to each other in slots. Returns new (pool8, scales)."""
+    block lie within 16 consecutive entries of slots, in any order; they share
+    one new scale. A block whose first slot is among them gets it anew, any
+    other keeps at least its own. Returns new (pool8, scales)."""
     pool, sc = np.array(pool8), np.array(scales)
     slots = np.asarray(slots)
-    t = 0
-    while t < len(slots):
-        if slots[t] < 0:
-            t += 1
-            continue
-        n = 1
-        while t + n < len(slots) and slots[t + n] == slots[t] + n and slots[t + n] % BS != 0:
-            n += 1
-        blk, off = int(slots[t]) // BS, int(slots[t]) % BS
+    block = np.where(slots < 0, -1, slots // BS)
+    for t in range(len(slots)):
+        blk = int(block[t])
+        if blk < 0 or (block[max(0, t - BS + 1):t] == blk).any():
+            continue  # skipped, or written with an earlier token of its block
+        rows = t + np.nonzero(block[t:t + BS] == blk)[0]
+        off = slots[rows] % BS
         for h in range(pool.shape[1]):
-            a = np.abs(x[t:t + n, h].astype(np.float64))
+            a = np.abs(x[rows, h].astype(np.float64))
             a = a[np.isfinite(a)]
             need = power_scale(float(a.max()) if a.size else 0.0)
-            old = float(sc[blk, h])
-            new = need if off == 0 else max(old, need)
-            if off != 0 and new != old:
+            old = read_scale(sc[blk, h])
+            new = np.float32(need if (off == 0).any() else max(old, need))
+            if not (off == 0).any() and new != old:
                 keep = np.ones(BS, bool)
-                keep[off:off + n] = False
-                pool[blk, h, keep] = f64_to_e4m3(e4m3_to_f64(pool[blk, h, keep]) * (old / new))
-            pool[blk, h, off:off + n] = f64_to_e4m3(x[t:t + n, h].astype(np.float64) / new)
-            sc[blk, h] = np.float32(new)
-        t += n
+                keep[off] = False
+                moved = e4m3_to_f64(pool[blk, h, keep]).astype(np.float32) * (np.float32(old) / new)
+                pool[blk, h, keep] = f64_to_e4m3(moved.astype(np.float64))
+            pool[blk, h, off] = f64_to_e4m3((x[rows, h].astype(np.float32) / new).astype(np.float64))
+            sc[blk, h] = new
     return pool, sc

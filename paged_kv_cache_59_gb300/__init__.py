@@ -535,7 +535,7 @@ def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_pool, v_pool, k_scale, v_scale
                                 interleaved: bool = False, stream=None) -> None:
     """pa_rope_and_cache into E4M3 pools with a scale per block and head:
     k_scale, v_scale fp32 [num_blocks][n_kv_heads], set and raised by the call.
-    A call's tokens of one block must be next to each other, in slot order."""
+    A call's tokens of one block must lie within 16 consecutive entries of slot_mapping."""
     if k_scale is None or v_scale is None:
         raise ValueError("k_scale and v_scale are needed")
     _rope("pa_rope_and_cache_fp8_block", True, q_out, q, k, v, k_pool, v_pool, k_scale, v_scale, cos_sin, positions,

@@ -236,17 +236,24 @@ __device__ __forceinline__ float power_scale(float amax) {
 }
 
 // K and V of a block-scaled cache. The scale of a (block, head) covers all of
-// its tokens, so the tokens of one call that go to one block - a run: tokens
-// next to each other in the call with consecutive slots of one block, up to
-// 16 - belong to one warp, which finds their largest magnitude and encodes them.
-// A run that starts at the block's first slot
-// gives the block its scale; any other run raises the scale if it must, and
-// then also encodes the block's other tokens again. As scales are powers of
-// two, that is exact for every code whose new value is not an E4M3 subnormal,
-// and off by at most 2^-10 of the new scale (half a subnormal step) there:
-// tokens do not lose a bit each time the block's scale grows.
-// One warp per (tokens_per_warp tokens, KV head, K or V).
-template <int D>
+// its tokens, so a call's tokens of one block - a run - belong to one warp, which
+// finds their largest magnitude and encodes them. They lie within 16 consecutive
+// entries of the call, in any order, skipped entries between them. The entry
+// without another of its block in the 15 before it leads, and its warp takes
+// those in the 15 behind it. One behind these that an entry of the run precedes
+// by less than 16 belongs to nobody: it is not written, and flagged.
+// A run with the block's first slot gives the block its scale; any other run
+// raises the scale if it must, and then also encodes the block's other tokens
+// again. As scales are powers of two, that is exact for every code whose new
+// value is not an E4M3 subnormal, and off by at most 2^-10 of the new scale (half
+// a subnormal step) there: tokens do not lose a bit each time the block's scale
+// grows.
+// One warp per (tokens_per_warp tokens, KV head, K or V). Finding the runs by
+// their blocks takes 0.1 us of a small call and 2 to 7% of a large one more than
+// by slots that follow each other without a gap, where a skipped token left two
+// warps with one block. (LARGE: passes without a token are jumped over one by
+// one; leaving the loop after the last, as small calls do, spilled 100 bytes.)
+template <int D, bool LARGE>
 __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta) {
     constexpr int LPR = D / 16, TPP = 32 / LPR, NP = kBS / TPP;  // lanes per row, rows per pass, passes
     const int lane = threadIdx.x & 31;
@@ -255,25 +262,30 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
     const int h = (int)((w >> 1) % P.n_kv_heads);
     const long long t0 = (w >> 1) / P.n_kv_heads * P.tokens_per_warp;
     if (t0 >= P.n_tokens) return;
-    // lane l: the slot of token t0 - 1 + l, -1 where nothing is written. Lanes
-    // 1 .. tokens_per_warp are this warp's; a run that starts there ends by lane 31.
-    const long long tl = t0 - 1 + lane;
-    long long slot = -1;
-    int pos = 0;
-    if (tl >= 0 && tl < P.n_tokens) {
-        const bool mine = lane >= 1 && lane <= P.tokens_per_warp && h == 0 && !is_v;
-        slot = P.slots[tl];
-        pos = token_position(P, (int)tl, mine);
-        if (slot >= P.pool_slots) {
-            if (mine) pa::set_error(P.err, PA_DEVERR_SLOT);
-            slot = -1;
-        }
-        if (pos < 0) slot = -1;
+    // The warp's own entries, t0 .. t0 + tokens_per_warp - 1 (at most 16), and those around them: lane l holds
+    // entry t0 + l, where every run of its own ends, and of one of the 16 entries before t0 (lanes 0 .. 15) and
+    // the 16 from t0 + 32 on (16 .. 31) the block. Block -1: nothing is written.
+    const long long e1 = t0 + lane, e2 = lane < 16 ? e1 - 16 : e1 + 16, last = P.n_tokens - 1;
+    const bool here = e1 <= last, here2 = e2 >= 0 && e2 <= last;
+    const long long t1 = min(e1, last), t2 = max(0LL, min(e2, last));  // no branch before any of the loads
+    const int64_t slot = P.slots[t1], slot2 = P.slots[t2];
+    int64_t at = 0, at2 = 0;
+    if (P.rot > 0) {
+        at = P.pos[t1];
+        at2 = P.pos[t2];
     }
-    const long long before = __shfl_up_sync(kFull, slot, 1);
-    const bool leads = slot >= 0 && (slot % kBS == 0 || lane == 0 || before != slot - 1);
-    const unsigned follow = __ballot_sync(kFull, slot >= 0 && !leads);
-    unsigned heads = __ballot_sync(kFull, leads && lane >= 1 && lane <= P.tokens_per_warp);
+    const bool mine = here && lane < P.tokens_per_warp;
+    if (mine && h == 0 && !is_v) {
+        if (slot >= P.pool_slots) pa::set_error(P.err, PA_DEVERR_SLOT);
+        if (P.rot > 0 && at >= P.max_position) pa::set_error(P.err, PA_DEVERR_POSITION);
+    }
+    auto block_of = [&](bool in, int64_t slot, int64_t at) {
+        in &= (uint64_t)slot < (uint64_t)P.pool_slots && (P.rot == 0 || (uint64_t)at < (uint64_t)P.max_position);
+        return in ? (int)(slot >> 4) : -1;  // slot / kBS
+    };
+    const int block = block_of(here, slot, at), block2 = block_of(here2, slot2, at2);
+    const int off = (int)slot & (kBS - 1), pos = (int)at;
+    unsigned todo = __ballot_sync(kFull, mine && block >= 0);
     const bool il = P.interleaved != 0;
     const int c = lane % LPR, tg = lane / LPR;
     int ca, cb;
@@ -283,22 +295,27 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
     const long long stride = is_v ? P.v_stride : P.k_stride;
     unsigned char* pool = is_v ? P.v_pool : P.k_pool;
     float* scales = is_v ? P.v_block_scale : P.k_block_scale;
-    while (heads) {
-        const int l0 = __ffs(heads) - 1;  // 1 .. 16
-        heads &= heads - 1;
-        const int n = 1 + __ffs(~(follow >> (l0 + 1))) - 1;  // tokens of the run
-        const long long slot0 = __shfl_sync(kFull, slot, l0);
-        const int off0 = (int)(slot0 % kBS);
-        const long long tile = slot0 / kBS * P.n_kv_heads + h;
+    while (todo) {
+        const int l0 = __ffs(todo) - 1;  // 0 .. 15
+        const int blk_id = __shfl_sync(kFull, block, l0);
+        const unsigned alike = __ballot_sync(kFull, block == blk_id), alike2 = __ballot_sync(kFull, block2 == blk_id);
+        todo &= ~alike;
+        if ((alike2 & 0xffffu) >> (l0 + 1)) continue;  // an entry before t0 leads
+        const unsigned run = alike >> l0 & 0xffffu;    // bit i: entry e0 + i
+        const long long e0 = t0 + l0;
+        if (((unsigned long long)(alike2 >> 16) << 16 | alike >> 16) >> l0 && lane == 0 && h == 0 && !is_v)
+            pa::set_error(P.err, PA_DEVERR_SLOT);
+        const bool fresh = __ballot_sync(kFull, off == 0) >> l0 & run;
+        const long long tile = (long long)blk_id * P.n_kv_heads + h;
         const float old = scales[tile];
         // the run's rows are read twice, the second time from L1: holding 16 rotated
         // rows in registers would halve the warps that hide the loads' latency
-        auto row_of = [&](int i) { return reinterpret_cast<const uint4*>(src + (t0 - 1 + l0 + i) * stride + h * D); };
-        auto rotated = [&](const uint4 a, const uint4 b, int i, float (&x)[16]) {  // lanes of a row: row i of the run
-            const int at = __shfl_sync(kFull, pos, min(l0 + i, 31));
+        auto row_of = [&](int i) { return reinterpret_cast<const uint4*>(src + (e0 + i) * stride + h * D); };
+        auto rotated = [&](const uint4 a, const uint4 b, int i, bool use, float (&x)[16]) {  // lanes of a row: entry i
+            const int at = __shfl_sync(kFull, pos, l0 + i);
             widen8(a, x);
             widen8(b, x + 8);
-            if (turn && i < n) {
+            if (turn && use) {
                 float cs[8], sn[8];
                 const float* row = P.cos_sin + (long long)at * P.rot;
                 load8(row + 8 * c, cs);
@@ -309,15 +326,17 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
         float amax = 0.f;  // over finite values
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            if (p * TPP >= n) break;
+            if (LARGE && !(run >> (p * TPP) & ((1u << TPP) - 1))) continue;
+            if (!LARGE && !(run >> (p * TPP))) break;
             const int i = p * TPP + tg;
+            const bool use = run >> i & 1;
             uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (i < n) {
+            if (use) {
                 a = row_of(i)[ca];
                 b = row_of(i)[cb];
             }
             float x[16];
-            rotated(a, b, i, x);
+            rotated(a, b, i, use, x);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const float v = fabsf(x[k]);
@@ -327,16 +346,16 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
 #pragma unroll
         for (int m = 16; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
         const float need = power_scale(amax);
-        const bool fresh = off0 == 0;
         const float s = fresh ? need : fmaxf(old, need);
         const float inv = 1.f / s;  // exact: a power of two
         unsigned char* blk = pool + tile * (kBS * D);
         if (!fresh && s != old) {
             const float ratio = old * inv;
+            const unsigned written = __reduce_or_sync(kFull, lane >= l0 && run >> (lane - l0) & 1 ? 1u << off : 0u);  // slots
 #pragma unroll
             for (int j = 0; j < kBS * D / 16 / 32; ++j) {
                 const int piece = lane + 32 * j, row = piece / (D / 16);
-                if (row >= off0 && row < off0 + n) continue;
+                if (written >> row & 1) continue;
                 uint4* at = reinterpret_cast<uint4*>(blk) + piece;
                 const uint4 u = *at;
                 const uint32_t in[4] = {u.x, u.y, u.z, u.w};
@@ -356,25 +375,27 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            if (p * TPP >= n) break;
+            if (LARGE && !(run >> (p * TPP) & ((1u << TPP) - 1))) continue;
+            if (!LARGE && !(run >> (p * TPP))) break;
             const int i = p * TPP + tg;
+            const bool use = run >> i & 1;
             uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (i < n) {
+            if (use) {
                 a = row_of(i)[ca];
                 b = row_of(i)[cb];
             }
             float x[16];
-            rotated(a, b, i, x);
-            if (i < n) {
+            rotated(a, b, i, use, x);
+            const int to = __shfl_sync(kFull, off, l0 + i);
+            if (use) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k) x[k] *= inv;
-                uint2* row = reinterpret_cast<uint2*>(blk + (off0 + i) * D);
+                uint2* row = reinterpret_cast<uint2*>(blk + to * D);
                 row[ca] = codes8(x);
                 row[cb] = codes8(x + 8);
             }
         }
         if (lane == 0) scales[tile] = s;
-        __syncwarp();  // a second run of the same block in this warp reads what this one wrote
     }
 }
 
@@ -399,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, Form<MODE, LARGE>::kCtasPerSm) rope_
     int cta = blockIdx.x;
     if (MODE == kBlockScale) {
         if (cta < P.kv_ctas) {
-            write_block_scaled<D>(P, cta);
+            write_block_scaled<D, LARGE>(P, cta);
             return;
         }
         cta -= P.kv_ctas;
