@@ -437,8 +437,8 @@ int pa_decode_fp8(void* out, const void* q, const void* k_pool, const void* v_po
  *                    aligned. The write below sets them: the smallest power
  *                    of two 2^e, -32 <= e <= 32, with max |x| <= 448 * 2^e
  *                    over the block's tokens, or a larger one of an earlier
- *                    maximum. The attention calls take any value in
- *                    [2^-32, 2^32] and clamp others to that range.
+ *                    maximum. All calls take any value in [2^-32, 2^32]
+ *                    and read others clamped to that range, NaN as 2^-32.
  * pa_copy_blocks_fp8_block copies blocks with their scales; a swapped block's
  * scales are the row [block] of each array.
  */
@@ -452,7 +452,9 @@ int pa_decode_fp8(void* out, const void* q, const void* k_pool, const void* v_po
  *    (what the block held is void: a block's first slot is written first);
  *  - else they raise the block's scale where they need a larger one, and the
  *    block's other slots are then encoded again: exact, unless the new code is
- *    an E4M3 subnormal (off by at most 2^-10 of the new scale).
+ *    an E4M3 subnormal (off by at most 2^-10 of the new scale). A scale from
+ *    elsewhere that is no power of two is raised to the next one (its codes
+ *    are then rounded once more).
  * Infinite and NaN elements do not enter the maximum. A call's tokens of one
  * block must lie within 16 consecutive entries of slot_mapping, in any order
  * (pa_bm_append_tokens gives them so); skipped entries, and other blocks' tokens,

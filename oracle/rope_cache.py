@@ -80,7 +80,8 @@ def block_scaled_write(x, pool8, scales, slots):
             a = a[np.isfinite(a)]
             need = power_scale(float(a.max()) if a.size else 0.0)
             old = read_scale(sc[blk, h])
-            new = np.float32(need if (off == 0).any() else max(old, need))
+            least = 2.0 ** np.ceil(np.log2(old))  # of a scale from elsewhere: the next power of two
+            new = np.float32(need if (off == 0).any() else max(least, need))
             if not (off == 0).any() and new != old:
                 keep = np.ones(BS, bool)
                 keep[off] = False

@@ -307,7 +307,7 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
             pa::set_error(P.err, PA_DEVERR_SLOT);
         const bool fresh = __ballot_sync(kFull, off == 0) >> l0 & run;
         const long long tile = (long long)blk_id * P.n_kv_heads + h;
-        const float old = scales[tile];
+        const float stored = scales[tile];
         // the run's rows are read twice, the second time from L1: holding 16 rotated
         // rows in registers would halve the warps that hide the loads' latency
         auto row_of = [&](int i) { return reinterpret_cast<const uint4*>(src + (e0 + i) * stride + h * D); };
@@ -346,7 +346,12 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
 #pragma unroll
         for (int m = 16; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
         const float need = power_scale(amax);
-        const float s = fresh ? need : fmaxf(old, need);
+        // as the attention calls read it: a scale from elsewhere may be out of range or NaN
+        const float old = fminf(fmaxf(stored, 0x1p-32f), 0x1p32f);
+        // the next power of two of old: the same, unless it is from elsewhere (to divide by any scale, rather
+        // than multiply by the exact inverse of a power of two, took 15% longer)
+        const float least = __uint_as_float((__float_as_uint(old) + 0x7fffffu) & 0x7f800000u);
+        const float s = fresh ? need : fmaxf(least, need);
         const float inv = 1.f / s;  // exact: a power of two
         unsigned char* blk = pool + tile * (kBS * D);
         if (!fresh && s != old) {
