@@ -606,6 +606,11 @@ int pa_prefill_paged_ex(void* out, const void* q, const void* k_pool, const void
  * of the chunk sees may hold anything; a non-finite V element of a visible
  * position spoils (and flags) the rows that share its key tile, also where it
  * is masked for them, as in pa_prefill_paged.
+ * The P.V product stages V in fp16, scaled by a power of two for every 32 keys:
+ * an element is off by at most 2^-17 of the largest magnitude among their rows
+ * (of 2^-64, where that is smaller). pa_prefill_paged scales all of V by 2^-8 and
+ * so rounds elements below 2^-6 to multiples of 2^-16; where every 32 keys have
+ * an element of 1 or more, both round alike.
  * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG. splits and workspace
  * as for pa_prefill_paged_ex; calls whose kernels may overlap need a workspace
  * each.

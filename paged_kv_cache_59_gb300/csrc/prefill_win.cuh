@@ -34,6 +34,17 @@
 // 1,079 TFLOP/s of visible pairs; 179 us with whole waves, cut tails and a
 // block-wide barrier between segments.
 //
+// bf16 V (EB = 2) is staged in fp16, whose range begins 2^-24: as v 2^-8, as in
+// prefill.cu, elements below 2^-6 lose bits, and a layer whose values are all of
+// magnitude 2^-12 would keep 2 or 3 of 8. So the rows of every 32 keys (a quarter
+// of the softmax) are staged as v 2^(-8 - e), e = min(0, exponent of their largest
+// magnitude), -64 at least: an element is off by at most 2^-17 of that magnitude,
+// 1/32 of a weight's rounding. As with a block's scale below, e enters the
+// exponent, w = 2^(s*scale + e - m), and the sum takes w 2^-e. Where e = 0 the bits
+// are those of prefill.cu. Looking for the magnitude costs 0.5 to 1% where the
+// first rows hold an element of 2 or more, which settles it, else 4 (2,048 rows,
+// window 4,096 + 4 sinks: 128.5 us without it, 129.1 and 132.6 with).
+//
 // E4M3 (EB = 1). The codes of a K and of a V tile (half the bytes) land in a
 // buffer each, and the converter warps widen both to fp16, exactly; Q is
 // converted to fp16 once. Scales never touch the operands: a block's K scale
@@ -53,6 +64,8 @@ namespace {
 template <int EB>
 constexpr int kWinThreads = EB == 2 ? 480 : 448;
 
+constexpr int kLeastExp = -64;  // of 32 keys' V rows (all zero, or too small for every purpose)
+
 // Shared memory, as PfLay: EB = bytes per cached element. With an E4M3 cache the
 // codes of a K and of a V tile land in a buffer of their own (128 rows of D
 // bytes), and the stages hold them widened to fp16.
@@ -70,7 +83,8 @@ struct WinLay {
     static constexpr uint32_t kRawTile = kKT * D;
     static constexpr uint32_t kBars = kRaw + (EB == 1 ? 2 * kRawTile : 0);  // mbarriers
     static constexpr uint32_t kMisc = kBars + 256;       // tmem slot, abort flag
-    static constexpr uint32_t kSmem = kMisc + 64;
+    static constexpr uint32_t kVExp = kMisc + 64;        // bf16: (e, 2^-e) of each V stage's 4 x 32 keys
+    static constexpr uint32_t kSmem = kVExp + (EB == 2 ? kVS * 4 * 8 : 0);
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -139,6 +153,7 @@ struct Segments {
 //   k_full, v_full [stage]  bf16: the K (V) tile landed; E4M3: [0] its codes landed
 //   raw_free [2]            E4M3: K's, V's codes are read (4 converter warps)
 //   k_conv, v_conv [stage]  the converted tile is in its stage (4 converter warps)
+//   v_exp [stage]           bf16: the tile's exponents of V are in their place (4 converter warps)
 //   k_free, v_free [stage]  the last MMA that reads the stage is done
 //   q_full, q_free          the segment's Q is in place (4 converter warps), its last Q.K^T done
 // A wait for a phase passes at once when the barrier is two phases behind, so a
@@ -148,7 +163,7 @@ template <int D, int EB>
 struct Bars {
     static constexpr int kKS = WinLay<D, EB>::kKS, kVS = WinLay<D, EB>::kVS;
     uint64_t* b;
-    static constexpr int kCount = 3 * kKS + 3 * kVS + 2 + 1 + 4 + 1 + 1;
+    static constexpr int kCount = 3 * kKS + 3 * kVS + 2 + 1 + 4 + 1 + 1 + kVS;
     static_assert(kCount * 8 <= 256, "barrier area");
     __device__ __forceinline__ uint64_t* k_full(int i) const { return b + i; }
     __device__ __forceinline__ uint64_t* k_conv(int i) const { return b + kKS + i; }
@@ -162,6 +177,7 @@ struct Bars {
     __device__ __forceinline__ uint64_t* pv_done(int x) const { return b + 3 * kKS + 3 * kVS + 5 + x; }
     __device__ __forceinline__ uint64_t* drain() const { return b + 3 * kKS + 3 * kVS + 7; }
     __device__ __forceinline__ uint64_t* q_free() const { return b + 3 * kKS + 3 * kVS + 8; }
+    __device__ __forceinline__ uint64_t* v_exp(int i) const { return b + 3 * kKS + 3 * kVS + 9 + i; }
 };
 
 // Whether no query of the pair sees the position (its V row is zeroed), and
@@ -335,7 +351,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             uint64_t* b = bars.b + i;
             // the converter warps' barriers take 4 arrivals
             const bool four = (b >= bars.k_conv(0) && b < bars.k_conv(kKS)) || (b >= bars.v_conv(0) && b < bars.v_conv(kVS)) ||
-                              (b >= bars.raw_free(0) && b < bars.raw_free(2)) || b == bars.q_full();
+                              (b >= bars.raw_free(0) && b < bars.raw_free(2)) || b >= bars.v_exp(0) || b == bars.q_full();
             pa::mbar_init(b, four ? 4 : 1);
         }
         pa::fence_mbar_init();
@@ -579,34 +595,56 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 arrive(bars.q_full());
             }
             if constexpr (EB == 2) {
-                const float2 k2 = make_float2(0.00390625f, 0.00390625f);  // 2^-8
-                auto cvt = [&](uint32_t u) {  // bf16 pair -> fp16 pair of v * 2^-8
-                    const float2 f = __fmul2_rn(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), k2);
-                    return float2_to_f16x2(f.x, f.y);
-                };
+                // A warp converts the 32 keys that a quarter of the softmax takes: their largest magnitude
+                // gives the quarter's exponent e. Loops of a few chunks: unrolled further, or with the rows
+                // held in registers from one pass to the other, the code took 3 to 8% more of the whole
+                // kernel's time.
+                const int w4 = warp - 10;
                 for (int j = 0; j < g.n_kt; ++j) {
                     const int J = J0 + j, st = J % kVS, tile = g.kt0 + j;
                     ok = pa::mbar_wait(bars.v_full(st), (uint32_t)((J / kVS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
-                    uint4* vs = reinterpret_cast<uint4*>(sm + L_::kV0 + st * kTile);
-                    auto convert = [&](auto partial) {
-#pragma unroll 4
-                        for (int c = 0; c < (int)(kTile / 2048); ++c) {
-                            const int e = t + 128 * c;
-                            uint4 w = vs[e];
-                            // rows that no query of the pair sees are zero (p = 0 must not meet a NaN)
-                            if constexpr (decltype(partial)::value)
-                                if (hidden_row(P, keys, g.ctx, keys.position(tile, (e & 1023) >> 3))) w = make_uint4(0, 0, 0, 0);
-                            w.x = cvt(w.x);
-                            w.y = cvt(w.y);
-                            w.z = cvt(w.z);
-                            w.w = cvt(w.w);
-                            vs[e] = w;
+                    // chunk c of the lane: 16 bytes of row 32 w4 + 4 (c % 8) + lane / 8, 64-dim half c / 8
+                    constexpr int NC = (int)(kTile / 2048);
+                    uint4* vs = reinterpret_cast<uint4*>(sm + L_::kV0 + st * kTile) + w4 * 256 + lane;
+                    auto at = [](int c) { return (c >> 3) * 1024 + (c & 7) * 32; };
+                    if (hides_rows(keys, g.ctx, tile)) {  // rows that no query of the pair sees are zero (p = 0 must not meet a NaN)
+#pragma unroll 1
+                        for (int c = 0; c < NC; ++c)
+                            if (hidden_row(P, keys, g.ctx, keys.position(tile, 32 * w4 + 4 * (c & 7) + (lane >> 3))))
+                                vs[at(c)] = make_uint4(0, 0, 0, 0);
+                    }
+                    uint32_t most = 0;  // the largest magnitude of either half-word, signs undefined
+                    auto larger = [&](uint32_t u) { asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(most) : "r"(u)); };
+#pragma unroll 1
+                    for (int c = 0; c < NC && !__any_sync(kFull, (most & 0x40004000u) != 0); c += 2) {  // one of 2 or more settles it
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint4 w = vs[at(c + k)];
+                            larger(w.x);
+                            larger(w.y);
+                            larger(w.z);
+                            larger(w.w);
                         }
+                    }
+                    most = __reduce_max_sync(kFull, max(most >> 16 & 0x7fffu, most & 0x7fffu));
+                    const int e = max(kLeastExp, min(0, (int)(most >> 7) - 127));
+                    if (lane == 0) {
+                        reinterpret_cast<float2*>(sm + L_::kVExp)[st * 4 + w4] = make_float2((float)e, __int_as_float((127 - e) << 23));
+                        pa::mbar_arrive(bars.v_exp(st));
+                    }
+                    const float f = __int_as_float((119 - e) << 23);  // 2^(-8 - e)
+                    const float2 f2 = make_float2(f, f);
+                    auto cvt = [&](uint32_t u) {  // bf16 pair -> fp16 pair of v * 2^(-8 - e)
+                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), f2);
+                        return float2_to_f16x2(x.x, x.y);
                     };
-                    if (hides_rows(keys, g.ctx, tile)) convert(std::true_type{});
-                    else convert(std::false_type{});
+#pragma unroll 4
+                    for (int c = 0; c < NC; ++c) {
+                        const uint4 w = vs[at(c)];
+                        vs[at(c)] = make_uint4(cvt(w.x), cvt(w.y), cvt(w.z), cvt(w.w));
+                    }
                     arrive(bars.v_conv(st));
                 }
             } else {
@@ -681,6 +719,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
         const uint32_t tS = tbase + x * 256 + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tO = tS + 128;
         const float sc = P.scale_log2;
+        int vst = 0, vph = 0;  // bf16: V stage and phase parity of the tile
         Segment after;  // the next segment, read while the last P.V of this one runs
         for (bool more = segments.next(g); more; g = after) {
             const KeyTiles keys = segments.keys(g);
@@ -722,9 +761,17 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     vs_next = scale_of(P.v_scale, bid_next);
                     bid_next = block_id(j + 2);
                 }
+                // bf16: the tile's exponents; nearly always there, as V is loaded ahead. A barrier of their own:
+                // waiting for the converted tile took up to 1% longer.
+                if (EB == 2 && ok) ok = pa::mbar_wait(bars.v_exp(vst), (uint32_t)vph, P.err, abort_flag);
                 if (ok) ok = pa::mbar_wait(bars.s_full(x), (uint32_t)(J & 1), P.err, abort_flag);
                 ok = __all_sync(kFull, ok);
                 tc::fence_after_sync();
+                const float2* v_exp = reinterpret_cast<const float2*>(sm + L_::kVExp) + vst * 4;
+                if (++vst == kVS) {
+                    vst = 0;
+                    vph ^= 1;
+                }
                 const int kb = j * kKT + (j < j_win ? kb_sinks : kb_win);
                 // A row does not see keys beyond its position or, sinks apart, before its window. A warp
                 // takes the masking code only for a tile where that hides a key from one of its rows (a
@@ -745,15 +792,15 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 // p of one quarter (raw scores in columns 32q..32q+31) -> fp16 pairs;
                 // P of keys 2w, 2w+1 goes to column 32q + w, so a quarter only
                 // overwrites columns it has already read.
-                // Returns the quarter's sum of p; `add` is what it adds to the row's sum
-                // (E4M3: each block's sum over its V scale).
-                float qk[2] = {sc, sc}, qe[2] = {0.f, 0.f}, qi[2] = {1.f, 1.f};  // E4M3: the quarter's two blocks
+                // Returns the quarter's sum of w; `add` is what it adds to the row's sum
+                // (E4M3: each block's sum over its V scale; bf16: the quarter's times 2^-e).
+                float qk[2] = {sc, sc}, qe[2] = {0.f, 0.f}, qi[2] = {1.f, 1.f};  // E4M3: the quarter's two blocks; bf16: [0]
                 auto exps = [&](auto masked, const uint32_t (&raw)[32], uint32_t visible, uint32_t (&ph)[16], float& add) {
                     float2 qs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
                         const int b = EB == 1 ? w >> 3 : 0;
-                        const float nm = EB == 1 ? qe[b] - m_used : -m_used;
+                        const float nm = qe[b] - m_used;
                         float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])),
                                               EB == 1 ? make_float2(qk[b], qk[b]) : sc2, make_float2(nm, nm));
                         if constexpr (decltype(masked)::value) {  // masked keys give p = 0 (also for a zero scale)
@@ -766,7 +813,10 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         ph[w] = float2_to_f16x2(e.x, e.y);
                     }
                     const float s0 = qs[0].x + qs[0].y;
-                    if constexpr (EB == 2) return add = s0;
+                    if constexpr (EB == 2) {
+                        add = s0 * qi[0];
+                        return s0;
+                    }
                     const float s1 = qs[1].x + qs[1].y;
                     add = s0 * qi[0] + s1 * qi[1];
                     return s0 + s1;
@@ -775,9 +825,14 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 #pragma unroll 1
                     for (int qd = 0; qd < 4; ++qd) {
                         uint32_t raw[32];
+                        float2 ve;  // (read here, its latency is covered by that of the scores)
+                        if constexpr (EB == 2) ve = v_exp[qd];
                         tc::tmem_ld32(tS + 32 * qd, raw);
                         tc::tmem_wait_ld();
-                        if constexpr (EB == 1) {
+                        if constexpr (EB == 2) {
+                            qe[0] = ve.x;
+                            qi[0] = ve.y;
+                        } else {
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
                                 qk[b] = __shfl_sync(kFull, my_k, 2 * qd + b);
@@ -799,7 +854,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                 for (int k = 0; k < 32; ++k) {
                                     const bool vis = !decltype(masked)::value || (visible & (1u << k));
                                     const float r = __uint_as_float(raw[k]);
-                                    if (vis) qmax = fmaxf(qmax, EB == 1 ? fmaf(r, qk[k >> 4], qe[k >> 4]) : r * sc);
+                                    const int b = EB == 1 ? k >> 4 : 0;
+                                    if (vis) qmax = fmaxf(qmax, fmaf(r, qk[b], qe[b]));
                                 }
                                 const float mq = ceilf(qmax);
                                 if (mq > m_used) {
