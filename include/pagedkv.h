@@ -76,12 +76,15 @@ enum pa_device_error {
     PA_DEVERR_SLOT = 2,     /* a slot >= num_blocks * block_size */
     PA_DEVERR_TIMEOUT = 4,  /* an mbarrier / async-copy wait ran out */
     PA_DEVERR_PAIR = 8,     /* a copy_blocks pair outside the pool */
-    PA_DEVERR_CONTEXT = 16, /* a context length beyond 16*max_blocks_per_seq or
-                               max_context_len (the excess is not attended), or a
-                               prefill chunk longer than its context; under a
-                               window with sinks or over block-scaled E4M3 also a
-                               prefill context beyond its table or a chunk beyond
-                               max_chunk_len (the sequence is left out) */
+    PA_DEVERR_CONTEXT = 16, /* a decode context beyond 16*max_blocks_per_seq or
+                               the whole partitions that cover max_context_len
+                               (the excess is not attended), in pa_decode_sinks
+                               and pa_decode_fp8_block any beyond max_context_len
+                               (read as that many tokens); or a prefill chunk
+                               longer than its context, under a window with sinks
+                               or over block-scaled E4M3 also a prefill context
+                               beyond its table or a chunk beyond max_chunk_len
+                               (the sequence is left out) */
     PA_DEVERR_LAYOUT = 32,  /* the shared-memory base was not 1024-byte aligned
                                (prefill; nothing computed) */
     PA_DEVERR_RANGE = 64,   /* a prefill output (or split partial) was not finite:
@@ -361,7 +364,8 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
  * between the sinks and the window may be -1 (pa_bm_release_between). K and V
  * rows of positions that are not visible may hold anything, NaN included.
  * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG; n_sinks = 0 is
- * pa_decode_window. bf16 pools (k_scale, v_scale NULL) or E4M3 pools with
+ * pa_decode_window. A context beyond max_context_len is read as one of
+ * max_context_len tokens and sets PA_DEVERR_CONTEXT. bf16 pools (k_scale, v_scale NULL) or E4M3 pools with
  * per-head scales (both given); workspace as for pa_decode_ex. partition_tokens
  * 0: on the tensor-core kernel (E4M3 or sinks) 512 .. 2048, by how the call
  * fills the GPU, instead of pa_decode_partition_tokens; of up to 4 sequences,

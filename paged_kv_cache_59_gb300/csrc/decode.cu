@@ -74,6 +74,7 @@ struct DecodeParams {
     int max_parts;
     int window;  // >= 0: the query at position ctx-1 sees positions ctx-1-window .. ctx-1
     int n_sinks; // and, with a window, positions 0 .. n_sinks-1
+    int max_ctx; // a longer context is flagged and read as this many tokens (INT_MAX: no such bound)
     unsigned int* err;
     // optional plan (pa_decode_planned): CTA i runs item i = (partition, KV head,
     // sequence, unused) instead of the one its grid position names
@@ -121,6 +122,14 @@ __device__ __forceinline__ bool cta_item(const DecodeParams& P, int& p, int& kvh
         return false;
     }
     return true;
+}
+
+// A sequence's context, within the call's bound.
+__device__ __forceinline__ int context_of(const DecodeParams& P, int b, bool flag) {
+    const int ctx = P.ctx[b];
+    if (ctx <= P.max_ctx) return ctx;
+    if (flag) pa::set_error(P.err, PA_DEVERR_CONTEXT);
+    return P.max_ctx;
 }
 
 // The blocks a sequence of ctx > 0 tokens attends to: the leading n_sink_blk
@@ -319,7 +328,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
     int p, kvh, b;
     if (!cta_item<SINKS>(P, p, kvh, b)) return;
     const int h0 = kvh * G;
-    const int ctx = P.ctx[b];
+    const int ctx = context_of(P, b, p == 0 && threadIdx.x == 0);
 
     if (ctx <= 0) {  // empty sequence: zero output rows, written once
         if (p == 0) {
@@ -746,7 +755,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
         if (threadIdx.x == 0) pa::set_error(P.err, PA_DEVERR_LAYOUT);
         return;
     }
-    const int ctx = P.ctx[b];
+    const int ctx = context_of(P, b, p == 0 && threadIdx.x == 0);
     if (ctx <= 0) {  // empty sequence: zero output rows, written once
         if (p == 0) {
             for (int e = threadIdx.x; e < G * D / 2; e += NW * 32) {
@@ -1158,7 +1167,7 @@ pa_decode_merge_kernel(const DecodeParams P, int n_rows) {
     if (row >= n_rows) return;
     const int H = P.n_heads;
     const int b = row / H;
-    const int ctx = P.ctx[b];
+    const int ctx = context_of(P, b, false);
     if (ctx <= 0) return;
     const int nparts = Span<true>(P, ctx).nparts;
     if (nparts <= 1) return;  // the partition kernel wrote this row
@@ -1216,7 +1225,7 @@ pa_decode_merge_wide_kernel(const DecodeParams P, int n_rows) {
     const int d = (warp % W) * 32 + lane;
     pa::grid_dependency_wait();  // every partition's partial is written
     if (row >= n_rows) return;
-    const int ctx = P.ctx[row / P.n_heads];
+    const int ctx = context_of(P, row / P.n_heads, false);
     if (ctx <= 0) return;
     const int nparts = Span<true>(P, ctx).nparts;
     if (nparts <= 1) return;  // the partition kernel wrote this row
@@ -1466,7 +1475,7 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
                 int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len, int num_blocks,
                 int window, int partition_tokens, void* workspace, size_t workspace_bytes,
                 pa_stream_t stream, bool force_tc = false, const int32_t* items = nullptr, int n_items = 0,
-                int n_sinks = 0, bool block_scaled = false, bool spread = false) {
+                int n_sinks = 0, bool block_scaled = false, bool spread = false, bool exact_bound = false) {
     if (n_seqs < 0 || max_context_len < 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
         n_heads <= 0 || n_kv_heads <= 0)
         return PA_ERR_INVALID_ARG;
@@ -1539,6 +1548,7 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     P.max_parts = max_parts;
     P.window = window;
     P.n_sinks = n_sinks;
+    P.max_ctx = exact_bound ? max_context_len : 0x7fffffff;
     P.err = err;
     P.items = reinterpret_cast<const int4*>(items);
     P.n_items = n_items;
@@ -1629,7 +1639,7 @@ extern "C" int pa_decode_sinks(void* out, const void* q, const void* k_pool, con
     return decode_impl(k_scale ? 1 : 2, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
                        n_heads, n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len,
                        num_blocks, window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0,
-                       n_sinks, false, k_scale || n_sinks > 0);
+                       n_sinks, false, k_scale || n_sinks > 0, true);
 }
 
 extern "C" int pa_decode_fp8_block(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -1644,7 +1654,7 @@ extern "C" int pa_decode_fp8_block(void* out, const void* q, const void* k_pool,
     return decode_impl(1, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, n_heads,
                        n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len, num_blocks,
                        window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0, n_sinks, true,
-                       true);
+                       true, true);
 }
 
 extern "C" int pa_decode(void* out, const void* q, const void* k_pool, const void* v_pool,
