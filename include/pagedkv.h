@@ -368,8 +368,9 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
  * max_context_len tokens and sets PA_DEVERR_CONTEXT. bf16 pools (k_scale, v_scale NULL) or E4M3 pools with
  * per-head scales (both given); workspace as for pa_decode_ex. partition_tokens
  * 0: on the tensor-core kernel (E4M3 or sinks) 512 .. 2048, by how the call
- * fills the GPU, instead of pa_decode_partition_tokens; of up to 4 sequences,
- * those far below max_context_len are cut into smaller partitions.
+ * fills the GPU, instead of pa_decode_partition_tokens; where sequences may
+ * attend to 16,384 tokens or more, those far below that are cut into smaller
+ * partitions.
  * A workspace serves one call at a time: calls, or captured graphs of them,
  * whose kernels may overlap need one each.
  */

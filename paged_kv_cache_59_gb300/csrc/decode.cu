@@ -1397,15 +1397,23 @@ int wave_partition_tokens(int n_seqs, int n_kv_heads, int context, int sms, int 
 // The same for the tensor-core kernel in pa_decode_sinks (but for a bf16 window
 // without sinks) and pa_decode_fp8_block. A call that leaves CTA slots empty
 // takes as long as its longest partition, and one that fills them as many
-// rounds; a round costs its partition and about 128 tokens more. Measured with
-// 1024 tokens and with this rule (E4M3, 32/8 and 64/8 heads): 1 sequence of 4,096
-// tokens 15.2 and 10.2 us (512), 2 of 16,384 18.8 and 15.6, 1 of 131,072 54.9
-// and 49.3 (1792), 4 of 100,000 .. 121,596 166 and 157. Where max_context_len is
-// far above a sequence's length, the kernel cuts it smaller (Span). Batches
-// differ in their lengths, so rounds say little for them: more than 4 sequences
-// take 1024 tokens, or fewer when that still is a single round (24 of 1,100
-// tokens: 19.6 and 14.9 us).
-constexpr int kFewSeqs = 4;
+// rounds; a round costs its partition and about 128 tokens more. Calls over long
+// spans take the size of least rounds x (size + 128), and where max_context_len is
+// far above a sequence's length the kernel cuts it smaller (Span), so that every
+// sequence has about as many partitions. Over short spans a sequence has a few
+// partitions, whose number differs with its length, so rounds of the bound say
+// little: 1024 tokens, or fewer when that still is a single round (24 of 1,100
+// tokens: 19.6 and 14.9 us). Measured against 1024 tokens throughout (E4M3, 32/8
+// and 64/8 heads, 1 to 32 sequences):
+//   131,072 (1 sequence)               54.9 us, 49.3
+//   16,384 each                        -2.5 to -21% (5: 40.1, 31.6; 32: 167, 163)
+//   99,999 .. 131,072, 5 and more      -2 to -6% (8: 296, 282)
+//   8,192 .. 32,768                    -8 to +2%, mean -2.5%
+//   4,096 .. 16,384                    -14 to +10%, mean -1.5%
+//   4,096, bound 131,072               -11 to -24% (5: 24.3, 18.6)
+//   10,000 .. 40,000, bound 131,072    +2 to +8% from 5 sequences on
+//   128 .. 4,096                       +3 to +20% (32: 27.4, 32.6), so short
+constexpr int kLongSpan = 16384;
 int mma_partition_tokens(int eb, int n_seqs, int n_kv_heads, int span) {
     const int sms = sm_count();
     const long long slots = (long long)sms * (eb == 1 ? 4 : 3) - sms / 16;  // see mma::Lay; a few may be late
@@ -1415,17 +1423,22 @@ int mma_partition_tokens(int eb, int n_seqs, int n_kv_heads, int span) {
     for (int pt = kDefaultPartitionTokens; pt <= 4 * kDefaultPartitionTokens; pt += 64) {
         const long long rounds = ((long long)n_seqs * n_kv_heads * ((span + pt - 1) / pt) + slots - 1) / slots;
         const long long cost = rounds * (pt + 128);
-        if (n_seqs > kFewSeqs ? rounds > 1 || pt >= best : least > 0 && cost > least) continue;
+        if (span >= kLongSpan ? least > 0 && cost > least : rounds > 1 || pt >= best) continue;
         least = cost;
         best = pt;
     }
     return best;
 }
 
+// The most tokens a sequence attends to: its context, or a window and its sinks.
+int attended_span(int max_context_len, int window, int n_sinks) {
+    const long long wide = (long long)window + n_sinks + (n_sinks > 0 ? 3 : 2) * kBS;
+    return window >= 0 && wide < max_context_len ? (int)wide : max_context_len;
+}
+
 int default_partition_tokens(bool tensor, int eb, int n_seqs, int n_kv_heads, int G, int head_dim,
                              int max_context_len, int window, int n_sinks = 0, bool spread = false) {
-    const long long wide = (long long)window + n_sinks + (n_sinks > 0 ? 3 : 2) * kBS;  // a window and its sinks
-    const int span = window >= 0 && wide < max_context_len ? (int)wide : max_context_len;
+    const int span = attended_span(max_context_len, window, n_sinks);
     if (tensor) return spread ? mma_partition_tokens(eb, n_seqs, n_kv_heads, span) : 2 * kDefaultPartitionTokens;
     const int sms = sm_count();
     return wave_partition_tokens(n_seqs, n_kv_heads, span, sms, sms * k1_ctas_per_sm(head_dim, G, eb));
@@ -1544,7 +1557,8 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     P.max_blocks = max_blocks_per_seq;
     P.num_blocks = num_blocks;
     P.part_blocks = P.part_least = pt / kBS;
-    if (partition_tokens == 0 && tensor && spread && n_seqs <= kFewSeqs) P.part_least = kDefaultPartitionTokens / kBS;
+    if (partition_tokens == 0 && tensor && spread && attended_span(max_context_len, window, n_sinks) >= kLongSpan)
+        P.part_least = kDefaultPartitionTokens / kBS;
     P.max_parts = max_parts;
     P.window = window;
     P.n_sinks = n_sinks;
