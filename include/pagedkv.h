@@ -325,6 +325,9 @@ int pa_copy_blocks_ex(void* k_pool, void* v_pool, const int64_t* block_mapping, 
  * pa_swap_in_blocks:  pool block block_ids[i] := host[i].
  * Asynchronous on stream: the host copy is complete once the stream is; a
  * swap-in must be ordered before any kernel that reads those blocks.
+ * Of an fp8 cache with a scale per block these calls move the codes alone: the
+ * rows block_ids[i] of k_scale and v_scale are the caller's to keep and to put
+ * at the new ids, as the codes mean nothing without them.
  */
 int pa_swap_out_blocks(const void* k_pool, const void* v_pool, const int32_t* block_ids, int n_blocks,
                        void* host_k, void* host_v, int n_kv_heads, int head_dim, int block_size,
@@ -444,8 +447,9 @@ int pa_decode_fp8(void* out, const void* q, const void* k_pool, const void* v_po
  *                    over the block's tokens, or a larger one of an earlier
  *                    maximum. All calls take any value in [2^-32, 2^32]
  *                    and read others clamped to that range, NaN as 2^-32.
- * pa_copy_blocks_fp8_block copies blocks with their scales; a swapped block's
- * scales are the row [block] of each array.
+ * pa_copy_blocks_fp8_block copies blocks with their scales; pa_swap_out_blocks
+ * and pa_swap_in_blocks leave a block's scales, the row [block] of each array, to
+ * the caller.
  */
 
 /*

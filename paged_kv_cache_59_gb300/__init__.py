@@ -215,7 +215,8 @@ def _swap_args(k_pool, host_k, host_v, block_ids):
 
 def pa_swap_out_blocks(k_pool, v_pool, block_ids, host_k, host_v, stream=None) -> None:
     """host_k[i], host_v[i] := pool block block_ids[i] (K and V, all heads);
-    host buffers page-locked, block_ids int32 on the device."""
+    host buffers page-locked, block_ids int32 on the device. Scales per block
+    stay behind: keep k_scale[block_ids] and v_scale[block_ids] beside them."""
     n, hk, d, bs, eb, nb, ids = _swap_args(k_pool, host_k, host_v, block_ids)
     st = load().pa_swap_out_blocks(_ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"), ids, n,
                                    _host_pinned(host_k, "host_k"), _host_pinned(host_v, "host_v"), hk, d, bs,
@@ -224,7 +225,8 @@ def pa_swap_out_blocks(k_pool, v_pool, block_ids, host_k, host_v, stream=None) -
 
 
 def pa_swap_in_blocks(host_k, host_v, k_pool, v_pool, block_ids, stream=None) -> None:
-    """pool block block_ids[i] := host_k[i], host_v[i]."""
+    """pool block block_ids[i] := host_k[i], host_v[i]. Of a cache with a scale
+    per block, put the kept rows at k_scale[block_ids] and v_scale[block_ids] too."""
     n, hk, d, bs, eb, nb, ids = _swap_args(k_pool, host_k, host_v, block_ids)
     st = load().pa_swap_in_blocks(_host_pinned(host_k, "host_k"), _host_pinned(host_v, "host_v"),
                                   _ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"), ids, n, hk, d, bs, eb, nb,

@@ -84,13 +84,15 @@ struct DecodeParams {
     int parts_last;  // the grid is (KV heads, sequences, partitions)
 };
 
-// The grid of a partition kernel. Under a window with sinks every sequence has as
-// many partitions, the last of them short: those run last, and fill the end of
-// the last wave (32 windows of 4,096 + 4, 32/8 heads: bf16 91.5 us with the
-// partitions of a sequence side by side, 87.8 so, E4M3 49.8 and 48.6; 16 with
-// 64/8 heads: E4M3 29.4 and 27.7, but bf16 51.3 and 52.6). Contexts of different
-// lengths are better off side by side (64 of 128 .. 4,096 tokens, E4M3: 46.0 us,
-// 47.2 otherwise).
+// The grid of a partition kernel. Under a window with sinks a sequence longer than
+// the window has a fixed number of partitions, the last of them short: the
+// sequences' first partitions run first, their last ones last, and fill the end of
+// the last wave. Against the partitions of a sequence side by side (bf16 and E4M3,
+// 32/8 and 64/8 heads, 4 to 100 sequences): windows of 4,096 + 4 from 5.6% faster
+// to 2.6% slower (32 in bf16: 91.3 and 89.2 us), of 1,024 + 4 from 17% to -3.6%.
+// Shorter contexts gain too while they are few (16 and 32 of 128 .. 4,096 tokens:
+// 16% to -3%), and lose where there are many (64: +1 to -3.6%). Without a window
+// they are side by side (64 of 128 .. 4,096 tokens, E4M3: 46.0 us, 47.2 otherwise).
 dim3 grid_of(const DecodeParams& P, int n_seqs) {
     if (P.items) return dim3((unsigned)P.n_items);
     return P.parts_last ? dim3(P.n_kv_heads, n_seqs, P.max_parts) : dim3(P.max_parts, P.n_kv_heads, n_seqs);
