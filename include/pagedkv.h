@@ -470,7 +470,8 @@ int pa_decode_fp8(void* out, const void* q, const void* k_pool, const void* v_po
  * may lie between them. A token further from the first of its block is not
  * written and sets PA_DEVERR_SLOT when another one of the block precedes it by
  * fewer than 16 entries; otherwise the block's two groups race.
- * Arguments as for pa_rope_and_cache, with rot_dim = 0 for a plain write.
+ * Arguments as for pa_rope_and_cache, with rot_dim = 0 for a plain write. K and V
+ * need a pool and a scale array each (PA_ERR_INVALID_ARG).
  */
 int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const void* v, void* k_pool,
                                 void* v_pool, float* k_scale, float* v_scale, const float* cos_sin,

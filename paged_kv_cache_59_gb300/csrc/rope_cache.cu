@@ -505,6 +505,8 @@ int rope_impl(RopeParams& P, int head_dim, int block_size, int num_blocks, pa_st
     } else {
         P.n_heads = 0;
     }
+    // K's and V's warps work on one block at the same time
+    if (MODE == kBlockScale && (P.k_pool == P.v_pool || P.k_block_scale == P.v_block_scale)) return PA_ERR_INVALID_ARG;
     P.pool_slots = (long long)num_blocks * kBS;
     P.err = pa_device_error_ptr();
     if (!P.err) return PA_ERR_CUDA;
