@@ -360,7 +360,10 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
  * Sliding window with sinks: as pa_decode_window, and positions 0 ..
  * n_sinks - 1 stay visible too, however long the sequence (the first tokens
  * collect attention that has nowhere else to go; a model that loses them
- * answers worse than one that keeps them). The query at i = context_lens[b]-1
+ * answers worse than one that keeps them). This is the mask alone: positions stay
+ * those that k was rotated by, so the sinks' distance grows with the sequence. A
+ * scheme that counts positions within the kept tokens only has to keep k, and
+ * rotate it, itself. The query at i = context_lens[b]-1
  * attends to t <= i with t >= i - window or t < n_sinks:
  *     out[b][h] = sum_t softmax_t(scale * q[b][h] . K_b[t]) V_b[t].
  * Only blocks with such a position are read: table entries of the blocks
@@ -368,8 +371,9 @@ int pa_decode_window(void* out, const void* q, const void* k_pool, const void* v
  * rows of positions that are not visible may hold anything, NaN included.
  * window >= 0 and n_sinks >= 0, else PA_ERR_INVALID_ARG; n_sinks = 0 is
  * pa_decode_window. A context beyond max_context_len is read as one of
- * max_context_len tokens and sets PA_DEVERR_CONTEXT. bf16 pools (k_scale, v_scale NULL) or E4M3 pools with
- * per-head scales (both given); workspace as for pa_decode_ex. partition_tokens
+ * max_context_len tokens and sets PA_DEVERR_CONTEXT. bf16 pools (k_scale,
+ * v_scale NULL) or E4M3 pools with per-head scales (both given); workspace as for
+ * pa_decode_ex. partition_tokens
  * 0: on the tensor-core kernel (E4M3 or sinks) 512 .. 2048, by how the call
  * fills the GPU, instead of pa_decode_partition_tokens; where sequences may
  * attend to 16,384 tokens or more, those far below that are cut into smaller
@@ -494,9 +498,10 @@ int pa_copy_blocks_fp8_block(void* k_pool, void* v_pool, float* k_scale, float* 
  *     K_b[t] = code * k_scale[block of t][kv head], V_b[t] likewise.
  * window -1: every position; window >= 0: as pa_decode_sinks, n_sinks too
  * (n_sinks is ignored without a window). Workspace and kernels as for
- * pa_decode_fp8; default partitions as for pa_decode_sinks. V's scale is folded into the softmax weight, w = p *
- * v_scale = 2^(s + log2 v_scale - m), which enters the P.V product as one
- * fp16 term at head_dim 128: within 2^-11 of w, or 2^-25 of the reference weight.
+ * pa_decode_fp8; default partitions and a context beyond max_context_len as for
+ * pa_decode_sinks. V's scale is folded into the softmax weight, w = p * v_scale
+ * = 2^(s + log2 v_scale - m), which enters the P.V product as one fp16 term at
+ * head_dim 128: within 2^-11 of w, or 2^-25 of the reference weight.
  */
 int pa_decode_fp8_block(void* out, const void* q, const void* k_pool, const void* v_pool,
                         const float* k_scale, const float* v_scale, const int32_t* block_tables,
@@ -641,6 +646,8 @@ int pa_prefill_sinks(void* out, const void* q, const void* k_pool, const void* v
  * |q| in its normal range, 2^-14 .. 65504; larger ones give non-finite outputs
  * and set PA_DEVERR_RANGE), and the softmax weight times V's scale is rounded
  * to fp16, as in pa_decode_fp8_block.
+ * A cache with per-head scales (pa_reshape_and_cache_fp8) is one whose rows of
+ * k_scale, and of v_scale, are all the same.
  */
 int pa_prefill_fp8_block(void* out, const void* q, const void* k_pool, const void* v_pool,
                          const float* k_scale, const float* v_scale, const int32_t* block_tables,
