@@ -30,9 +30,9 @@
 // 1.47. Converters that load V (E4M3: K and V) themselves, a tile ahead in
 // registers instead of by TMA, took 1.82, and 270 us instead of 201 for four
 // chunks whose cache comes from HBM.
-// 2,048 rows, window 4,096 + 4 sinks (256 items of 33 tiles on 152 SMs): 127.5 us,
-// 1,079 TFLOP/s of visible pairs; 179 us with whole waves, cut tails and a
-// block-wide barrier between segments.
+// 2,048 rows, window 4,096 + 4 sinks (256 items of 33 tiles on 152 SMs): 129.1 us on
+// one cache, 1,066 TFLOP/s of visible pairs, 132.6 over three in turn; 179 us with
+// whole waves, cut tails and a block-wide barrier between segments.
 //
 // bf16 V (EB = 2) is staged in fp16, whose range begins 2^-24: as v 2^-8, as in
 // prefill.cu, elements below 2^-6 lose bits, and a layer whose values are all of
@@ -376,7 +376,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
         // A stage is refilled as soon as its last reader is done. bf16: K and V have a warp each:
         // when a tile's load waits in line behind the other operand's, the tensor core waits for it
         // (one warp for both: 11% more a tile). E4M3, half the bytes and boxes: one warp for both
-        // (a second one takes issue slots from the softmax: 5% more a tile); K(J)'s codes replace K(J-1)'s once those are widened, V's likewise.
+        // (a second one takes issue slots from the softmax: 5% more a tile); K(J)'s codes replace
+        // K(J-1)'s once those are widened, V's likewise.
         constexpr int kBoth = EB == 1;
         constexpr uint32_t kBytes = EB == 2 ? kTile : L_::kRawTile;
         // bf16: lane l < 8 kNH moves box (block l / kNH, dims 64 g .., g = l % kNH); E4M3: lane
@@ -609,7 +610,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     constexpr int NC = (int)(kTile / 2048);
                     uint4* vs = reinterpret_cast<uint4*>(sm + L_::kV0 + st * kTile) + w4 * 256 + lane;
                     auto at = [](int c) { return (c >> 3) * 1024 + (c & 7) * 32; };
-                    if (hides_rows(keys, g.ctx, tile)) {  // rows that no query of the pair sees are zero (p = 0 must not meet a NaN)
+                    if (hides_rows(keys, g.ctx, tile)) {  // no query of the pair sees: zero (p = 0 must not meet a NaN)
 #pragma unroll 1
                         for (int c = 0; c < NC; ++c)
                             if (hidden_row(P, keys, g.ctx, keys.position(tile, 32 * w4 + 4 * (c & 7) + (lane >> 3))))
@@ -1018,9 +1019,9 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 // and 190 us for two of 1,024 rows, 231, 204, 202 and 207 us for four of 512
 // rows behind 700 .. 16,384 tokens). The costs of all non-empty items, in item
 // order, are cut into C runs of equal length, C the CTAs (fewer when a run would
-// be shorter than kStart + 4), so that all CTAs finish together: each has at most one piece of an item begun
-// by the CTA before, whole items, and one piece of an item that the next CTA
-// goes on with. (A window makes the items equally long and few waves deep: 256
+// be shorter than kStart + 4), so that all CTAs finish together: each has at most
+// one piece of an item begun by the CTA before, whole items, and one piece of an
+// item that the next CTA goes on with. (A window makes the items equally long and few waves deep: 256
 // items of 33 tiles on 152 CTAs take 4 segments on the busiest CTA with whole
 // waves and cut tails, 2 or 3 here, and no CTA idles.) A cut that would leave
 // fewer than kLeast tiles on one side moves to that end of the item. When the

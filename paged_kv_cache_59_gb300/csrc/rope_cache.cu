@@ -411,7 +411,7 @@ __device__ __forceinline__ void write_block_scaled(const RopeParams& P, int cta)
 // cache, whatever spills. Measured small / large (64 / 8,192 tokens of 64/8
 // heads of 128 in bf16; 64 tokens / 6,742 in ragged chunks of 32/8 heads in
 // E4M3): 2.2 / 54.1 us and 2.9 / 35.4 us in the first form, 2.4 / 52.6 and 3.8 /
-// 30.8 in the second.
+// 30.8 in the second (E4M3 before runs were found by block: 3.0 and 32.0 us now).
 template <int MODE, bool LARGE>
 struct Form {
     static constexpr int U = LARGE && MODE == kBlockScale ? 2 : 4;
@@ -467,10 +467,12 @@ int launch(RopeParams& P, cudaStream_t stream) {
     if (MODE == kBlockScale) {
         const long long units = 2LL * P.n_kv_heads;
         // K/V warps look at one token each while that is one wave of them. Beyond it a warp
-        // takes several: 16 suit prompt chunks (30.8 us against 34.2 with 4 for 6,742 tokens),
-        // where a warp finds one run, but a decode batch has a run per token and its warps
-        // would work through 16 (2,048 sequences: 39.9 us against 22.6), so calls that can
-        // still be one take 4.
+        // takes several: 16 suit prompt chunks, where a warp finds one run (6,742 tokens: 32.0 us,
+        // 35 with 4), but a decode batch has a run per token and its warps would work through
+        // 16 of them (1,024 and 2,048 sequences: 38.1 and 44.0 us, 12.8 and 24.4 with 4). The
+        // host cannot tell one from the other, so calls that can still be a batch take 4, which
+        // costs a prompt of 2,048 tokens 4% and one of 4,096 15% (13.2 and 23.5 us, 12.8 and
+        // 20.4 with 16).
         P.tokens_per_warp = P.n_tokens * units <= 16LL * kWarps * sms ? 1 : P.n_tokens <= 4096 ? 4 : 16;
         const long long warps = ((long long)P.n_tokens + P.tokens_per_warp - 1) / P.tokens_per_warp * units;
         kv = (warps + kWarps - 1) / kWarps;
