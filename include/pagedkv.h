@@ -73,7 +73,8 @@ enum pa_status {
 /* Bits of the device error word. */
 enum pa_device_error {
     PA_DEVERR_BLOCK_ID = 1, /* a block-table entry outside [0, num_blocks) */
-    PA_DEVERR_SLOT = 2,     /* a slot >= num_blocks * block_size */
+    PA_DEVERR_SLOT = 2,     /* a slot >= num_blocks * block_size, or tokens of one block
+                               too far apart in a block-scaled cache write */
     PA_DEVERR_TIMEOUT = 4,  /* an mbarrier / async-copy wait ran out */
     PA_DEVERR_PAIR = 8,     /* a copy_blocks pair outside the pool */
     PA_DEVERR_CONTEXT = 16, /* a decode context beyond 16*max_blocks_per_seq or
