@@ -79,13 +79,14 @@ enum pa_device_error {
     PA_DEVERR_PAIR = 8,     /* a copy_blocks pair outside the pool */
     PA_DEVERR_CONTEXT = 16, /* a decode context beyond 16*max_blocks_per_seq or
                                the whole partitions that cover max_context_len
-                               (the excess is not attended), in pa_decode_sinks
-                               and pa_decode_fp8_block any beyond max_context_len
+                               (the excess is not attended), in pa_decode_sinks,
+                               pa_decode_fp8_block and pa_decode_score_mod any
+                               beyond max_context_len
                                (read as that many tokens); or a prefill chunk
                                longer than its context, under a window with sinks
-                               or over block-scaled E4M3 also a prefill context
-                               beyond its table or a chunk beyond max_chunk_len
-                               (the sequence is left out) */
+                               over block-scaled E4M3 or with reshaped scores also
+                               a prefill context beyond its table or a chunk
+                               beyond max_chunk_len (the sequence is left out) */
     PA_DEVERR_LAYOUT = 32,  /* the shared-memory base was not 1024-byte aligned
                                (prefill; nothing computed) */
     PA_DEVERR_RANGE = 64,   /* a prefill output (or split partial) was not finite:
@@ -94,7 +95,8 @@ enum pa_device_error {
                                non-finite inputs */
     PA_DEVERR_PLAN = 128,   /* a pa_decode_planned item outside the call's bounds
                                (that CTA did nothing) */
-    PA_DEVERR_POSITION = 256 /* a token position beyond the rotation table
+    PA_DEVERR_POSITION = 256 /* a token position beyond the rotation table, or a
+                               kept position that pa_compact_blocks cannot use
                                (that token was skipped) */
 };
 
@@ -658,6 +660,100 @@ int pa_prefill_fp8_block(void* out, const void* q, const void* k_pool, const voi
                          int n_sinks, int splits, void* workspace, size_t workspace_bytes,
                          pa_stream_t stream);
 
+/* ------------------------------------------------------- reshaped scores */
+
+/*
+ * Decode whose scores are reshaped before the softmax, for models that cap their
+ * logits, that weigh keys by their distance instead of rotating them, or both.
+ * With s = scale * q[b][h] . K_b[t] and i = context_lens[b] - 1:
+ *     z = softcap * tanh(s / softcap)        (softcap > 0; else z = s)
+ *     z = z - alibi_slopes[h] * (i - t)      (alibi_slopes given)
+ *     out[b][h] = sum_t softmax_t(z) V_b[t]
+ * over the positions of pa_decode_sinks (window >= 0, n_sinks), or all (window
+ * -1: n_sinks is ignored).
+ *  softcap       0 (none), or positive with scale / softcap finite, else
+ *                PA_ERR_INVALID_ARG
+ *  alibi_slopes  fp32 [n_heads], device memory, 4-byte aligned, finite; NULL: no
+ *                bias. Distances count cache positions: a cache compacted by
+ *                pa_compact_blocks has lost those that its tokens were written at
+ *  k_scale, v_scale  both NULL: bf16 pools; both given: E4M3 pools with a scale per
+ *                (block, KV head), fp32 [num_blocks][n_kv_heads]. (A cache with
+ *                scales per head serves as one whose blocks all have them.)
+ * tanh is computed in fp32 to a few 2^-23; the scores' other arithmetic, the
+ * partitions, the workspace, a context beyond max_context_len and the errors are
+ * those of pa_decode_sinks and pa_decode_fp8_block.
+ */
+int pa_decode_score_mod(void* out, const void* q, const void* k_pool, const void* v_pool,
+                        const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                        const int32_t* context_lens, float scale, float softcap,
+                        const float* alibi_slopes, int n_heads, int n_kv_heads, int head_dim,
+                        int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len,
+                        int num_blocks, int window, int n_sinks, int partition_tokens,
+                        void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * The same scores for prompt chunks: pa_prefill_paged_ex, row at position p,
+ *     z = softcap * tanh(s / softcap) - alibi_slopes[h] * |p - t|.
+ *  prefix_lens   int32 [n_seqs], device memory: a row sees the positions before
+ *                prefix_lens[s] whether or not they come after its own (a prompt,
+ *                or its images, read in both directions), as far as they are in
+ *                the cache: t < min(prefix_lens[s], context_lens[s]). So a prefix
+ *                belongs in the cache before the chunk that begins it is computed.
+ *                NULL, or an entry <= 0: causal
+ * Row p attends to t <= p and t < prefix, of those, under a window (window >= 0),
+ * to t >= p - window or t < n_sinks. (Decode needs no prefix: its query comes last.)
+ * K and V beyond what a row sees may hold anything, as in pa_prefill_sinks; V's
+ * staging, splits, the workspace and the errors are as there, over E4M3 as in
+ * pa_prefill_fp8_block. softcap, alibi_slopes, k_scale and v_scale as in
+ * pa_decode_score_mod.
+ */
+int pa_prefill_score_mod(void* out, const void* q, const void* k_pool, const void* v_pool,
+                         const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                         const int32_t* context_lens, const int32_t* q_start_loc, float scale,
+                         float softcap, const float* alibi_slopes, const int32_t* prefix_lens,
+                         int n_heads, int n_kv_heads, int head_dim, int block_size, int n_seqs,
+                         int max_blocks_per_seq, int max_chunk_len, int num_blocks, int window,
+                         int n_sinks, int splits, void* workspace, size_t workspace_bytes,
+                         pa_stream_t stream);
+
+/* ------------------------------------------------------------ compaction */
+
+/*
+ * Drops tokens from the middle of sequences: the tokens that stay move, in place,
+ * to the sequence's first positions ([DR] "Paged KV: virtual memory for tokens":
+ * memory comes free by the block, so a dropped token frees nothing until the
+ * others are moved together). For sequence s, with a = keep_start_loc[s], and
+ * every KV head, in K and V:
+ *     position j := what position keep[a + j] held,   0 <= j < keep_start_loc[s+1] - a.
+ * What the table's later positions hold afterwards is undefined; slots behind the
+ * last kept token in its block, and positions that stay in place at the beginning
+ * of the sequence, in blocks before the first that moves, are not written. Keys
+ * keep the rotation of the position they were written at.
+ *  block_tables    int32 [n_seqs][max_blocks_per_seq]: the tables before the call
+ *  keep            int32 [keep_heads][n_kept], keep_heads 1 (one list for all KV
+ *                  heads) or n_kv_heads; within a sequence strictly ascending,
+ *                  >= 0, positions the sequence holds
+ *  keep_start_loc  int32 [n_seqs + 1], non-decreasing, within [0, n_kept]
+ *  elem_bytes      2: bf16 pools; 1: E4M3 pools
+ *  k_scale,v_scale fp32 [num_blocks][n_kv_heads] of an E4M3 cache with a scale per
+ *                  block, which are updated: a block takes the largest of its new
+ *                  tokens' scales (read within [2^-32, 2^32]), and codes of tokens
+ *                  from blocks with a smaller one are encoded again (exact, unless
+ *                  the new code is an E4M3 subnormal or the quotient of the scales
+ *                  no power of two: then off by at most half a step). Both NULL
+ *                  otherwise: the elements are moved as they are
+ * A position that is out of order or beyond the table sets PA_DEVERR_POSITION, one
+ * in a block outside the pool PA_DEVERR_BLOCK_ID: that token is skipped, its new
+ * position keeps its bytes. No block that the call writes may be in another
+ * sequence's table of the same call, nor shared otherwise (pa_bm_compact gives
+ * private copies). head_dim 64 or 128, pools 16-byte aligned.
+ */
+int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                      const int32_t* block_tables, const int32_t* keep, const int32_t* keep_start_loc,
+                      int keep_heads, int n_kept, int n_kv_heads, int head_dim, int block_size,
+                      int elem_bytes, int n_seqs, int max_blocks_per_seq, int num_blocks,
+                      pa_stream_t stream);
+
 /* ----------------------------------------------------------- diagnostics */
 
 /* Reads the current device's error word into *flags_out (a PA_DEVERR_* mask)
@@ -735,6 +831,23 @@ int pa_bm_release_before(pa_bm* bm, int64_t seq_id, int64_t first_pos, int* n_re
  * PA_ERR_INVALID_ARG if from_pos > to_pos or from_pos < 0.
  */
 int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t to_pos, int* n_released_out);
+
+/*
+ * Compaction: shortens seq_id to n_tokens (0 .. its length), the kept tokens to be
+ * moved by pa_compact_blocks, of which positions below first_moved stay in place
+ * (keep[j] == j for j < first_moved; 0 if not known).
+ *  table_out  the table for that call: the sequence's blocks before it, where
+ *             blocks that it will write and others share are replaced by fresh ones
+ *  pairs_out  int64 [pair_cap][2]: the copies (old, fresh) to make first
+ * Then the blocks behind the kept tokens are released, so that the copies and the
+ * compaction have to be on the stream before anything that writes blocks handed out
+ * later. pa_bm_cache_blocks registers no position from first_moved on afterwards.
+ * PA_ERR_INVALID_ARG where a block that would be written, or appended to, was
+ * released (pa_bm_release_*); PA_ERR_CAPACITY with both counts set, and PA_ERR_OOM:
+ * nothing changed. With n_tokens the sequence's length nothing moves.
+ */
+int pa_bm_compact(pa_bm* bm, int64_t seq_id, int64_t n_tokens, int64_t first_moved, int64_t* pairs_out,
+                  int pair_cap, int* n_pairs_out, int32_t* table_out, int table_cap, int* n_table_out);
 
 /*
  * Preemption by swapping ([MA] 9.1 "Batching and the scheduler": a preempted

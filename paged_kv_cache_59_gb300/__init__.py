@@ -25,7 +25,8 @@ __all__ = [
     "prefill_workspace", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_window",
     "pa_swap_out_blocks", "pa_swap_in_blocks", "pa_get_device_error", "pa_rope_and_cache",
     "pa_rope_and_cache_fp8_block", "pa_decode_sinks", "pa_decode_fp8_block",
-    "pa_prefill_sinks", "pa_prefill_fp8_block", "pa_copy_blocks_fp8_block",
+    "pa_prefill_sinks", "pa_prefill_fp8_block", "pa_copy_blocks_fp8_block", "pa_decode_score_mod",
+    "pa_prefill_score_mod", "pa_compact_blocks",
     "BlockManager", "load", "PagedKVError",
 ]
 
@@ -335,6 +336,30 @@ def pa_decode_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, 
     window >= 0: as pa_decode_sinks."""
     _decode_call("pa_decode_fp8_block", True, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
                  max_context_len, window, n_sinks, workspace, partition_tokens, stream)
+
+
+def _head_slopes(alibi_slopes, n_heads: int, dev: int):
+    if alibi_slopes is None:
+        return None
+    if alibi_slopes.numel() != n_heads:
+        raise ValueError(f"alibi_slopes needs {n_heads} entries")
+    return _at(alibi_slopes, "alibi_slopes", _Types.f32, dev)
+
+
+def pa_decode_score_mod(out, q, k_pool, v_pool, block_tables, context_lens, scale: float, max_context_len: int,
+                        softcap: float = 0.0, alibi_slopes=None, window: int = -1, n_sinks: int = 0, k_scale=None,
+                        v_scale=None, workspace=None, partition_tokens: int = 0, stream=None) -> None:
+    """Decode with reshaped scores: s = scale q.k becomes softcap tanh(s / softcap)
+    (softcap > 0), less alibi_slopes[head] times the key's distance (fp32 [n_heads]).
+    Masks as pa_decode_sinks (window -1: none). bf16 pools, or E4M3 pools with a
+    scale per block and head (k_scale, v_scale fp32 [num_blocks][n_kv_heads])."""
+    dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale,
+                                                           k_scale is not None and v_scale is not None, block_tables,
+                                                           context_lens, q.shape[0])
+    longest, window, n_sinks, partition_tokens = _ints(max_context_len, window, n_sinks, partition_tokens)
+    _call("pa_decode_score_mod", dev, stream, *data, *tables, float(scale), float(softcap),
+          _head_slopes(alibi_slopes, sizes[0], dev), *sizes, longest, num_blocks, window, n_sinks, partition_tokens,
+          *_workspace(workspace, dev))
 
 
 def pa_decode_plan(context_lens, n_heads: int, n_kv_heads: int, head_dim: int, max_blocks_per_seq: int,
@@ -648,6 +673,62 @@ def pa_prefill_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
                   q_start_loc, scale, max_chunk_len, window, n_sinks, splits, workspace, stream)
 
 
+def pa_prefill_score_mod(out, q, k_pool, v_pool, block_tables, context_lens, q_start_loc, scale: float,
+                         max_chunk_len: int, softcap: float = 0.0, alibi_slopes=None, prefix_lens=None, window: int = -1,
+                         n_sinks: int = 0, k_scale=None, v_scale=None, splits: int = 0, workspace=None,
+                         stream=None) -> None:
+    """Chunked prefill with the reshaped scores of pa_decode_score_mod. prefix_lens
+    (int32 [n_seqs]): keys before it are visible to earlier rows of the sequence
+    too. Caches as pa_decode_score_mod; workspace: prefill_workspace."""
+    n_seqs = context_lens.numel()
+    if q_start_loc.numel() != n_seqs + 1:
+        raise ValueError("q_start_loc must have n_seqs + 1 entries")
+    dev, data, tables, sizes, num_blocks = _attention_args(out, q, k_pool, v_pool, k_scale, v_scale,
+                                                           k_scale is not None and v_scale is not None, block_tables,
+                                                           context_lens, n_seqs)
+    prefix = None
+    if prefix_lens is not None:
+        if prefix_lens.numel() != n_seqs:
+            raise ValueError("prefix_lens must have n_seqs entries")
+        prefix = _at(prefix_lens, "prefix_lens", _Types.i32, dev)
+    longest, window, n_sinks, splits = _ints(max_chunk_len, window, n_sinks, splits)
+    _call("pa_prefill_score_mod", dev, stream, *data, *tables, _at(q_start_loc, "q_start_loc", _Types.i32, dev),
+          float(scale), float(softcap), _head_slopes(alibi_slopes, sizes[0], dev), prefix, *sizes, longest, num_blocks,
+          window, n_sinks, splits, *_workspace(workspace, dev))
+
+
+def pa_compact_blocks(k_pool, v_pool, block_tables, keep, keep_start_loc, k_scale=None, v_scale=None, stream=None) -> None:
+    """Moves the tokens of each sequence that stay to its first positions, in
+    place: position j becomes what position keep[keep_start_loc[s] + j] was.
+    keep: int32 [n_kept], ascending in each sequence, or [n_kv_heads][n_kept];
+    keep_start_loc: int32 [n_seqs + 1]. bf16 or E4M3 pools; k_scale and v_scale
+    (fp32 [num_blocks][n_kv_heads]) when E4M3 pools have a scale per block and
+    head. BlockManager.compact gives the tables and frees the blocks."""
+    dev = _device(k_pool, "k_pool")
+    T = _Types
+    num_blocks, n_kv_heads, block_size, head_dim = pool_shape = k_pool.shape
+    n_seqs, max_blocks = block_tables.shape
+    if v_pool.shape != pool_shape or v_pool.element_size() != k_pool.element_size():
+        raise ValueError("k_pool and v_pool must have one shape and element size")
+    if keep.dim() not in (1, 2) or (keep.dim() == 2 and keep.shape[0] != n_kv_heads):
+        raise ValueError("keep must be [n_kept] or [n_kv_heads][n_kept]")
+    if keep_start_loc.numel() != n_seqs + 1:
+        raise ValueError("keep_start_loc must have n_seqs + 1 entries")
+    ks = vs = None
+    if k_scale is not None and v_scale is not None:
+        ns = num_blocks * n_kv_heads
+        if k_scale.numel() != ns or v_scale.numel() != ns:
+            raise ValueError(f"k_scale and v_scale need {ns} entries")
+        ks, vs = _at(k_scale, "k_scale", T.f32, dev), _at(v_scale, "v_scale", T.f32, dev)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale go together")
+    kinds = T.e4m3 if ks is not None else T.bf16 + T.e4m3
+    _call("pa_compact_blocks", dev, stream, _at(k_pool, "k_pool", kinds, dev), _at(v_pool, "v_pool", kinds, dev), ks, vs,
+          _at(block_tables, "block_tables", T.i32, dev), _at(keep, "keep", T.i32, dev) if keep.numel() else None,
+          _at(keep_start_loc, "keep_start_loc", T.i32, dev), n_kv_heads if keep.dim() == 2 else 1, keep.shape[-1],
+          n_kv_heads, head_dim, block_size, k_pool.element_size(), n_seqs, max_blocks, num_blocks)
+
+
 def pa_copy_blocks_fp8_block(k_pool, v_pool, k_scale, v_scale, block_mapping, stream=None) -> None:
     """pa_copy_blocks of an E4M3 cache with a scale per block and head: the
     blocks' rows of k_scale and v_scale [num_blocks][n_kv_heads] are copied too."""
@@ -768,6 +849,25 @@ class BlockManager:
         n = C.c_int(0)
         check("pa_bm_release_between", self._lib.pa_bm_release_between(self._h, seq_id, from_pos, to_pos, C.byref(n)))
         return n.value
+
+    def compact(self, seq_id: int, n_tokens: int, first_moved: int = 0) -> Tuple[List[int], List[Tuple[int, int]]]:
+        """Shortens the sequence to n_tokens, for pa_compact_blocks: returns the
+        block table that call needs (the old one, with shared blocks that it
+        writes replaced by private ones) and the copy pairs of those blocks
+        (pa_copy_blocks first). Positions below first_moved stay where they are;
+        the blocks behind the kept tokens are released."""
+        n_pairs, n_table = C.c_int(0), C.c_int(0)
+        st = self._lib.pa_bm_compact(self._h, seq_id, n_tokens, first_moved, None, 0, C.byref(n_pairs), None, 0,
+                                     C.byref(n_table))
+        if st == _capi.PA_OK:
+            return [], []
+        if st != _capi.PA_ERR_CAPACITY:
+            check("pa_bm_compact", st)
+        pairs = (C.c_int64 * (2 * max(n_pairs.value, 1)))()
+        table = (C.c_int32 * max(n_table.value, 1))()
+        check("pa_bm_compact", self._lib.pa_bm_compact(self._h, seq_id, n_tokens, first_moved, pairs, n_pairs.value,
+                                                       C.byref(n_pairs), table, n_table.value, C.byref(n_table)))
+        return list(table)[:n_table.value], [(pairs[2 * i], pairs[2 * i + 1]) for i in range(n_pairs.value)]
 
     def block_table(self, seq_id: int) -> List[int]:
         n = C.c_int(0)

@@ -34,6 +34,7 @@
 // independent 64-bit chains, each token absorbed with the splitmix64
 // finalizer of Steele, Lea and Flood); distinct prefixes collide with
 // probability about 2^-128 per pair.
+#include <algorithm>
 #include <cstdint>
 #include <list>
 #include <new>
@@ -81,6 +82,7 @@ struct pa_bm {
         std::vector<int32_t> table;
         int64_t len = 0;
         int64_t swapped = -1;  // >= 0: that many trailing blocks are in host memory
+        int64_t intact = INT64_MAX;  // positions from here on were moved by a compaction
     };
     std::unordered_map<int64_t, Seq> seqs;
     struct Entry {
@@ -261,6 +263,48 @@ int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t t
     return PA_OK;
 }
 
+int pa_bm_compact(pa_bm* bm, int64_t seq_id, int64_t n_tokens, int64_t first_moved, int64_t* pairs_out, int pair_cap,
+                  int* n_pairs_out, int32_t* table_out, int table_cap, int* n_table_out) {
+    if (!bm || !n_pairs_out || !n_table_out || pair_cap < 0 || table_cap < 0 || (pair_cap > 0 && !pairs_out) ||
+        (table_cap > 0 && !table_out))
+        return PA_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end()) return PA_ERR_REFCOUNT;
+    pa_bm::Seq& s = it->second;
+    if (s.swapped >= 0 || n_tokens < 0 || n_tokens > s.len || first_moved < 0 || first_moved > n_tokens) return PA_ERR_INVALID_ARG;
+    const int64_t bs = bm->block_size, keep = (n_tokens + bs - 1) / bs;  // blocks that stay
+    if (n_tokens == s.len) first_moved = n_tokens;                       // nothing moves
+    const int64_t from = first_moved < n_tokens ? first_moved / bs : keep;  // blocks from here to `keep` are written
+    int pairs = 0;
+    for (int64_t j = from; j < keep; ++j) {
+        if (s.table[j] < 0) return PA_ERR_INVALID_ARG;  // released: there is no block to move into
+        pairs += bm->ref[s.table[j]] > 1;
+    }
+    if (n_tokens % bs != 0 && s.table[keep - 1] < 0) return PA_ERR_INVALID_ARG;  // nor one to append to
+    *n_pairs_out = pairs;
+    *n_table_out = (int)s.table.size();
+    if (pairs > pair_cap || (int)s.table.size() > table_cap) return PA_ERR_CAPACITY;  // nothing changed
+    if (pairs > bm->available()) return PA_ERR_OOM;
+    pairs = 0;
+    for (int64_t j = from; j < keep; ++j) {
+        const int32_t b = s.table[j];
+        if (bm->ref[b] <= 1) continue;
+        const int32_t fresh = bm->alloc();
+        bm->put(b);
+        s.table[j] = fresh;
+        pairs_out[2 * pairs] = b;
+        pairs_out[2 * pairs + 1] = fresh;
+        ++pairs;
+    }
+    std::copy(s.table.begin(), s.table.end(), table_out);
+    for (int64_t j = keep; j < (int64_t)s.table.size(); ++j)
+        if (s.table[j] >= 0) bm->put(s.table[j]);
+    s.table.resize(keep);
+    s.len = n_tokens;
+    if (first_moved < s.intact) s.intact = first_moved;
+    return PA_OK;
+}
+
 int pa_bm_swap_out(pa_bm* bm, int64_t seq_id, int32_t* blocks_out, int cap, int* n_out) {
     if (!bm || !n_out || cap < 0 || (cap > 0 && !blocks_out)) return PA_ERR_INVALID_ARG;
     auto it = bm->seqs.find(seq_id);
@@ -308,7 +352,7 @@ int pa_bm_cache_blocks(pa_bm* bm, int64_t seq_id, const int32_t* tokens, int64_t
     const pa_bm::Seq& s = it->second;
     if (s.swapped >= 0) return PA_ERR_INVALID_ARG;
     const int64_t bs = bm->block_size;
-    const int64_t n_full = (n_tokens < s.len ? n_tokens : s.len) / bs;
+    const int64_t n_full = std::min({n_tokens, s.len, s.intact}) / bs;
     int added = 0;
     PrefixKey h = kEmptyPrefix;
     try {

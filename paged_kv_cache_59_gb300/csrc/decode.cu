@@ -82,6 +82,10 @@ struct DecodeParams {
     int n_items;
     int n_seqs;
     int parts_last;  // the grid is (KV heads, sequences, partitions)
+    // pa_decode_score_mod: scores are cap2 tanh(x) with x = q.k * scale_log2 (which is scale / cap there),
+    // cap2 = cap * log2(e); 0: not capped. slopes: fp32 [n_heads] or null
+    float cap2;
+    const float* slopes;
 };
 
 // The grid of a partition kernel. Under a window with sinks a sequence longer than
@@ -224,6 +228,8 @@ struct BlockScales {
         inv = __shfl_sync(kFull, my_inv, i);
     }
     __device__ __forceinline__ float score(float s) const { return fmaf(s, k, e); }
+    __device__ __forceinline__ float scaled(float s) const { return s * k; }
+    __device__ __forceinline__ float shift() const { return e; }
     __device__ __forceinline__ float weight(float w) const { return w * inv; }
 };
 template <>
@@ -231,8 +237,20 @@ struct BlockScales<false> {
     __device__ __forceinline__ BlockScales(const DecodeParams&, int, int, float) {}
     __device__ __forceinline__ void take(int) {}
     __device__ __forceinline__ float score(float s) const { return s; }
+    __device__ __forceinline__ float scaled(float s) const { return s; }
+    __device__ __forceinline__ float shift() const { return 0.f; }
     __device__ __forceinline__ float weight(float w) const { return w; }
 };
+
+// A reshaped score in base-2 units, x as DecodeParams::cap2 says, `dist` positions back; slope2 = a head's
+// slope * log2(e), 0 without biases.
+__device__ __forceinline__ float reshaped(const DecodeParams& P, float x, float slope2, int dist) {
+    const float y = P.cap2 > 0.f ? P.cap2 * pa::tanh_f32(x) : x;
+    return fmaf(-slope2, (float)dist, y);
+}
+__device__ __forceinline__ float slope_of(const DecodeParams& P, int head) {
+    return P.slopes ? P.slopes[head] * 1.4426950408889634f : 0.f;
+}
 
 // EB = bytes per cached element: 2 (bf16) or 1 (E4M3 codes with scales).
 template <int D, int G, int LPT, int EB>
@@ -307,7 +325,10 @@ struct Chunk8<1> {
 // so the P.V product runs on the codes with one running reference m for loud
 // and quiet blocks alike, no output is ever rescaled for a scale, and the only
 // extra work is one multiply-add per score and one multiply per block.
-template <int D, int G, int LPT, int EB, bool BSC, bool SINKS, int NW, int S, int MINB>
+// MOD: scores are reshaped (pa_decode_score_mod). A warp then takes its blocks from
+// the last to the first: under a bias by distance the nearest keys set the running
+// maximum, and far ones seldom raise it.
+template <int D, int G, int LPT, int EB, bool BSC, bool SINKS, bool MOD, int NW, int S, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB)
 pa_decode_partition_kernel(const DecodeParams P) {
     using SH = Shape<D, G, LPT, EB>;
@@ -364,9 +385,10 @@ pa_decode_partition_kernel(const DecodeParams P) {
     }
     __syncwarp();
 
-    // one block-table entry per lane: local block warp + NW*lane
+    // one block-table entry per lane: local block warp + NW*lane (MOD: counted from the warp's last)
+    auto block_of = [&](int i) { return sp.block(blk_begin + warp + NW * (MOD ? my_n - 1 - i : i)); };
     int my_bid = -1;
-    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + sp.block(blk_begin + warp + NW * lane)];
+    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + block_of(lane)];
 
     const uint64_t pol = pa::l2_evict_first_policy();
     const size_t head_stride = (size_t)SH::TILE_BYTES;
@@ -422,6 +444,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
     const int h_own = base / NPASS;
     const int ip0 = base % NPASS;
     const bool alpha_writer = (lane & NONHEAD) == 0;
+    const float slope2 = MOD ? slope_of(P, h0 + h_own) : 0.f;
 
     float m_run = -INFINITY;  // running max of this lane's head (base-2 units)
     float l_run = 0.f;        // partial sum of p over this lane's kept tokens
@@ -450,7 +473,7 @@ pa_decode_partition_kernel(const DecodeParams P) {
         if (bid >= 0 && bid < P.num_blocks) {
             const unsigned char* sK = my_stages + (size_t)st * 2 * SH::TILE_BYTES;
             const unsigned char* sV = sK + SH::TILE_BYTES;
-            const int tok0 = sp.block(blk_begin + warp + NW * i) * kBS;
+            const int tok0 = block_of(i) * kBS;
 
             // ---- scores: partial dots over this lane's dims
             float sc[NV];
@@ -483,7 +506,10 @@ pa_decode_partition_kernel(const DecodeParams P) {
 #pragma unroll
             for (int k = 0; k < NKEEP; ++k) {
                 const int t = (ip0 + k) * TPP + tg;
-                sc[k] = visible<SINKS>(tok0 + t, ctx, first_pos, P.n_sinks) ? scales.score(sc[k]) : -INFINITY;
+                float s2;
+                if constexpr (MOD) s2 = reshaped(P, scales.scaled(sc[k]), slope2, ctx - 1 - tok0 - t) + scales.shift();
+                else s2 = scales.score(sc[k]);
+                sc[k] = visible<SINKS>(tok0 + t, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
                 tmax = fmaxf(tmax, sc[k]);
             }
 #pragma unroll
@@ -733,7 +759,7 @@ __device__ __forceinline__ uint32_t sw_off(int row, int dims8) {
 
 }  // namespace mma
 
-template <int G, int EB, bool BSC, bool SINKS>
+template <int G, int EB, bool BSC, bool SINKS, bool MOD>
 __global__ void __launch_bounds__(mma::kNW * 32, EB == 1 ? 4 : 3)
 pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
@@ -784,8 +810,10 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
     }
     __syncwarp();
 
-    int my_bid = -1;  // one block-table entry per lane: local block warp + NW*lane
-    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + sp.block(blk_begin + warp + NW * lane)];
+    // one block-table entry per lane: local block warp + NW*lane (MOD: counted from the warp's last)
+    auto block_of = [&](int i) { return sp.block(blk_begin + warp + NW * (MOD ? my_n - 1 - i : i)); };
+    int my_bid = -1;
+    if (lane < my_n) my_bid = P.tables[(size_t)b * P.max_blocks + block_of(lane)];
 
     const uint64_t pol = pa::l2_evict_first_policy();
     auto issue = [&](int i) {  // all lanes call (shuffle); lanes 0..3 issue the four boxes
@@ -844,6 +872,15 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
     // lane holds heads 2t and 2t + 1: their reference maxima and its part of
     // their sums (the same reference on the 8 lanes of a head)
     float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
+    // MOD: slopes of this lane's heads (E4M3: 2t and 2t + 1; bf16: g)
+    float slope2[2] = {0.f, 0.f};
+    if constexpr (MOD) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int h = EB == 1 ? 2 * t + k : g;
+            slope2[k] = h < G ? slope_of(P, h0 + h) : 0.f;
+        }
+    }
     // E4M3 cache: q.(code*s_k) = s_k (q.code), folded into the score scale
     const float sc = EB == 1 && !BSC ? P.scale_log2 * P.k_scale[kvh] : P.scale_log2;
 
@@ -863,7 +900,7 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
         if (bid >= 0 && bid < P.num_blocks) {
             const uint32_t kb = pa::smem_u32(my_stages + (size_t)st * kStage);
             const uint32_t vb = kb + 4096;  // bf16 cache: the V tile
-            const int tok0 = sp.block(blk_begin + warp + NW * i) * kBS;
+            const int tok0 = block_of(i) * kBS;
             // ---- S = Q K^T: two n-tiles of 8 tokens
             float s_acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
             if constexpr (EB == 2) {
@@ -909,7 +946,13 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int pos = tok0 + g + 8 * (u >> 1);
-                    const float s2 = BSC ? scales.score(sT[u]) : sT[u] * sc;
+                    float s2;
+                    if constexpr (MOD) {
+                        const float x = BSC ? scales.scaled(sT[u]) : sT[u] * sc;
+                        s2 = reshaped(P, x, slope2[u & 1], ctx - 1 - pos) + scales.shift();
+                    } else {
+                        s2 = BSC ? scales.score(sT[u]) : sT[u] * sc;
+                    }
                     sv[u] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
                 }
                 auto exps = [&]() {
@@ -961,7 +1004,9 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int pos = tok0 + 8 * n + 2 * t + k;
-                        sv[2 * n + k] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s_acc[n][k] * sc : -INFINITY;
+                        float s2 = s_acc[n][k] * sc;
+                        if constexpr (MOD) s2 = reshaped(P, s2, slope2[0], ctx - 1 - pos);
+                        sv[2 * n + k] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
                     }
                 float tmax = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
                 tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 1));
@@ -1270,11 +1315,11 @@ struct Launch {
     static constexpr int S = FP8_WIDE ? 2 : (D == 128 ? 2 : 4) * (MINB == 3 ? 1 : 3) / (MINB == 3 ? 1 : 2) * (2 / EB);
 };
 
-template <int D, int G, int EB, bool BSC, bool SINKS>
+template <int D, int G, int EB, bool BSC, bool SINKS, bool MOD>
 int launch_partition(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     using LC = Launch<D, G, EB>;
     using SM = Smem<D, G, LC::LPT, EB, kNW, LC::S>;
-    auto kern = pa_decode_partition_kernel<D, G, LC::LPT, EB, BSC, SINKS, kNW, LC::S, LC::MINB>;
+    auto kern = pa_decode_partition_kernel<D, G, LC::LPT, EB, BSC, SINKS, MOD, kNW, LC::S, LC::MINB>;
     static bool attr_done[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1288,22 +1333,22 @@ int launch_partition(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     return pa_launch_pdl(kern, grid, dim3(kNW * 32), SM::TOTAL, stream, P);
 }
 
-template <int D, int EB, bool BSC, bool SINKS>
+template <int D, int EB, bool BSC, bool SINKS, bool MOD>
 int dispatch_group(int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_partition<D, 1, EB, BSC, SINKS>(P, n_seqs, stream);
-        case 2: return launch_partition<D, 2, EB, BSC, SINKS>(P, n_seqs, stream);
-        case 4: return launch_partition<D, 4, EB, BSC, SINKS>(P, n_seqs, stream);
-        case 8: return launch_partition<D, 8, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 1: return launch_partition<D, 1, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
+        case 2: return launch_partition<D, 2, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
+        case 4: return launch_partition<D, 4, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
+        case 8: return launch_partition<D, 8, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
         default: return PA_ERR_UNSUPPORTED;
     }
 }
 
 // The tensor-core partition kernel (head_dim 128, bf16 cache): K and V pools
 // as 2-D TMA maps of [num_blocks * n_kv_heads * 16 rows][128 dims].
-template <int G, int EB, bool BSC, bool SINKS>
+template <int G, int EB, bool BSC, bool SINKS, bool MOD>
 int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream) {
-    auto kern = pa_decode_mma_kernel<G, EB, BSC, SINKS>;
+    auto kern = pa_decode_mma_kernel<G, EB, BSC, SINKS, MOD>;
     constexpr int kSmem = mma::Lay<EB>::kSmem;
     static bool attr_done[64] = {false};
     int dev = 0;
@@ -1324,22 +1369,24 @@ int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream)
     return pa_launch_pdl(kern, grid, dim3(mma::kNW * 32), kSmem, stream, P, tk, tv);
 }
 
-template <int EB, bool BSC, bool SINKS>
+template <int EB, bool BSC, bool SINKS, bool MOD>
 int dispatch_group_mma(int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
+    if constexpr (MOD && EB == 2)  // reshaped scores over a bf16 cache: groups of 8 only (see decode_impl)
+        return launch_partition_mma<8, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
     switch (G) {
-        case 1: return launch_partition_mma<1, EB, BSC, SINKS>(P, n_seqs, stream);
-        case 2: return launch_partition_mma<2, EB, BSC, SINKS>(P, n_seqs, stream);
-        case 4: return launch_partition_mma<4, EB, BSC, SINKS>(P, n_seqs, stream);
-        case 8: return launch_partition_mma<8, EB, BSC, SINKS>(P, n_seqs, stream);
+        case 1: return launch_partition_mma<1, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
+        case 2: return launch_partition_mma<2, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
+        case 4: return launch_partition_mma<4, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
+        case 8: return launch_partition_mma<8, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
         default: return PA_ERR_UNSUPPORTED;
     }
 }
 
-template <int EB, bool BSC, bool SINKS>
+template <int EB, bool BSC, bool SINKS, bool MOD = false>
 int dispatch_kernel(bool tensor, int head_dim, int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
-    if (tensor) return dispatch_group_mma<EB, BSC, SINKS>(G, P, n_seqs, stream);
-    return head_dim == 128 ? dispatch_group<128, EB, BSC, SINKS>(G, P, n_seqs, stream)
-                           : dispatch_group<64, EB, BSC, SINKS>(G, P, n_seqs, stream);
+    if (tensor) return dispatch_group_mma<EB, BSC, SINKS, MOD>(G, P, n_seqs, stream);
+    return head_dim == 128 ? dispatch_group<128, EB, BSC, SINKS, MOD>(G, P, n_seqs, stream)
+                           : dispatch_group<64, EB, BSC, SINKS, MOD>(G, P, n_seqs, stream);
 }
 
 constexpr int kDefaultPartitionTokens = 512;
@@ -1490,7 +1537,8 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
                 int block_size, int n_seqs, int max_blocks_per_seq, int max_context_len, int num_blocks,
                 int window, int partition_tokens, void* workspace, size_t workspace_bytes,
                 pa_stream_t stream, bool force_tc = false, const int32_t* items = nullptr, int n_items = 0,
-                int n_sinks = 0, bool block_scaled = false, bool spread = false, bool exact_bound = false) {
+                int n_sinks = 0, bool block_scaled = false, bool spread = false, bool exact_bound = false,
+                bool reshape = false, float softcap = 0.f, const float* slopes = nullptr) {
     if (n_seqs < 0 || max_context_len < 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
         n_heads <= 0 || n_kv_heads <= 0)
         return PA_ERR_INVALID_ARG;
@@ -1553,7 +1601,9 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     P.ws_o = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                              ((rows * 2 * sizeof(float) + 255) & ~(size_t)255))
                   : nullptr;
-    P.scale_log2 = scale * 1.4426950408889634f;
+    P.scale_log2 = softcap > 0.f ? scale / softcap : scale * 1.4426950408889634f;
+    P.cap2 = softcap * 1.4426950408889634f;
+    P.slopes = slopes;
     P.n_heads = n_heads;
     P.n_kv_heads = n_kv_heads;
     P.max_blocks = max_blocks_per_seq;
@@ -1573,7 +1623,10 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int st;
-    if (block_scaled)  // one instantiation, with sinks
+    if (reshape)  // with sinks; E4M3: with block scales
+        st = eb == 2 ? dispatch_kernel<2, false, true, true>(tensor, head_dim, G, P, n_seqs, s)
+                     : dispatch_kernel<1, true, true, true>(tensor, head_dim, G, P, n_seqs, s);
+    else if (block_scaled)  // one instantiation, with sinks
         st = dispatch_kernel<1, true, true>(tensor, head_dim, G, P, n_seqs, s);
     else if (spread)
         st = eb == 2 ? dispatch_kernel<2, false, true>(tensor, head_dim, G, P, n_seqs, s)
@@ -1671,6 +1724,22 @@ extern "C" int pa_decode_fp8_block(void* out, const void* q, const void* k_pool,
                        n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len, num_blocks,
                        window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0, n_sinks, true,
                        true, true);
+}
+
+extern "C" int pa_decode_score_mod(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                   const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                   const int32_t* context_lens, float scale, float softcap, const float* alibi_slopes,
+                                   int n_heads, int n_kv_heads, int head_dim, int block_size, int n_seqs,
+                                   int max_blocks_per_seq, int max_context_len, int num_blocks, int window, int n_sinks,
+                                   int partition_tokens, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+    if (window < -1 || n_sinks < 0 || (k_scale == nullptr) != (v_scale == nullptr)) return PA_ERR_INVALID_ARG;
+    if (!pa_softcap_ok(softcap, scale) || (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u)) return PA_ERR_INVALID_ARG;
+    if (window < 0) n_sinks = 0;  // everything is visible
+    if (n_sinks > max_context_len) n_sinks = max_context_len;
+    return decode_impl(k_scale ? 1 : 2, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                       n_heads, n_kv_heads, head_dim, block_size, n_seqs, max_blocks_per_seq, max_context_len, num_blocks,
+                       window, partition_tokens, workspace, workspace_bytes, stream, false, nullptr, 0, n_sinks,
+                       k_scale != nullptr, true, true, true, softcap, alibi_slopes);
 }
 
 extern "C" int pa_decode(void* out, const void* q, const void* k_pool, const void* v_pool,

@@ -6,6 +6,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/pagedkv.h"
@@ -27,6 +28,11 @@ void* pa_symbol_address(PaSymbolCache* cache, const void* symbol);
 
 // Host-side helpers shared by the entry points.
 static inline bool pa_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A score cap the kernels can work with: 0 (none), or positive with finite scale / cap and cap * log2(e).
+static inline bool pa_softcap_ok(float cap, float scale) {
+    return cap == 0.f || (cap > 0.f && isfinite(scale / cap) && isfinite(cap * 1.4426950408889634f));
+}
 
 // Host: launches `kern` with programmatic stream serialization, so its launch
 // and prologue overlap the tail of the previous kernel in the stream. The
@@ -231,6 +237,33 @@ __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either is
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// tanh for scores. Below kTanhSmall in magnitude x + x^3 P(x^2), P the polynomial of
+// degree 3 whose relative error to tanh is least (a linear program over 4,000 points
+// of [0, 0.7]): 2^-21.6. Above, 1 - 2 / (1 + e^(2|x|)), off by a few 2^-23; below,
+// that form would lose what it subtracts, and a score that a wide cap hardly bends
+// with it. (The hardware's approximate tanh is off by 2^-11: at a cap of 50, 2% of a
+// weight.)
+constexpr float kTanhSmall = 0.7f;
+constexpr float kTanhC[4] = {-0.33330938622f, 0.13286074149f, -0.05096434607f, 0.01388524047f};
+__device__ __forceinline__ float tanh_f32(float x) {
+    const float z = x * x, a = fabsf(x);
+    const float p = fmaf(fmaf(fmaf(kTanhC[3], z, kTanhC[2]), z, kTanhC[1]), z, kTanhC[0]);
+    const float big = fmaf(-2.f, fast_rcp(1.f + fast_exp2(a * 2.8853900817779268f)), 1.f);
+    return a < kTanhSmall ? fmaf(x * z, p, x) : copysignf(big, x);
 }
 
 }  // namespace pa

@@ -807,7 +807,8 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
                  int n_kv_heads, int head_dim, int block_size, int n_seqs, int max_blocks_per_seq,
                  int max_chunk_len, int num_blocks, int splits, void* workspace, size_t workspace_bytes,
                  pa_stream_t stream, int eb = 2, const float* k_scale = nullptr, const float* v_scale = nullptr,
-                 int window = -1, int n_sinks = 0) {
+                 int window = -1, int n_sinks = 0, bool reshape = false, float softcap = 0.f,
+                 const float* slopes = nullptr, const int32_t* prefix = nullptr) {
     if (n_seqs < 0 || max_chunk_len < 0 || num_blocks < 0 || max_blocks_per_seq < 0 || n_heads <= 0 ||
         n_kv_heads <= 0 || splits < 0 || splits > 64)
         return PA_ERR_INVALID_ARG;
@@ -853,7 +854,7 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
     Pp.tables = block_tables;
     Pp.ctx = context_lens;
     Pp.qsl = q_start_loc;
-    Pp.scale_log2 = scale * 1.4426950408889634f;
+    Pp.scale_log2 = softcap > 0.f ? scale / softcap : scale * 1.4426950408889634f;
     Pp.n_heads = n_heads;
     Pp.n_kv_heads = n_kv_heads;
     Pp.max_blocks = max_blocks_per_seq;
@@ -877,11 +878,18 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
     Pp.n_sinks = n_sinks;
     Pp.k_scale = k_scale;
     Pp.v_scale = v_scale;
+    Pp.reshape = reshape;
+    Pp.cap2 = softcap * 1.4426950408889634f;
+    Pp.slopes = slopes;
+    Pp.prefix = prefix;
     // chunk rows bound for the merge grid (rows past the last chunk exit)
     const long long n_rows = (long long)n_seqs * max_chunk_len;
     if (n_rows > 0x7fffffffLL || n_rows * n_heads > 0x7fffffffLL * 4LL) return PA_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int nr = (int)n_rows;
+    if (reshape)
+        return eb == 2 ? pa_prefill_dispatch_score(head_dim, G, Pp, tk, tv, n_seqs, nr, st)
+                       : pa_prefill_dispatch_score_fp8(head_dim, G, Pp, tk, tv, n_seqs, nr, st);
     if (eb == 1) return pa_prefill_dispatch_fp8(head_dim, G, Pp, tk, tv, n_seqs, nr, st);
     if (window >= 0) return pa_prefill_dispatch_sinks(head_dim, G, Pp, tk, tv, n_seqs, nr, st);
     return head_dim == 64 ? dispatch_prefill<64>(G, Pp, tk, tv, n_seqs, max_chunk_len, nr, st)
@@ -946,4 +954,22 @@ extern "C" int pa_prefill_fp8_block(void* out, const void* q, const void* k_pool
     return prefill_impl(out, q, k_pool, v_pool, block_tables, context_lens, q_start_loc, scale, n_heads, n_kv_heads,
                         head_dim, block_size, n_seqs, max_blocks_per_seq, max_chunk_len, num_blocks, splits, workspace,
                         workspace_bytes, stream, 1, k_scale, v_scale, window, n_sinks);
+}
+
+extern "C" int pa_prefill_score_mod(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                    const int32_t* context_lens, const int32_t* q_start_loc, float scale, float softcap,
+                                    const float* alibi_slopes, const int32_t* prefix_lens, int n_heads, int n_kv_heads,
+                                    int head_dim, int block_size, int n_seqs, int max_blocks_per_seq, int max_chunk_len,
+                                    int num_blocks, int window, int n_sinks, int splits, void* workspace,
+                                    size_t workspace_bytes, pa_stream_t stream) {
+    if (window < -1 || n_sinks < 0 || (k_scale == nullptr) != (v_scale == nullptr)) return PA_ERR_INVALID_ARG;
+    if (!pa_softcap_ok(softcap, scale) || (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) ||
+        (reinterpret_cast<uintptr_t>(prefix_lens) & 3u))
+        return PA_ERR_INVALID_ARG;
+    if (window < 0) n_sinks = 0;  // everything is visible
+    return prefill_impl(out, q, k_pool, v_pool, block_tables, context_lens, q_start_loc, scale, n_heads, n_kv_heads,
+                        head_dim, block_size, n_seqs, max_blocks_per_seq, max_chunk_len, num_blocks, splits, workspace,
+                        workspace_bytes, stream, k_scale ? 1 : 2, k_scale, v_scale, window, n_sinks, true, softcap,
+                        alibi_slopes, prefix_lens);
 }

@@ -41,6 +41,13 @@ struct PaPrefillParams {
     int n_sinks;
     const float* k_scale;  // E4M3: [num_blocks][n_kv_heads]
     const float* v_scale;
+    // pa_prefill_score_mod (reshape): scores are cap2 tanh(x), x = q.k * scale_log2 (scale / cap there) and
+    // cap2 = cap * log2(e), 0: not capped, less slopes[head] * distance (null: none); prefix [n_seqs] (null:
+    // none): keys before it are visible to earlier rows too
+    int reshape;
+    float cap2;
+    const float* slopes;
+    const int32_t* prefix;
 };
 
 // Launches of the windowed and of the E4M3 instantiations (translation units
@@ -49,6 +56,10 @@ int pa_prefill_dispatch_sinks(int head_dim, int G, const PaPrefillParams& P, con
                               int n_seqs, int n_rows, cudaStream_t stream);
 int pa_prefill_dispatch_fp8(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
                             int n_seqs, int n_rows, cudaStream_t stream);
+int pa_prefill_dispatch_score(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                              int n_seqs, int n_rows, cudaStream_t stream);
+int pa_prefill_dispatch_score_fp8(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, int n_seqs, int n_rows, cudaStream_t stream);
 
 namespace {
 
@@ -61,11 +72,15 @@ constexpr uint32_t kTmemCols = 512;  // tile X: S at 256X, O at 256X + 128 (D co
 
 using PrefillParams = PaPrefillParams;
 
-// The key tiles that the rows of a query-tile pair attend to: the cache blocks
+// A sequence's prefix, at most its context; 0 without one.
+// KeyTiles: the key tiles that the rows of a query-tile pair attend to: the cache blocks
 // that some row sees, in order - the n_sink leading ones that hold sinks, then
 // those from `first` on, the block of `lo`, the first position in the window of
 // the pair's first row (all blocks without a window) - eight a tile, so that a
 // tile may hold sinks and the window's beginning. n tiles.
+__device__ __forceinline__ int prefix_of(const PrefillParams& P, int s, int ctx) {
+    return P.prefix ? min(P.prefix[s], ctx) : 0;
+}
 struct KeyTiles {
     int lo, first, n_sink, n;
     __device__ __forceinline__ KeyTiles(const PrefillParams& P, int first_row_pos, int last_row_pos) {
@@ -121,13 +136,13 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_majo
 }
 
 // Whether a sequence of L > 0 rows is left out and flagged: its chunk is not in
-// the cache yet, or (calls with a window or over E4M3) its context runs past its
+// the cache yet, or (calls with a window, over E4M3 or of reshaped scores) its context runs past its
 // table or its chunk past max_chunk_len.
 template <int G>
 __device__ __forceinline__ bool left_out(const PrefillParams& P, int L, int ctx) {
     constexpr int QT = kRows / G;
     if (ctx < L) return true;
-    return (P.window >= 0 || P.k_scale) && ((ctx - 1) / kBS >= P.max_blocks || (L - 1) / (2 * QT) >= P.n_qp);
+    return (P.window >= 0 || P.k_scale || P.reshape) && ((ctx - 1) / kBS >= P.max_blocks || (L - 1) / (2 * QT) >= P.n_qp);
 }
 
 // Key tiles of item it = (sequence * n_kv_heads + kv head) * n_qp + pair:
@@ -145,7 +160,7 @@ __device__ int item_tiles(const PrefillParams& P, int it) {
         if (it % per_seq == 0) pa::set_error(P.err, PA_DEVERR_CONTEXT);
         return 0;
     }
-    return KeyTiles(P, ctx - L + i0, ctx - L + min(i0 + 2 * QT, L) - 1).n;
+    return KeyTiles(P, ctx - L + i0, max(ctx - L + min(i0 + 2 * QT, L), prefix_of(P, s, ctx)) - 1).n;
 }
 
 // Combines the pieces of one output row: O = sum_k O_k 2^(m_k - M),
@@ -281,7 +296,7 @@ pa_prefill_merge_kernel(const PrefillParams P, int n_seqs, int n_rows_total, int
     const int qp = i / (2 * QT), x = (i % (2 * QT)) / QT, r = (i % QT) * G + h % G, kvh = h / G;
     if (qp >= n_qp) return;  // a chunk beyond max_chunk_len: no partials
     const int i0 = qp * 2 * QT;
-    const int n_kt_all = KeyTiles(P, ctx - L + i0, ctx - L + min(i0 + 2 * QT, L) - 1).n;
+    const int n_kt_all = KeyTiles(P, ctx - L + i0, max(ctx - L + min(i0 + 2 * QT, L), prefix_of(P, s, ctx)) - 1).n;
     const size_t item = ((size_t)s * Hk + kvh) * n_qp + qp;
     merge_row<D>(P.splits, n_kt_all,
                  [&](int k) { return P.part + (((item * P.splits + k) * 2 + x) * 128 + r) * kPartStride; }, lane,

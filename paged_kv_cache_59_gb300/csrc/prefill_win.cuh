@@ -144,7 +144,7 @@ struct Segments {
     __device__ __forceinline__ KeyTiles keys(const Segment& g) const {
         constexpr int QT = kRows / G;
         const int i0 = g.qp * 2 * QT, first = g.ctx - g.L;
-        return KeyTiles(P, first + i0, first + min(i0 + 2 * QT, g.L) - 1);
+        return KeyTiles(P, first + i0, max(first + min(i0 + 2 * QT, g.L), prefix_of(P, g.s, g.ctx)) - 1);
     }
 };
 
@@ -328,7 +328,61 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
     }
 }
 
-template <int G, int D, int EB>
+// The scores of 32 keys of a row, reshaped in place: in, products q.k; out, in base-2
+// units, cap2 tanh(q.k * k) - slope2 * distance (cap2 0: q.k * k). k: the factors of the
+// two blocks; back: how far the row is behind each block's first key (BOTH: it may be
+// before a key).
+// tanh x = 1 - 2 / (1 + e^(2x)): two exponentials a score with the softmax's, and one
+// reciprocal for four scores, r = 1 / (abcd) giving 1 / a = r b cd and so on (an
+// argument of 2^30 at most keeps the product finite and changes nothing: 1 - 2^-29 is 1
+// in fp32). Off by a few 2^-23 absolute, so a score by cap times that: for caps above
+// kWideCap pa::tanh_f32 takes over, which is as exact relative to the score.
+constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
+template <bool BOTH>
+__device__ __forceinline__ void reshape_scores(uint32_t (&raw)[32], const float (&k)[2], float cap2, float slope2,
+                                               const float (&back)[2]) {
+    auto pair = [&](int w) { return make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])); };
+    auto put = [&](int w, float2 v) {
+        raw[2 * w] = __float_as_uint(v.x);
+        raw[2 * w + 1] = __float_as_uint(v.y);
+    };
+    if (cap2 > 0.f && cap2 <= kWideCap2) {
+        const float2 one = make_float2(1.f, 1.f), c0 = make_float2(cap2, cap2), c1 = make_float2(-2.f * cap2, -2.f * cap2);
+#pragma unroll
+        for (int w = 0; w < 16; w += 2) {
+            const float f = k[w >> 3] * 2.8853900817779268f;
+            float2 a = __fmul2_rn(pair(w), make_float2(f, f)), c = __fmul2_rn(pair(w + 1), make_float2(f, f));
+            a = __fadd2_rn(make_float2(pa::fast_exp2(pa::min_nan(a.x, 30.f)), pa::fast_exp2(pa::min_nan(a.y, 30.f))), one);
+            c = __fadd2_rn(make_float2(pa::fast_exp2(pa::min_nan(c.x, 30.f)), pa::fast_exp2(pa::min_nan(c.y, 30.f))), one);
+            const float2 ac = __fmul2_rn(a, c);              // (a.x c.x, a.y c.y)
+            const float r = pa::fast_rcp(ac.x * ac.y);
+            const float2 rr = __fmul2_rn(make_float2(ac.y, ac.x), make_float2(r, r));  // 1 / (a.x c.x), 1 / (a.y c.y)
+            put(w, __ffma2_rn(__fmul2_rn(rr, c), c1, c0));
+            put(w + 1, __ffma2_rn(__fmul2_rn(rr, a), c1, c0));
+        }
+    } else {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            float2 x = __fmul2_rn(pair(w), make_float2(k[w >> 3], k[w >> 3]));
+            if (cap2 > 0.f) x = make_float2(cap2 * pa::tanh_f32(x.x), cap2 * pa::tanh_f32(x.y));
+            put(w, x);
+        }
+    }
+    if (slope2 != 0.f) {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            const float at = (float)(2 * w & (kBS - 1));
+            float2 d = __fadd2_rn(make_float2(back[w >> 3], back[w >> 3]), make_float2(-at, -at - 1.f));
+            if constexpr (BOTH) d = make_float2(fabsf(d.x), fabsf(d.y));
+            put(w, __ffma2_rn(d, make_float2(-slope2, -slope2), pair(w)));
+        }
+    }
+}
+
+// MOD: scores are reshaped (pa_prefill_score_mod). A segment's tiles are then walked
+// from its last to its first: under a bias by distance the nearest keys, usually the
+// heaviest, set a row's reference, and far ones seldom raise it.
+template <int G, int D, int EB, bool MOD>
 __global__ void __launch_bounds__(kWinThreads<EB>, 1)
 pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
@@ -370,6 +424,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
     Segment g;
     bool ok = true;  // after a failed wait a role goes on without waiting, so that no other role is left alone
     int J0 = 0;      // tiles of the segments before
+    auto tile_of = [&](int j) { return g.kt0 + (MOD ? g.n_kt - 1 - j : j); };  // the segment's j-th tile
 
     if (warp == 9 || warp == 14) {
         // ----------------------------------------------------------- TMA producers
@@ -435,8 +490,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 }
             };
             for (int j = 0; ok && j < g.n_kt; ++j) {
-                load(first, g.kt0 + j);
-                if (kBoth && ok) load(second, g.kt0 + j);
+                load(first, tile_of(j));
+                if (kBoth && ok) load(second, tile_of(j));
             }
         }
         // Every issued copy lands before the CTA exits: normally the converters and the tensor
@@ -602,7 +657,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 // kernel's time.
                 const int w4 = warp - 10;
                 for (int j = 0; j < g.n_kt; ++j) {
-                    const int J = J0 + j, st = J % kVS, tile = g.kt0 + j;
+                    const int J = J0 + j, st = J % kVS, tile = tile_of(j);
                     ok = pa::mbar_wait(bars.v_full(st), (uint32_t)((J / kVS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
@@ -694,7 +749,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     arrive(bars.raw_free(x));
                 };
                 for (int j = 0; j < g.n_kt; ++j) {
-                    const int J = J0 + j, tile = g.kt0 + j, ks = J % kKS, vs = J % kVS;
+                    const int J = J0 + j, tile = tile_of(j), ks = J % kKS, vs = J % kVS;
                     ok = pa::mbar_wait(bars.k_full(0), (uint32_t)(J & 1), P.err, abort_flag);
                     if (ok && J >= kKS) ok = pa::mbar_wait(bars.k_free(ks), (uint32_t)(((J - kKS) / kKS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
@@ -726,6 +781,9 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             const KeyTiles keys = segments.keys(g);
             const int i = g.qp * 2 * QT + x * QT + r / G;
             const int pos = g.ctx - g.L + i;  // this row's position (padding rows: beyond the chunk)
+            const int limit = MOD ? max(pos, prefix_of(P, g.s, g.ctx) - 1) : pos;  // the last position it sees
+            float slope2 = 0.f;
+            if constexpr (MOD) slope2 = P.slopes ? P.slopes[g.kvh * G + r % G] * 1.4426950408889634f : 0.f;
             float m_used = -INFINITY, l = 0.f;
             // Key k of tile j is at position 128 j + k + kb_sinks if it is a sink, else + kb_win. In tiles
             // from j_win on, the limits below are those of the window's keys: where such a tile begins
@@ -737,7 +795,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             // worked on.
             const int nblk = min((g.ctx + kBS - 1) / kBS, P.max_blocks);
             auto block_id = [&](int j) {
-                const int blk = j < g.n_kt ? keys.block((g.kt0 + j) * kBPT + (lane & (kBPT - 1))) : nblk;
+                const int blk = j < g.n_kt ? keys.block(tile_of(j) * kBPT + (lane & (kBPT - 1))) : nblk;
                 return blk < nblk ? P.tables[(size_t)g.s * P.max_blocks + blk] : -1;
             };
             auto scale_of = [&](const float* scales, int bid) {
@@ -773,15 +831,17 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     vst = 0;
                     vph ^= 1;
                 }
-                const int kb = j * kKT + (j < j_win ? kb_sinks : kb_win);
+                const int jt = tile_of(j) - g.kt0;
+                const int kb = jt * kKT + (jt < j_win ? kb_sinks : kb_win);
                 // A row does not see keys beyond its position or, sinks apart, before its window. A warp
                 // takes the masking code only for a tile where that hides a key from one of its rows (a
                 // warp-uniform branch): a tile or two at either end of a window, and that of the sinks.
                 // Key k of a quarter is bit k of the quarter's mask: two instructions an element (as
                 // three comparisons, a masked tile took twice a plain one's time).
-                const int lim0 = pos - kb;  // keys k > lim0 of the tile are not visible
-                const int lim1 = P.window >= 0 ? lim0 - P.window : 0, sink1 = P.n_sinks - kb_sinks - j * kKT;  // nor k < lim1, k >= sink1
-                const bool mask_warp = __any_sync(kFull, lim0 < kKT - 1 || (lim1 > 0 && sink1 < kKT));
+                const int lim0 = limit - kb;  // keys k > lim0 of the tile are not visible
+                const int lim1 = P.window >= 0 ? pos - kb - P.window : 0, sink1 = P.n_sinks - kb_sinks - jt * kKT;  // nor k < lim1, k >= sink1
+                // (MOD: and for one with a key after a row's own position, which a prefix may show)
+                const bool mask_warp = __any_sync(kFull, (MOD ? pos - kb : lim0) < kKT - 1 || (lim1 > 0 && sink1 < kKT));
                 auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };  // bits 0 .. n-1
                 auto visible_of = [&](int qd) {
                     const int k0 = 32 * qd;
@@ -802,8 +862,9 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     for (int w = 0; w < 16; ++w) {
                         const int b = EB == 1 ? w >> 3 : 0;
                         const float nm = qe[b] - m_used;
-                        float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])),
-                                              EB == 1 ? make_float2(qk[b], qk[b]) : sc2, make_float2(nm, nm));
+                        float2 e = make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1]));
+                        if constexpr (MOD) e = __fadd2_rn(e, make_float2(nm, nm));  // (scaled already)
+                        else e = __ffma2_rn(e, EB == 1 ? make_float2(qk[b], qk[b]) : sc2, make_float2(nm, nm));
                         if constexpr (decltype(masked)::value) {  // masked keys give p = 0 (also for a zero scale)
                             if (!(visible & (1u << (2 * w)))) e.x = -INFINITY;
                             if (!(visible & (1u << (2 * w + 1)))) e.y = -INFINITY;
@@ -842,6 +903,18 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             }
                         }
                         const uint32_t visible = decltype(masked)::value ? visible_of(qd) : 0xffffffffu;
+                        if constexpr (MOD) {
+                            // keys hidden from the row may hold anything, and reshape_scores mixes four of them
+                            if constexpr (decltype(masked)::value) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!(visible & (1u << k))) raw[k] = 0u;
+                            }
+                            float back[2];  // how far the row is behind key 0 of the quarter's two blocks
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) back[b] = (float)(pos - keys.position(tile_of(j), 32 * qd + kBS * b));
+                            reshape_scores<decltype(masked)::value>(raw, qk, P.cap2, slope2, back);
+                        }
                         uint32_t ph[16];
                         float add;
                         const float qs = exps(masked, raw, visible, ph, add);
@@ -856,7 +929,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                     const bool vis = !decltype(masked)::value || (visible & (1u << k));
                                     const float r = __uint_as_float(raw[k]);
                                     const int b = EB == 1 ? k >> 4 : 0;
-                                    if (vis) qmax = fmaxf(qmax, fmaf(r, qk[b], qe[b]));
+                                    if (vis) qmax = fmaxf(qmax, MOD ? r + qe[b] : fmaf(r, qk[b], qe[b]));
                                 }
                                 const float mq = ceilf(qmax);
                                 if (mq > m_used) {
@@ -1129,10 +1202,10 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
     }
 }
 
-template <int G, int D, int EB>
+template <int G, int D, int EB, bool MOD>
 int launch_prefill_win(const PrefillParams& Pp, const CUtensorMap& tk, const CUtensorMap& tv, int n_seqs,
                        int n_rows, cudaStream_t stream) {
-    auto kern = pa_prefill_win_kernel<G, D, EB>;
+    auto kern = pa_prefill_win_kernel<G, D, EB, MOD>;
     constexpr uint32_t kSmemBytes = WinLay<D, EB>::kSmem;
     static bool attr_done[64] = {false};
     int dev = 0;
@@ -1156,14 +1229,14 @@ int launch_prefill_win(const PrefillParams& Pp, const CUtensorMap& tk, const CUt
                          n_rows, Pp.n_qp);
 }
 
-template <int D, int EB>
+template <int D, int EB, bool MOD = false>
 int dispatch_prefill_win(int G, const PrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv, int n_seqs,
                          int n_rows, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_prefill_win<1, D, EB>(P, tk, tv, n_seqs, n_rows, stream);
-        case 2: return launch_prefill_win<2, D, EB>(P, tk, tv, n_seqs, n_rows, stream);
-        case 4: return launch_prefill_win<4, D, EB>(P, tk, tv, n_seqs, n_rows, stream);
-        default: return launch_prefill_win<8, D, EB>(P, tk, tv, n_seqs, n_rows, stream);
+        case 1: return launch_prefill_win<1, D, EB, MOD>(P, tk, tv, n_seqs, n_rows, stream);
+        case 2: return launch_prefill_win<2, D, EB, MOD>(P, tk, tv, n_seqs, n_rows, stream);
+        case 4: return launch_prefill_win<4, D, EB, MOD>(P, tk, tv, n_seqs, n_rows, stream);
+        default: return launch_prefill_win<8, D, EB, MOD>(P, tk, tv, n_seqs, n_rows, stream);
     }
 }
 
