@@ -8,18 +8,18 @@
 // for K and V, for every KV head (or by a list for each one).
 //
 // In place and without a copy of the cache: keep[j] >= j, so whoever writes position j
-// last reads from positions >= j. A CTA takes one (sequence, KV head, K or V) - or a
-// slice of the rows' columns, which move independently - from the first position on, a
-// step of T tokens at a time: step s is stored after every thread has loaded steps up
-// to s + 1, and later steps read only positions beyond those that step s writes. So no
-// CTA waits for another, and a step's loads are in flight while the one before is
-// stored. Positions before the first moved one (keep[j] == j) are not touched.
+// last reads from positions >= j. A CTA, or a cluster of CTAs that share a step's
+// tokens, takes one (sequence, KV head, K or V) from the first position on, a step of
+// tokens at a time: a step is stored when all of its tokens are loaded (a barrier of the
+// cluster), and later steps read only positions beyond those it writes, so their loads
+// are in flight meanwhile. No CTA waits for one that may not be running. Positions before
+// the block of the first moved one (keep[j] == j) are not touched.
 //
 // With block-scaled E4M3 a block takes the largest scale of its new tokens and codes
 // of tokens from quieter blocks are encoded again: code * old / new, exact unless the
-// result is an E4M3 subnormal (scales are powers of two). Column slices of one head
-// then form a cluster, so that no slice's block scales are replaced while another reads
-// them.
+// result is an E4M3 subnormal (scales are powers of two). A step's scales are read
+// before the barrier of an earlier step, and so before any that it reads is replaced.
+#include <stdlib.h>
 #include "pa_common.cuh"
 
 namespace {
@@ -27,7 +27,6 @@ namespace {
 constexpr int kBS = 16;
 constexpr int kThreads = 256;
 constexpr int kUnroll = 8;  // 16-byte loads in flight a thread and step
-constexpr uint32_t kNone = 0xffffffffu;
 constexpr unsigned kFull = 0xffffffffu;
 
 struct CompactParams {
@@ -64,9 +63,9 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t w, float f) {
     return lo | (hi << 16);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+// A barrier of the cluster's threads (of the CTA's, where it is alone), in two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // The first position of a list that moves (n: none does). Whether keep[j] == j holds
 // for a leading part of an ascending list only, so samples narrow it down by the
@@ -93,11 +92,13 @@ __device__ int first_moved(const int32_t* keep, int n) {
     return lo;
 }
 
-// C: 16-byte chunks of a row that the CTA moves; grid (column slices, 2 * KV heads, sequences).
+// C: 16-byte chunks of a row; grid (CTAs of a cluster, 2 * KV heads, sequences).
 template <int C, bool BSC>
 __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const CompactParams P) {
-    constexpr int kPerPass = kThreads / C, T = kPerPass * kUnroll;  // tokens a pass, a step
-    __shared__ uint32_t src[4][T], dst[4][T];                       // slots (block * 16 + offset) or kNone
+    constexpr int kPerPass = kThreads / C, T = kPerPass * kUnroll;  // tokens a pass, a CTA's share of a step
+    constexpr int F = (T + kThreads - 1) / kThreads;                // tokens a thread looks up a step
+    constexpr int kRow = C * 16, kTile = kBS * kRow;                // bytes of a row, of a block's tile
+    __shared__ long long src[4][T], dst[4][T / kBS];                // byte offsets in the pool; none: negative
     __shared__ float factor[BSC ? 4 : 1][BSC ? T : 1], new_scale[BSC ? 4 : 1][BSC ? T / kBS : 1];
     const int tid = threadIdx.x, side = blockIdx.y & 1, h = blockIdx.y >> 1, b = blockIdx.z;
     pa::launch_dependents();
@@ -109,39 +110,67 @@ __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const Compa
     const int32_t* table = P.tables + (size_t)b * P.max_blocks;
     const int moved = first_moved(keep, n);
     if (moved >= n) return;
-    const int j0 = moved / kBS * kBS;
-    const int steps = (n - j0 + T - 1) / T;
+    const int stride = (int)gridDim.x * T;  // tokens of a step
+    const int j0 = moved / kBS * kBS + (int)blockIdx.x * T;
+    const int steps = (int)(((long long)n - moved / kBS * kBS + stride - 1) / stride);
     unsigned char* pool = side ? P.pool[1] : P.pool[0];
     float* scales = side ? P.scale[1] : P.scale[0];
 
-    // where the tokens of a step come from and go to
-    auto fetch = [&](int s) {
+    // Where the tokens of a step come from and go to: list, table and scale are three loads deep, so
+    // each is issued a step after the one it needs, and none is waited for at once.
+    int kept[F], before[F];             // of step s + 5 (during step s)
+    int from[F], src_block[F], dst_block[F];  // s + 4
+    int from2[F], src2[F], dst2[F];     // s + 3
+    float scale[F];
+    auto position = [&](int s, int f) {  // of the token, or -1
+        const int t = f * kThreads + tid;
+        const long long j = j0 + (long long)s * stride + t;
+        return s < steps && t < T && j < n ? (int)j : -1;
+    };
+    auto ask_list = [&](int s) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int j = position(s, f);
+            kept[f] = j >= 0 ? keep[j] : -1;
+            before[f] = j > 0 ? keep[j - 1] : -1;
+        }
+    };
+    auto ask_table = [&](int s) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int j = position(s, f), k = kept[f];
+            const bool good = j >= 0 && k >= j && k > before[f] && k / kBS < P.max_blocks;
+            if (j >= 0 && !good) pa::set_error(P.err, PA_DEVERR_POSITION);
+            from[f] = good ? k % kBS : -1;
+            src_block[f] = good ? table[k / kBS] : 0;
+            dst_block[f] = good ? table[j / kBS] : 0;
+        }
+    };
+    auto ask_scale = [&]() {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            from2[f] = from[f];
+            src2[f] = src_block[f];
+            dst2[f] = dst_block[f];
+            if (from2[f] >= 0 && !(src2[f] >= 0 && src2[f] < P.num_blocks && dst2[f] >= 0 && dst2[f] < P.num_blocks)) {
+                pa::set_error(P.err, PA_DEVERR_BLOCK_ID);
+                from2[f] = -1;
+            }
+            if constexpr (BSC) scale[f] = from2[f] >= 0 ? scales[(size_t)src2[f] * P.n_kv_heads + h] : 0.f;
+        }
+    };
+    auto note = [&](int s) {
         const int buf = s & 3;
 #pragma unroll
-        for (int t0 = 0; t0 < T; t0 += kThreads) {
-            const int t = t0 + tid;
+        for (int f = 0; f < F; ++f) {
+            const int t = f * kThreads + tid;
             if (T < kThreads && t >= T) break;  // whole warps
-            const int j = j0 + s * T + t;
-            uint32_t from = kNone, to = kNone;
-            float old = 0.f;
-            if (s < steps && j < n) {
-                const int k = keep[j], before = j > 0 ? keep[j - 1] : -1;
-                if (k < j || k <= before || k / kBS >= P.max_blocks) {
-                    pa::set_error(P.err, PA_DEVERR_POSITION);
-                } else {
-                    const int sb = table[k / kBS], db = table[j / kBS];
-                    if (sb < 0 || sb >= P.num_blocks || db < 0 || db >= P.num_blocks) {
-                        pa::set_error(P.err, PA_DEVERR_BLOCK_ID);
-                    } else {
-                        from = (uint32_t)sb * kBS + k % kBS;
-                        to = (uint32_t)db * kBS + j % kBS;
-                        if constexpr (BSC) old = clamp_scale(scales[(size_t)sb * P.n_kv_heads + h]);
-                    }
-                }
-            }
-            src[buf][t] = from;
-            dst[buf][t] = to;
+            src[buf][t] = from2[f] >= 0 ? ((long long)src2[f] * P.n_kv_heads + h) * kTile + from2[f] * kRow : -1;
+            // the block's first good token (all of them have the same destination) notes it
+            const unsigned good = __ballot_sync(kFull, from2[f] >= 0) & (0xffffu << (tid & 16));
+            if (good && (tid & 31) == __ffs(good) - 1) dst[buf][t / kBS] = ((long long)dst2[f] * P.n_kv_heads + h) * kTile;
             if constexpr (BSC) {
+                const float old = from2[f] >= 0 ? clamp_scale(scale[f]) : 0.f;
                 float most = old;
 #pragma unroll
                 for (int o = 1; o < kBS; o <<= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
@@ -151,75 +180,85 @@ __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const Compa
         }
     };
     const int c = tid % C, tp = tid / C;
-    const size_t column = (size_t)blockIdx.x * (C * 16) + c * 16;
-    auto row = [&](uint32_t slot) {
-        return pool + (((size_t)(slot / kBS) * P.n_kv_heads + h) * kBS + slot % kBS) * P.row_bytes + column;
-    };
+    unsigned char* in = pool + c * 16;
+    unsigned char* out = in + (tp % kBS) * kRow;
     auto load = [&](int s, uint4 (&v)[kUnroll]) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const uint32_t from = src[s & 3][u * kPerPass + tp];
-            v[u] = from != kNone ? __ldcg(reinterpret_cast<const uint4*>(row(from))) : make_uint4(0, 0, 0, 0);
+            const long long at = src[s & 3][u * kPerPass + tp];
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (at >= 0) v[u] = __ldcg(reinterpret_cast<const uint4*>(in + at));
         }
     };
     auto store = [&](int s, uint4 (&v)[kUnroll]) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int t = u * kPerPass + tp;
-            const uint32_t to = dst[s & 3][t];
-            if (to == kNone) continue;
+            if (src[s & 3][t] < 0) continue;
             if constexpr (BSC) {
                 const float f = factor[s & 3][t];
                 if (f != 1.f) v[u] = make_uint4(scale_codes(v[u].x, f), scale_codes(v[u].y, f), scale_codes(v[u].z, f), scale_codes(v[u].w, f));
             }
-            *reinterpret_cast<uint4*>(row(to)) = v[u];
+            *reinterpret_cast<uint4*>(out + dst[s & 3][t / kBS]) = v[u];
         }
         if constexpr (BSC) {
-            if (blockIdx.x == 0 && tid < T / kBS && new_scale[s & 3][tid] > 0.f) {
-                // a token of the block is valid, so the block is in the table's and the pool's range
-                const int db = table[(j0 + s * T) / kBS + tid];
-                scales[(size_t)db * P.n_kv_heads + h] = new_scale[s & 3][tid];
-            }
+            if (tid < T / kBS && new_scale[s & 3][tid] > 0.f)
+                scales[dst[s & 3][tid] / kTile] = new_scale[s & 3][tid];  // [block][KV head]
         }
     };
-    // Buffer s & 3 is filled two steps ahead and read until step s is stored, a barrier before it is filled again.
-    auto sync = [&]() {
-        if constexpr (BSC) cluster_sync();
-        else __syncthreads();
+    // Step s is stored once every thread of the cluster holds its tokens. What a step's place and
+    // scales need is noted two steps ahead, in buffer s & 3, which is read until that step is stored.
+    auto step = [&](int s, uint4 (&now)[kUnroll], uint4 (&next)[kUnroll]) {
+        note(s + 2);
+        ask_scale();
+        ask_table(s + 4);
+        ask_list(s + 5);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)  // they have arrived
+            asm volatile("" : "+r"(now[u].x), "+r"(now[u].y), "+r"(now[u].z), "+r"(now[u].w)::"memory");
+        cluster_arrive();
+        load(s + 1, next);
+        cluster_wait();
+        store(s, now);
     };
-    uint4 even[kUnroll], odd[kUnroll];
-    fetch(0);
-    fetch(1);
+    // the look-ups' first steps, one after the other; during step s: note s + 2, scale s + 3, table s + 4, list s + 5
+    ask_list(0);
+    ask_table(0);
+    ask_list(1);
+    ask_scale();   // 0
+    ask_table(1);
+    ask_list(2);
+    note(0);
+    ask_scale();   // 1
+    ask_table(2);
+    ask_list(3);
+    note(1);
+    ask_scale();   // 2
+    ask_table(3);
+    ask_list(4);
     __syncthreads();
+    uint4 even[kUnroll], odd[kUnroll];
     load(0, even);
     for (int s = 0; s < steps; s += 2) {
-        load(s + 1, odd);
-        fetch(s + 2);
-        sync();
-        store(s, even);
-        if (s + 1 < steps) {
-            load(s + 2, even);
-            fetch(s + 3);
-            sync();
-            store(s + 1, odd);
-        }
+        step(s, even, odd);
+        if (s + 1 < steps) step(s + 1, odd, even);
     }
 }
 
 template <int C, bool BSC>
-int launch_compact(const CompactParams& P, int slices, int n_seqs, cudaStream_t stream) {
+int launch_compact(const CompactParams& P, int ctas, int n_seqs, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(slices, 2 * P.n_kv_heads, n_seqs);
+    cfg.gridDim = dim3(ctas, 2 * P.n_kv_heads, n_seqs);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = slices;
+    attr[1].val.clusterDim.x = ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = BSC ? 2 : 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, compact_blocks_kernel<C, BSC>, P) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -242,8 +281,9 @@ extern "C" int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, flo
         (k_scale == nullptr) != (v_scale == nullptr) || (k_scale && elem_bytes != 1))
         return PA_ERR_INVALID_ARG;
     if (block_size != kBS || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
-    if (n_kv_heads > 32767 || n_seqs > 65535 || (long long)num_blocks * kBS >= (long long)kNone) return PA_ERR_UNSUPPORTED;
+    if (n_kv_heads > 32767 || n_seqs > 65535) return PA_ERR_UNSUPPORTED;
     if (n_seqs == 0 || n_kept == 0) return PA_OK;
+    if (max_blocks_per_seq == 0) return PA_ERR_INVALID_ARG;
     if (!k_pool || !v_pool || !block_tables || !keep || !keep_start_loc) return PA_ERR_INVALID_ARG;
     if (!pa_aligned16(k_pool) || !pa_aligned16(v_pool) || k_pool == v_pool || (k_scale && k_scale == v_scale) ||
         ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) | reinterpret_cast<uintptr_t>(block_tables) |
@@ -266,20 +306,17 @@ extern "C" int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, flo
     P.max_blocks = max_blocks_per_seq;
     P.num_blocks = num_blocks;
     P.err = err;
-    // Few (sequence, head, K or V) are sliced by columns until there are two CTAs for each SM: rows of
-    // 64 bytes at the least with block scales, 32 without.
-    int chunks = P.row_bytes / 16, slices = 1;
-    const int least = k_scale ? 4 : 2;
-    while (chunks > least && 2LL * n_kv_heads * n_seqs * slices < 2LL * sms) {
-        chunks /= 2;
-        slices *= 2;
-    }
+    const int chunks = P.row_bytes / 16, tokens = kThreads / chunks * kUnroll;
+    const long long units = 2LL * n_kv_heads * n_seqs;
+    const char* e_ = getenv("PA_X");
+    const double want_ = e_ ? atof(e_) : 2.0;
+    int ctas = 1;
+    while (ctas < 8 && units * ctas < want_ * sms && (long long)n_kept > (long long)n_seqs * ctas * tokens) ctas *= 2;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (k_scale) return chunks == 8 ? launch_compact<8, true>(P, slices, n_seqs, st) : launch_compact<4, true>(P, slices, n_seqs, st);
+    if (k_scale) return chunks == 8 ? launch_compact<8, true>(P, ctas, n_seqs, st) : launch_compact<4, true>(P, ctas, n_seqs, st);
     switch (chunks) {
-        case 2: return launch_compact<2, false>(P, slices, n_seqs, st);
-        case 4: return launch_compact<4, false>(P, slices, n_seqs, st);
-        case 8: return launch_compact<8, false>(P, slices, n_seqs, st);
-        default: return launch_compact<16, false>(P, slices, n_seqs, st);
+        case 4: return launch_compact<4, false>(P, ctas, n_seqs, st);
+        case 8: return launch_compact<8, false>(P, ctas, n_seqs, st);
+        default: return launch_compact<16, false>(P, ctas, n_seqs, st);
     }
 }

@@ -245,25 +245,23 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return y;
 }
 
-__device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either is
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-    return r;
+// tanh for scores. Below kTanhSmall in magnitude x (1 + z P(z)), z = x^2, P the
+// polynomial of degree 4 whose largest relative error there is least (a linear program
+// over 6,000 points): 2^-20.3 with its coefficients and steps in fp32. Above,
+// 1 - 2 / (1 + e^(2|x|)), off by a few 2^-23; below, that form would lose what it
+// subtracts, and with it a score that a wide cap hardly bends. (The hardware's
+// approximate tanh is off by 2^-11: at a cap of 50, 2% of a weight.)
+constexpr float kTanhSmall = 1.f;
+__device__ constexpr float tanh_coef(int i) {
+    return i == 0 ? -0.3333028f : i == 1 ? 0.1328849f : i == 2 ? -0.05176828f : i == 3 ? 0.01690641f : -0.003126577f;
 }
-
-// tanh for scores. Below kTanhSmall in magnitude x + x^3 P(x^2), P the polynomial of
-// degree 3 whose relative error to tanh is least (a linear program over 4,000 points
-// of [0, 0.7]): 2^-21.6. Above, 1 - 2 / (1 + e^(2|x|)), off by a few 2^-23; below,
-// that form would lose what it subtracts, and a score that a wide cap hardly bends
-// with it. (The hardware's approximate tanh is off by 2^-11: at a cap of 50, 2% of a
-// weight.)
-constexpr float kTanhSmall = 0.7f;
-constexpr float kTanhC[4] = {-0.33330938622f, 0.13286074149f, -0.05096434607f, 0.01388524047f};
 __device__ __forceinline__ float tanh_f32(float x) {
     const float z = x * x, a = fabsf(x);
-    const float p = fmaf(fmaf(fmaf(kTanhC[3], z, kTanhC[2]), z, kTanhC[1]), z, kTanhC[0]);
+    float q = tanh_coef(4);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) q = fmaf(q, z, tanh_coef(i));
     const float big = fmaf(-2.f, fast_rcp(1.f + fast_exp2(a * 2.8853900817779268f)), 1.f);
-    return a < kTanhSmall ? fmaf(x * z, p, x) : copysignf(big, x);
+    return a < kTanhSmall ? x * fmaf(q, z, 1.f) : copysignf(big, x);
 }
 
 }  // namespace pa

@@ -329,53 +329,56 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
 }
 
 // The scores of 32 keys of a row, reshaped in place: in, products q.k; out, in base-2
-// units, cap2 tanh(q.k * k) - slope2 * distance (cap2 0: q.k * k). k: the factors of the
-// two blocks; back: how far the row is behind each block's first key (BOTH: it may be
-// before a key).
-// tanh x = 1 - 2 / (1 + e^(2x)): two exponentials a score with the softmax's, and one
-// reciprocal for four scores, r = 1 / (abcd) giving 1 / a = r b cd and so on (an
-// argument of 2^30 at most keeps the product finite and changes nothing: 1 - 2^-29 is 1
-// in fp32). Off by a few 2^-23 absolute, so a score by cap times that: for caps above
-// kWideCap pa::tanh_f32 takes over, which is as exact relative to the score.
+// units, cap2 tanh(q.k * k), or q.k * k where cap2 is 0. k: the factors of the two blocks.
+// A warp takes the polynomial of pa::tanh_f32 while its largest |x| allows (a cap of 50
+// hardly ever sees scores beyond 50): six packed multiply-adds for two scores, and no
+// special function, of which the softmax's own exponential keeps the unit half busy.
+// Else 1 - 2 / (1 + e^(2x)), an exponential more a score and one reciprocal for four:
+// r = 1 / (abcd) gives 1 / a = r b cd and so on (|x| <= 10 keeps the product finite).
+// Off by a few 2^-23 of the cap; so above kWideCap2, and for |x| > 10,
+// pa::tanh_f32 itself, exact relative to the score.
 constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
-template <bool BOTH>
-__device__ __forceinline__ void reshape_scores(uint32_t (&raw)[32], const float (&k)[2], float cap2, float slope2,
-                                               const float (&back)[2]) {
+__device__ __forceinline__ void reshape_scores(uint32_t (&raw)[32], const float (&k)[2], float cap2) {
     auto pair = [&](int w) { return make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])); };
     auto put = [&](int w, float2 v) {
         raw[2 * w] = __float_as_uint(v.x);
         raw[2 * w + 1] = __float_as_uint(v.y);
     };
-    if (cap2 > 0.f && cap2 <= kWideCap2) {
-        const float2 one = make_float2(1.f, 1.f), c0 = make_float2(cap2, cap2), c1 = make_float2(-2.f * cap2, -2.f * cap2);
+    auto both = [](float x) { return make_float2(x, x); };
+    if (cap2 == 0.f) {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) put(w, __fmul2_rn(pair(w), both(k[w >> 3])));
+        return;
+    }
+    float most[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) most[i >> 4] = fmaxf(most[i >> 4], fabsf(__uint_as_float(raw[i])));
+    const float largest = fmaxf(most[0] * fabsf(k[0]), most[1] * fabsf(k[1]));
+    if (!__any_sync(kFull, largest >= pa::kTanhSmall)) {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            const float2 x = __fmul2_rn(pair(w), both(k[w >> 3])), z = __fmul2_rn(x, x);
+            float2 q = both(pa::tanh_coef(4) * cap2);
+#pragma unroll
+            for (int i = 3; i >= 0; --i) q = __ffma2_rn(q, z, both(pa::tanh_coef(i) * cap2));
+            put(w, __fmul2_rn(x, __ffma2_rn(q, z, both(cap2))));
+        }
+    } else if (cap2 <= kWideCap2 && !__any_sync(kFull, largest > 10.f)) {
 #pragma unroll
         for (int w = 0; w < 16; w += 2) {
-            const float f = k[w >> 3] * 2.8853900817779268f;
-            float2 a = __fmul2_rn(pair(w), make_float2(f, f)), c = __fmul2_rn(pair(w + 1), make_float2(f, f));
-            a = __fadd2_rn(make_float2(pa::fast_exp2(pa::min_nan(a.x, 30.f)), pa::fast_exp2(pa::min_nan(a.y, 30.f))), one);
-            c = __fadd2_rn(make_float2(pa::fast_exp2(pa::min_nan(c.x, 30.f)), pa::fast_exp2(pa::min_nan(c.y, 30.f))), one);
-            const float2 ac = __fmul2_rn(a, c);              // (a.x c.x, a.y c.y)
+            const float2 f = both(k[w >> 3] * 2.8853900817779268f);
+            float2 a = __fmul2_rn(pair(w), f), c = __fmul2_rn(pair(w + 1), f);
+            a = __fadd2_rn(make_float2(pa::fast_exp2(a.x), pa::fast_exp2(a.y)), both(1.f));
+            c = __fadd2_rn(make_float2(pa::fast_exp2(c.x), pa::fast_exp2(c.y)), both(1.f));
+            const float2 ac = __fmul2_rn(a, c);  // (a.x c.x, a.y c.y)
             const float r = pa::fast_rcp(ac.x * ac.y);
-            const float2 rr = __fmul2_rn(make_float2(ac.y, ac.x), make_float2(r, r));  // 1 / (a.x c.x), 1 / (a.y c.y)
-            put(w, __ffma2_rn(__fmul2_rn(rr, c), c1, c0));
-            put(w + 1, __ffma2_rn(__fmul2_rn(rr, a), c1, c0));
+            const float2 rr = __fmul2_rn(make_float2(ac.y, ac.x), both(r));  // 1 / (a.x c.x), 1 / (a.y c.y)
+            put(w, __ffma2_rn(__fmul2_rn(rr, c), both(-2.f * cap2), both(cap2)));
+            put(w + 1, __ffma2_rn(__fmul2_rn(rr, a), both(-2.f * cap2), both(cap2)));
         }
     } else {
 #pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            float2 x = __fmul2_rn(pair(w), make_float2(k[w >> 3], k[w >> 3]));
-            if (cap2 > 0.f) x = make_float2(cap2 * pa::tanh_f32(x.x), cap2 * pa::tanh_f32(x.y));
-            put(w, x);
-        }
-    }
-    if (slope2 != 0.f) {
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            const float at = (float)(2 * w & (kBS - 1));
-            float2 d = __fadd2_rn(make_float2(back[w >> 3], back[w >> 3]), make_float2(-at, -at - 1.f));
-            if constexpr (BOTH) d = make_float2(fabsf(d.x), fabsf(d.y));
-            put(w, __ffma2_rn(d, make_float2(-slope2, -slope2), pair(w)));
-        }
+        for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(cap2 * pa::tanh_f32(__uint_as_float(raw[i]) * k[i >> 4]));
     }
 }
 
@@ -861,7 +864,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
                         const int b = EB == 1 ? w >> 3 : 0;
-                        const float nm = qe[b] - m_used;
+                        const float nm = qe[MOD ? w >> 3 : b] - m_used;
                         float2 e = make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1]));
                         if constexpr (MOD) e = __fadd2_rn(e, make_float2(nm, nm));  // (scaled already)
                         else e = __ffma2_rn(e, EB == 1 ? make_float2(qk[b], qk[b]) : sc2, make_float2(nm, nm));
@@ -910,10 +913,33 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                 for (int k = 0; k < 32; ++k)
                                     if (!(visible & (1u << k))) raw[k] = 0u;
                             }
-                            float back[2];  // how far the row is behind key 0 of the quarter's two blocks
+                            if constexpr (EB == 2) qe[1] = qe[0];
+                            reshape_scores(raw, qk, P.cap2);
+                            if (P.slopes) {
+                                // -slope2 (back - at): the keys' places `at` in their block here, the row's distance
+                                // `back` to the block's first key with the exponent
+                                auto biased = [&](int w, float2 at, float by) {
+                                    const float2 v = __ffma2_rn(at, make_float2(by, by), make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])));
+                                    raw[2 * w] = __float_as_uint(v.x);
+                                    raw[2 * w + 1] = __float_as_uint(v.y);
+                                };
+                                float back[2];
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) back[b] = (float)(pos - keys.position(tile_of(j), 32 * qd + kBS * b));
-                            reshape_scores<decltype(masked)::value>(raw, qk, P.cap2, slope2, back);
+                                for (int b = 0; b < 2; ++b) {
+                                    back[b] = (float)(pos - keys.position(tile_of(j), 32 * qd + kBS * b));
+                                    qe[b] = fmaf(-slope2, back[b], qe[b]);
+                                }
+#pragma unroll
+                                for (int w = 0; w < 16; ++w) biased(w, make_float2(2 * w & 15, (2 * w & 15) + 1), slope2);
+                                if constexpr (decltype(masked)::value) {
+                                    if (P.prefix) {  // a key after the row, at > back: its distance is at - back
+#pragma unroll
+                                        for (int w = 0; w < 16; ++w)
+                                            biased(w, make_float2(fmaxf((2 * w & 15) - back[w >> 3], 0.f), fmaxf((2 * w & 15) + 1 - back[w >> 3], 0.f)),
+                                                   -2.f * slope2);
+                                    }
+                                }
+                            }
                         }
                         uint32_t ph[16];
                         float add;
@@ -929,7 +955,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                     const bool vis = !decltype(masked)::value || (visible & (1u << k));
                                     const float r = __uint_as_float(raw[k]);
                                     const int b = EB == 1 ? k >> 4 : 0;
-                                    if (vis) qmax = fmaxf(qmax, MOD ? r + qe[b] : fmaf(r, qk[b], qe[b]));
+                                    if (vis) qmax = fmaxf(qmax, MOD ? r + qe[k >> 4] : fmaf(r, qk[b], qe[b]));
                                 }
                                 const float mq = ceilf(qmax);
                                 if (mq > m_used) {
