@@ -19,19 +19,33 @@
 // of tokens from quieter blocks are encoded again: code * old / new, exact unless the
 // result is an E4M3 subnormal (scales are powers of two). A step's scales are read
 // before the barrier of an earlier step, and so before any that it reads is replaced.
-#include <stdlib.h>
+//
+// Bound by HBM: every moved byte is read once and written once. 32 chats of 2,000 to
+// 8,192 tokens that keep a third, a list for each of 8 heads (128 dims, bf16): 72 us,
+// 5.5 TB/s, 0.81 of a copy. One document of 131,072 tokens that keeps 0.6: 124 us,
+// 5.2 TB/s (16 clusters of 8; whole rows in a CTA's own columns, each with all the
+// look-ups, took 302). 6 documents of 23,000 to 65,000 tokens in block-scaled E4M3: 84 us,
+// 5.4 TB/s. 100 chats, a list for all heads: 143 us, 6.3 TB/s.
 #include "pa_common.cuh"
 
 namespace {
 
 constexpr int kBS = 16;
 constexpr int kThreads = 256;
-constexpr int kUnroll = 8;  // 16-byte loads in flight a thread and step
+constexpr int kUnroll = 8;    // 16-byte copies a thread and step
+// Steps in the ring of copies: two CTAs' rings and notes fill an SM's shared memory. Rows of
+// 64 bytes with block scales are more tokens a step, with more notes (64 chats of 2,000 to
+// 8,000 tokens: 83 us, 119 with three steps and one CTA an SM).
+template <int C, bool BSC>
+constexpr int kSteps = BSC && C == 4 ? 2 : 3;
+constexpr int kNotes = 8;     // steps whose places are held
+constexpr uint32_t kNone = 0xffffffffu;
 constexpr unsigned kFull = 0xffffffffu;
 
 struct CompactParams {
     unsigned char* pool[2];  // K, V
     float* scale[2];
+    int n_kept;
     const int32_t* tables;
     const int32_t* keep;
     const int32_t* starts;
@@ -63,9 +77,12 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t w, float f) {
     return lo | (hi << 16);
 }
 
-// A barrier of the cluster's threads (of the CTA's, where it is alone), in two halves.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// A barrier of the cluster's threads, in two halves. Nothing is published by it: what it
+// orders are copies that have arrived, before the arrival, against stores after the wait.
+// (A releasing arrival waits until a thread's earlier stores are performed, a round trip
+// a step.)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 
 // The first position of a list that moves (n: none does). Whether keep[j] == j holds
 // for a leading part of an ascending list only, so samples narrow it down by the
@@ -97,15 +114,21 @@ template <int C, bool BSC>
 __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const CompactParams P) {
     constexpr int kPerPass = kThreads / C, T = kPerPass * kUnroll;  // tokens a pass, a CTA's share of a step
     constexpr int F = (T + kThreads - 1) / kThreads;                // tokens a thread looks up a step
-    constexpr int kRow = C * 16, kTile = kBS * kRow;                // bytes of a row, of a block's tile
-    __shared__ long long src[4][T], dst[4][T / kBS];                // byte offsets in the pool; none: negative
-    __shared__ float factor[BSC ? 4 : 1][BSC ? T : 1], new_scale[BSC ? 4 : 1][BSC ? T / kBS : 1];
+    constexpr int kRow = C * 16, S = kSteps<C, BSC>;                // bytes of a row, steps of the ring
+    __shared__ uint32_t src[kNotes][T], dst[kNotes][T / kBS];       // rows of the pool (dst: a block's first) or kNone
+    __shared__ float factor[BSC ? kNotes : 1][BSC ? T : 1], new_scale[BSC ? kNotes : 1][BSC ? T / kBS : 1];
+    extern __shared__ __align__(16) uint4 ring[];                   // [S][kUnroll][kThreads]
+    static_assert(kNotes >= S + 2, "places noted S steps ahead replace those of a step that all have stored");
     const int tid = threadIdx.x, side = blockIdx.y & 1, h = blockIdx.y >> 1, b = blockIdx.z;
     pa::launch_dependents();
     pa::grid_dependency_wait();
     const int first = P.starts[b], n = P.starts[b + 1] - first;
     // every CTA of a cluster takes the same branches: they share the sequence and the head
     if (n <= 0) return;
+    if (first < 0 || first > P.n_kept - n || P.max_blocks <= 0) {
+        if (tid == 0) pa::set_error(P.err, PA_DEVERR_POSITION);
+        return;
+    }
     const int32_t* keep = P.keep + h * P.keep_stride + first;
     const int32_t* table = P.tables + (size_t)b * P.max_blocks;
     const int moved = first_moved(keep, n);
@@ -118,9 +141,9 @@ __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const Compa
 
     // Where the tokens of a step come from and go to: list, table and scale are three loads deep, so
     // each is issued a step after the one it needs, and none is waited for at once.
-    int kept[F], before[F];             // of step s + 5 (during step s)
-    int from[F], src_block[F], dst_block[F];  // s + 4
-    int from2[F], src2[F], dst2[F];     // s + 3
+    int kept[F], before[F];
+    int from[F], src_block[F], dst_block[F];
+    int from2[F], src2[F], dst2[F];
     float scale[F];
     auto position = [&](int s, int f) {  // of the token, or -1
         const int t = f * kThreads + tid;
@@ -160,15 +183,15 @@ __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const Compa
         }
     };
     auto note = [&](int s) {
-        const int buf = s & 3;
+        const int buf = s % kNotes;
 #pragma unroll
         for (int f = 0; f < F; ++f) {
             const int t = f * kThreads + tid;
             if (T < kThreads && t >= T) break;  // whole warps
-            src[buf][t] = from2[f] >= 0 ? ((long long)src2[f] * P.n_kv_heads + h) * kTile + from2[f] * kRow : -1;
+            src[buf][t] = from2[f] >= 0 ? ((uint32_t)src2[f] * P.n_kv_heads + h) * kBS + from2[f] : kNone;
             // the block's first good token (all of them have the same destination) notes it
             const unsigned good = __ballot_sync(kFull, from2[f] >= 0) & (0xffffu << (tid & 16));
-            if (good && (tid & 31) == __ffs(good) - 1) dst[buf][t / kBS] = ((long long)dst2[f] * P.n_kv_heads + h) * kTile;
+            if (good && (tid & 31) == __ffs(good) - 1) dst[buf][t / kBS] = ((uint32_t)dst2[f] * P.n_kv_heads + h) * kBS;
             if constexpr (BSC) {
                 const float old = from2[f] >= 0 ? clamp_scale(scale[f]) : 0.f;
                 float most = old;
@@ -180,74 +203,83 @@ __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const Compa
         }
     };
     const int c = tid % C, tp = tid / C;
-    unsigned char* in = pool + c * 16;
-    unsigned char* out = in + (tp % kBS) * kRow;
-    auto load = [&](int s, uint4 (&v)[kUnroll]) {
+    unsigned char* column = pool + c * 16;
+    auto load = [&](int s) {  // a thread's chunks of a step into its places of the ring
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const long long at = src[s & 3][u * kPerPass + tp];
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (at >= 0) v[u] = __ldcg(reinterpret_cast<const uint4*>(in + at));
+            const uint32_t row = s < steps ? src[s % kNotes][u * kPerPass + tp] : kNone;
+            if (row != kNone)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(pa::smem_u32(&ring[(s % S * kUnroll + u) * kThreads + tid])),
+                             "l"(column + (size_t)row * kRow)
+                             : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto store = [&](int s, uint4 (&v)[kUnroll]) {
+    auto store = [&](int s) {
+        const int buf = s % kNotes;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int t = u * kPerPass + tp;
-            if (src[s & 3][t] < 0) continue;
+            if (src[buf][t] == kNone) continue;
+            uint4 v = ring[(s % S * kUnroll + u) * kThreads + tid];
             if constexpr (BSC) {
-                const float f = factor[s & 3][t];
-                if (f != 1.f) v[u] = make_uint4(scale_codes(v[u].x, f), scale_codes(v[u].y, f), scale_codes(v[u].z, f), scale_codes(v[u].w, f));
+                const float f = factor[buf][t];
+                if (f != 1.f) v = make_uint4(scale_codes(v.x, f), scale_codes(v.y, f), scale_codes(v.z, f), scale_codes(v.w, f));
             }
-            *reinterpret_cast<uint4*>(out + dst[s & 3][t / kBS]) = v[u];
+            *reinterpret_cast<uint4*>(column + (size_t)(dst[buf][t / kBS] + tp % kBS) * kRow) = v;
         }
         if constexpr (BSC) {
-            if (tid < T / kBS && new_scale[s & 3][tid] > 0.f)
-                scales[dst[s & 3][tid] / kTile] = new_scale[s & 3][tid];  // [block][KV head]
+            if (tid < T / kBS && new_scale[buf][tid] > 0.f) scales[dst[buf][tid] / kBS] = new_scale[buf][tid];  // [block][KV head]
         }
     };
-    // Step s is stored once every thread of the cluster holds its tokens. What a step's place and
-    // scales need is noted two steps ahead, in buffer s & 3, which is read until that step is stored.
-    auto step = [&](int s, uint4 (&now)[kUnroll], uint4 (&next)[kUnroll]) {
-        note(s + 2);
-        ask_scale();
-        ask_table(s + 4);
-        ask_list(s + 5);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)  // they have arrived
-            asm volatile("" : "+r"(now[u].x), "+r"(now[u].y), "+r"(now[u].z), "+r"(now[u].w)::"memory");
-        cluster_arrive();
-        load(s + 1, next);
-        cluster_wait();
-        store(s, now);
-    };
-    // the look-ups' first steps, one after the other; during step s: note s + 2, scale s + 3, table s + 4, list s + 5
+    // During step s: its tokens are stored; copies of the next S - 1 are in flight; the places of step
+    // s + S are noted, its successors looked up.
     ask_list(0);
     ask_table(0);
     ask_list(1);
-    ask_scale();   // 0
+    ask_scale();
     ask_table(1);
     ask_list(2);
-    note(0);
-    ask_scale();   // 1
-    ask_table(2);
-    ask_list(3);
-    note(1);
-    ask_scale();   // 2
-    ask_table(3);
-    ask_list(4);
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) {
+        note(s);
+        ask_scale();
+        ask_table(s + 2);
+        ask_list(s + 3);
+    }
     __syncthreads();
-    uint4 even[kUnroll], odd[kUnroll];
-    load(0, even);
-    for (int s = 0; s < steps; s += 2) {
-        step(s, even, odd);
-        if (s + 1 < steps) step(s + 1, odd, even);
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) load(s);
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+        note(s + S);
+        ask_scale();
+        ask_table(s + S + 2);
+        ask_list(s + S + 3);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this thread's part of step s is here
+        __syncthreads();  // and every thread's, and the notes
+        if (gridDim.x > 1) cluster_arrive();
+        load(s + S - 1);
+        if (gridDim.x > 1) cluster_wait();
+        store(s);
     }
 }
 
 template <int C, bool BSC>
 int launch_compact(const CompactParams& P, int ctas, int n_seqs, cudaStream_t stream) {
+    auto kern = compact_blocks_kernel<C, BSC>;
+    constexpr int kRing = kSteps<C, BSC> * kUnroll * kThreads * 16;
+    static bool attr_done[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) != cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return PA_ERR_CUDA;
+        attr_done[dev] = true;
+    }
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = kRing;
     cfg.gridDim = dim3(ctas, 2 * P.n_kv_heads, n_seqs);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
@@ -259,7 +291,7 @@ int launch_compact(const CompactParams& P, int ctas, int n_seqs, cudaStream_t st
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, compact_blocks_kernel<C, BSC>, P) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, P) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 int sm_count() {
@@ -281,9 +313,8 @@ extern "C" int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, flo
         (k_scale == nullptr) != (v_scale == nullptr) || (k_scale && elem_bytes != 1))
         return PA_ERR_INVALID_ARG;
     if (block_size != kBS || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
-    if (n_kv_heads > 32767 || n_seqs > 65535) return PA_ERR_UNSUPPORTED;
+    if (n_kv_heads > 32767 || n_seqs > 65535 || (long long)num_blocks * n_kv_heads * kBS >= (long long)kNone) return PA_ERR_UNSUPPORTED;
     if (n_seqs == 0 || n_kept == 0) return PA_OK;
-    if (max_blocks_per_seq == 0) return PA_ERR_INVALID_ARG;
     if (!k_pool || !v_pool || !block_tables || !keep || !keep_start_loc) return PA_ERR_INVALID_ARG;
     if (!pa_aligned16(k_pool) || !pa_aligned16(v_pool) || k_pool == v_pool || (k_scale && k_scale == v_scale) ||
         ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) | reinterpret_cast<uintptr_t>(block_tables) |
@@ -297,6 +328,7 @@ extern "C" int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, flo
     P.pool[1] = static_cast<unsigned char*>(v_pool);
     P.scale[0] = k_scale;
     P.scale[1] = v_scale;
+    P.n_kept = n_kept;
     P.tables = block_tables;
     P.keep = keep;
     P.starts = keep_start_loc;
@@ -306,12 +338,14 @@ extern "C" int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, flo
     P.max_blocks = max_blocks_per_seq;
     P.num_blocks = num_blocks;
     P.err = err;
+    // CTAs of a cluster: until there are two for each SM, as far as a sequence's tokens (on average) give each
+    // a step's share; up to 16 where 8 leave half of the SMs idle (4 sequences, one KV head: 43.5 and 27.0 us),
+    // as a larger cluster's barrier costs more (16 units of one document: 124 and 131 us).
     const int chunks = P.row_bytes / 16, tokens = kThreads / chunks * kUnroll;
     const long long units = 2LL * n_kv_heads * n_seqs;
-    const char* e_ = getenv("PA_X");
-    const double want_ = e_ ? atof(e_) : 2.0;
+    const int most = units * 8 <= sms / 2 ? 16 : 8;
     int ctas = 1;
-    while (ctas < 8 && units * ctas < want_ * sms && (long long)n_kept > (long long)n_seqs * ctas * tokens) ctas *= 2;
+    while (ctas < most && units * ctas < 2LL * sms && (long long)n_kept > (long long)n_seqs * ctas * tokens) ctas *= 2;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (k_scale) return chunks == 8 ? launch_compact<8, true>(P, ctas, n_seqs, st) : launch_compact<4, true>(P, ctas, n_seqs, st);
     switch (chunks) {

@@ -63,7 +63,7 @@ def _compact(capi, **over):
     (dict(eb=4), -1), (dict(D=96), -2), (dict(bs=8), -2), (dict(k=None), -1), (dict(v=P), -1), (dict(keep=None), -1),
     (dict(tab=None), -1), (dict(loc=None), -1), (dict(k=C.c_void_p(4104)), -1), (dict(keep=C.c_void_p(4098)), -1),
     (dict(ks=P), -1), (dict(ks=P, vs=C.c_void_p(8192)), -1), (dict(ks=P, vs=P, eb=1), -1),
-    (dict(ks=C.c_void_p(4098), vs=P, eb=1), -1), (dict(B=65536), -2), (dict(maxb=0), -1), (dict(Hk=0), -1),
+    (dict(ks=C.c_void_p(4098), vs=P, eb=1), -1), (dict(B=65536), -2), (dict(Hk=0), -1),
 ])
 def test_compact_argument_errors_need_no_device(capi, over, status):
     assert _compact(capi, **over) == status

@@ -163,6 +163,10 @@ def test_positions_it_cannot_use_are_skipped_and_flagged(pk):
                 j = at % 16
                 if scales is None:
                     assert np.array_equal(got[i][tables[0, at // 16], :, j], pools[i][tables[0, at // 16], :, j])
+        for loc in ([0, 41], [-1, 20], [2 ** 30, 2 ** 30 + 5]):   # a list beyond the entries
+            got, _ = run(pk, pools, scales, tables, keep, np.array(loc, np.int32))
+            check_device_error(256)
+            assert all(np.array_equal(a, b) for a, b in zip(got, pools))
         t = tables.copy()
         t[0, keep[30] // 16] = -1
         run(pk, pools, scales, t, keep, starts)
