@@ -46,6 +46,7 @@ struct PaPrefillParams {
     // none): keys before it are visible to earlier rows too
     int reshape;
     float cap2;
+    float poly[4], small;  // cap2 tanh(x) = y (poly[0] + poly[1] y^2 + ..) for |y| <= small; y = q.k, over E4M3 x
     const float* slopes;
     const int32_t* prefix;
 };
@@ -56,10 +57,19 @@ int pa_prefill_dispatch_sinks(int head_dim, int G, const PaPrefillParams& P, con
                               int n_seqs, int n_rows, cudaStream_t stream);
 int pa_prefill_dispatch_fp8(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
                             int n_seqs, int n_rows, cudaStream_t stream);
-int pa_prefill_dispatch_score(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
-                              int n_seqs, int n_rows, cudaStream_t stream);
-int pa_prefill_dispatch_score_fp8(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, int n_seqs, int n_rows, cudaStream_t stream);
+// of reshaped scores: with a cap alone, a bias by distance or none, both
+int pa_prefill_dispatch_cap(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                            int n_seqs, int n_rows, cudaStream_t stream);
+int pa_prefill_dispatch_cap_fp8(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                                int n_seqs, int n_rows, cudaStream_t stream);
+int pa_prefill_dispatch_bias(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                             int n_seqs, int n_rows, cudaStream_t stream);
+int pa_prefill_dispatch_bias_fp8(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 int n_seqs, int n_rows, cudaStream_t stream);
+int pa_prefill_dispatch_both(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                             int n_seqs, int n_rows, cudaStream_t stream);
+int pa_prefill_dispatch_both_fp8(int head_dim, int G, const PaPrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 int n_seqs, int n_rows, cudaStream_t stream);
 
 namespace {
 

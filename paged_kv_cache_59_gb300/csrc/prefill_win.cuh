@@ -328,42 +328,48 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
     }
 }
 
-// The scores of 32 keys of a row, reshaped in place: in, products q.k; out, in base-2
-// units, cap2 tanh(q.k * k), or q.k * k where cap2 is 0. k: the factors of the two blocks.
-// A warp takes the polynomial of pa::tanh_f32 while its largest |x| allows (a cap of 50
-// hardly ever sees scores beyond 50): six packed multiply-adds for two scores, and no
-// special function, of which the softmax's own exponential keeps the unit half busy.
-// Else 1 - 2 / (1 + e^(2x)), an exponential more a score and one reciprocal for four:
-// r = 1 / (abcd) gives 1 / a = r b cd and so on (|x| <= 10 keeps the product finite).
-// Off by a few 2^-23 of the cap; so above kWideCap2, and for |x| > 10,
-// pa::tanh_f32 itself, exact relative to the score.
+// Kernels of reshaped scores (pa_prefill_score_mod), one for each way to reshape them, as the
+// instructions of the others cost even where they are not taken (2,048 rows under a window of
+// 4,096, 32 heads: a bias 176 us in a kernel for all, 144 in its own): a cap alone, a bias by
+// distance or none (a prefix over plain scores), and both.
+enum { kPlain, kCap, kBias, kBoth };
+
+// The largest magnitude of a quarter's products, by its two blocks.
+__device__ __forceinline__ void largest_of(const uint32_t (&raw)[32], float (&most)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        most[b] = 0.f;
+#pragma unroll
+        for (int i = 16 * b; i < 16 * b + 16; i += 2)
+            asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(most[b]) : "f"(__uint_as_float(raw[i])), "f"(__uint_as_float(raw[i + 1])));
+    }
+}
+
+// A quarter's 32 scores, reshaped in place by whatever form of tanh their sizes ask for: in,
+// products q.k; out, in base-2 units, cap2 tanh(q.k * k), or q.k * k where cap2 is 0. k: the
+// factors of the two blocks.
+// - |x| < pa::kTanhSmall in the whole warp: the polynomial of pa::tanh_f32.
+// - Else 1 - 2 / (1 + e^(2x)), an exponential more a score and one reciprocal for four:
+//   r = 1 / (abcd) gives 1 / a = r b cd and so on (|x| <= 10 keeps the product finite). Off
+//   by a few 2^-23 of the cap, so for caps up to kWideCap2 only.
+// - Else pa::tanh_f32, exact relative to the score.
 constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ void reshape_scores(uint32_t (&raw)[32], const float (&k)[2], float cap2) {
     auto pair = [&](int w) { return make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])); };
     auto put = [&](int w, float2 v) {
         raw[2 * w] = __float_as_uint(v.x);
         raw[2 * w + 1] = __float_as_uint(v.y);
     };
-    auto both = [](float x) { return make_float2(x, x); };
     if (cap2 == 0.f) {
 #pragma unroll
         for (int w = 0; w < 16; ++w) put(w, __fmul2_rn(pair(w), both(k[w >> 3])));
         return;
     }
-    float most[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 32; ++i) most[i >> 4] = fmaxf(most[i >> 4], fabsf(__uint_as_float(raw[i])));
+    float most[2];
+    largest_of(raw, most);
     const float largest = fmaxf(most[0] * fabsf(k[0]), most[1] * fabsf(k[1]));
-    if (!__any_sync(kFull, largest >= pa::kTanhSmall)) {
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            const float2 x = __fmul2_rn(pair(w), both(k[w >> 3])), z = __fmul2_rn(x, x);
-            float2 q = both(pa::tanh_coef(4) * cap2);
-#pragma unroll
-            for (int i = 3; i >= 0; --i) q = __ffma2_rn(q, z, both(pa::tanh_coef(i) * cap2));
-            put(w, __fmul2_rn(x, __ffma2_rn(q, z, both(cap2))));
-        }
-    } else if (cap2 <= kWideCap2 && !__any_sync(kFull, largest > 10.f)) {
+    if (cap2 <= kWideCap2 && !__any_sync(kFull, largest > 10.f)) {
 #pragma unroll
         for (int w = 0; w < 16; w += 2) {
             const float2 f = both(k[w >> 3] * 2.8853900817779268f);
@@ -376,16 +382,32 @@ __device__ __forceinline__ void reshape_scores(uint32_t (&raw)[32], const float 
             put(w, __ffma2_rn(__fmul2_rn(rr, c), both(-2.f * cap2), both(cap2)));
             put(w + 1, __ffma2_rn(__fmul2_rn(rr, a), both(-2.f * cap2), both(cap2)));
         }
+    } else if (!__any_sync(kFull, largest >= pa::kTanhSmall)) {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            const float2 x = __fmul2_rn(pair(w), both(k[w >> 3])), z = __fmul2_rn(x, x);
+            float2 q = both(pa::tanh_coef(4) * cap2);
+#pragma unroll
+            for (int i = 3; i >= 0; --i) q = __ffma2_rn(q, z, both(pa::tanh_coef(i) * cap2));
+            put(w, __fmul2_rn(x, __ffma2_rn(q, z, both(cap2))));
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(cap2 * pa::tanh_f32(__uint_as_float(raw[i]) * k[i >> 4]));
     }
 }
 
-// MOD: scores are reshaped (pa_prefill_score_mod). A segment's tiles are then walked
-// from its last to its first: under a bias by distance the nearest keys, usually the
-// heaviest, set a row's reference, and far ones seldom raise it.
-template <int G, int D, int EB, bool MOD>
+// What a quarter's registers hold: products q.k (to be scaled; to be scaled and capped; to be
+// scaled and biased), or scores.
+enum { kProducts, kCapped, kBiased, kScores };
+template <int X>
+using Form = std::integral_constant<int, X>;
+
+// MOD: how scores are reshaped. A segment's tiles are then walked from its last to its
+// first: under a bias by distance the nearest keys, usually the heaviest, set a row's
+// reference, and far ones seldom raise it. With a cap alone the first is the last one that
+// all rows see whole, which gives a row 128 keys' largest score for a reference.
+template <int G, int D, int EB, int MOD>
 __global__ void __launch_bounds__(kWinThreads<EB>, 1)
 pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
@@ -427,7 +449,12 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
     Segment g;
     bool ok = true;  // after a failed wait a role goes on without waiting, so that no other role is left alone
     int J0 = 0;      // tiles of the segments before
-    auto tile_of = [&](int j) { return g.kt0 + (MOD ? g.n_kt - 1 - j : j); };  // the segment's j-th tile
+    auto tile_of = [&](int j) {  // the segment's j-th tile
+        if constexpr (MOD == kPlain) return g.kt0 + j;
+        constexpr int kEnd = (2 * QT + 2 * kKT - 2) / kKT;  // tiles that hold the rows' own positions, or one more
+        const int lead = MOD != kCap || g.n_kt <= kEnd ? 0 : kEnd;
+        return g.kt0 + g.n_kt - 1 - (j == 0 ? lead : j <= lead ? j - 1 : j);
+    };
 
     if (warp == 9 || warp == 14) {
         // ----------------------------------------------------------- TMA producers
@@ -786,7 +813,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             const int pos = g.ctx - g.L + i;  // this row's position (padding rows: beyond the chunk)
             const int limit = MOD ? max(pos, prefix_of(P, g.s, g.ctx) - 1) : pos;  // the last position it sees
             float slope2 = 0.f;
-            if constexpr (MOD) slope2 = P.slopes ? P.slopes[g.kvh * G + r % G] * 1.4426950408889634f : 0.f;
+            if constexpr (MOD >= kBias) slope2 = P.slopes ? P.slopes[g.kvh * G + r % G] * 1.4426950408889634f : 0.f;
             float m_used = -INFINITY, l = 0.f;
             // Key k of tile j is at position 128 j + k + kb_sinks if it is a sink, else + kb_win. In tiles
             // from j_win on, the limits below are those of the window's keys: where such a tile begins
@@ -843,8 +870,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 // three comparisons, a masked tile took twice a plain one's time).
                 const int lim0 = limit - kb;  // keys k > lim0 of the tile are not visible
                 const int lim1 = P.window >= 0 ? pos - kb - P.window : 0, sink1 = P.n_sinks - kb_sinks - jt * kKT;  // nor k < lim1, k >= sink1
-                // (MOD: and for one with a key after a row's own position, which a prefix may show)
-                const bool mask_warp = __any_sync(kFull, (MOD ? pos - kb : lim0) < kKT - 1 || (lim1 > 0 && sink1 < kKT));
+                // (With a bias also for one with a key after a row's own position, which a prefix may show.)
+                const bool mask_warp = __any_sync(kFull, (MOD >= kBias && P.slopes ? pos - kb : lim0) < kKT - 1 || (lim1 > 0 && sink1 < kKT));
                 auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };  // bits 0 .. n-1
                 auto visible_of = [&](int qd) {
                     const int k0 = 32 * qd;
@@ -859,15 +886,28 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 // Returns the quarter's sum of w; `add` is what it adds to the row's sum
                 // (E4M3: each block's sum over its V scale; bf16: the quarter's times 2^-e).
                 float qk[2] = {sc, sc}, qe[2] = {0.f, 0.f}, qi[2] = {1.f, 1.f};  // E4M3: the quarter's two blocks; bf16: [0]
-                auto exps = [&](auto masked, const uint32_t (&raw)[32], uint32_t visible, uint32_t (&ph)[16], float& add) {
+                // `form`: what raw holds
+                auto exps = [&](auto masked, auto form, const uint32_t (&raw)[32], uint32_t visible, uint32_t (&ph)[16], float& add) {
                     float2 qs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
                         const int b = EB == 1 ? w >> 3 : 0;
-                        const float nm = qe[MOD ? w >> 3 : b] - m_used;
+                        const float nm = qe[MOD >= kBias ? w >> 3 : b] - m_used;
                         float2 e = make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1]));
-                        if constexpr (MOD) e = __fadd2_rn(e, make_float2(nm, nm));  // (scaled already)
-                        else e = __ffma2_rn(e, EB == 1 ? make_float2(qk[b], qk[b]) : sc2, make_float2(nm, nm));
+                        if constexpr (decltype(form)::value == kScores) {
+                            e = __fadd2_rn(e, both(nm));
+                        } else if constexpr (decltype(form)::value == kCapped) {
+                            if constexpr (EB == 1) e = __fmul2_rn(e, both(qk[b]));  // bf16: in the coefficients
+                            const float2 z = __fmul2_rn(e, e);
+                            float2 q = both(P.poly[3]);
+#pragma unroll
+                            for (int i = 2; i >= 0; --i) q = __ffma2_rn(q, z, both(P.poly[i]));
+                            e = __ffma2_rn(e, q, both(nm));
+                        } else if constexpr (decltype(form)::value == kBiased) {
+                            e = __ffma2_rn(e, both(qk[b]), __ffma2_rn(make_float2(2 * w & 15, (2 * w & 15) + 1), both(slope2), both(nm)));
+                        } else {
+                            e = __ffma2_rn(e, EB == 1 ? both(qk[b]) : sc2, both(nm));
+                        }
                         if constexpr (decltype(masked)::value) {  // masked keys give p = 0 (also for a zero scale)
                             if (!(visible & (1u << (2 * w)))) e.x = -INFINITY;
                             if (!(visible & (1u << (2 * w + 1)))) e.y = -INFINITY;
@@ -906,47 +946,68 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             }
                         }
                         const uint32_t visible = decltype(masked)::value ? visible_of(qd) : 0xffffffffu;
-                        if constexpr (MOD) {
+                        // A bias -slope2 (back - at): the keys' places `at` in their block with the scores, the
+                        // row's distance `back` to the block's first key with the exponent.
+                        float back[2] = {0.f, 0.f};
+                        if constexpr (MOD >= kBias) {
+                            if constexpr (EB == 2) qe[1] = qe[0];
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                back[b] = (float)(pos - keys.position(tile_of(j), 32 * qd + kBS * b));
+                                qe[b] = fmaf(-slope2, back[b], qe[b]);
+                            }
+                        }
+                        auto scores_of = [&]() {  // whatever raw's products make, the bias's `at` among it
                             // keys hidden from the row may hold anything, and reshape_scores mixes four of them
                             if constexpr (decltype(masked)::value) {
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
                                     if (!(visible & (1u << k))) raw[k] = 0u;
                             }
-                            if constexpr (EB == 2) qe[1] = qe[0];
-                            reshape_scores(raw, qk, P.cap2);
-                            if (P.slopes) {
-                                // -slope2 (back - at): the keys' places `at` in their block here, the row's distance
-                                // `back` to the block's first key with the exponent
-                                auto biased = [&](int w, float2 at, float by) {
-                                    const float2 v = __ffma2_rn(at, make_float2(by, by), make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])));
+                            reshape_scores(raw, qk, MOD == kBias ? 0.f : P.cap2);
+                            if constexpr (MOD >= kBias) {
+                                auto add_bias = [&](int w, float2 at, float by) {
+                                    const float2 v = __ffma2_rn(at, both(by), make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])));
                                     raw[2 * w] = __float_as_uint(v.x);
                                     raw[2 * w + 1] = __float_as_uint(v.y);
                                 };
-                                float back[2];
 #pragma unroll
-                                for (int b = 0; b < 2; ++b) {
-                                    back[b] = (float)(pos - keys.position(tile_of(j), 32 * qd + kBS * b));
-                                    qe[b] = fmaf(-slope2, back[b], qe[b]);
-                                }
-#pragma unroll
-                                for (int w = 0; w < 16; ++w) biased(w, make_float2(2 * w & 15, (2 * w & 15) + 1), slope2);
+                                for (int w = 0; w < 16; ++w) add_bias(w, make_float2(2 * w & 15, (2 * w & 15) + 1), slope2);
                                 if constexpr (decltype(masked)::value) {
                                     if (P.prefix) {  // a key after the row, at > back: its distance is at - back
 #pragma unroll
                                         for (int w = 0; w < 16; ++w)
-                                            biased(w, make_float2(fmaxf((2 * w & 15) - back[w >> 3], 0.f), fmaxf((2 * w & 15) + 1 - back[w >> 3], 0.f)),
-                                                   -2.f * slope2);
+                                            add_bias(w, make_float2(fmaxf((2 * w & 15) - back[w >> 3], 0.f), fmaxf((2 * w & 15) + 1 - back[w >> 3], 0.f)),
+                                                     -2.f * slope2);
                                     }
                                 }
                             }
+                        };
+                        // Products go straight into the exponent while that is one form for all of them: a
+                        // quarter without hidden keys, and with a cap, scores that the short polynomial covers
+                        // (P.small: 0.6 of the cap; 2^-18.6 of the score, 2^-13.7 of a weight at a cap of 50,
+                        // half of P's own rounding). Measured for 2,048 rows under a window of 4,096.
+                        bool whole = !decltype(masked)::value && MOD != kBoth;
+                        if constexpr (MOD == kCap && !decltype(masked)::value) {
+                            float most[2];
+                            largest_of(raw, most);
+                            whole = !__any_sync(kFull, !((EB == 1 ? fmaxf(most[0] * fabsf(qk[0]), most[1] * fabsf(qk[1])) : fmaxf(most[0], most[1])) <= P.small));
                         }
                         uint32_t ph[16];
-                        float add;
-                        const float qs = exps(masked, raw, visible, ph, add);
+                        float add, qs;
+                        constexpr int kForm = MOD == kCap ? kCapped : MOD == kBias ? kBiased : kProducts;
+                        if constexpr (MOD == kPlain) {
+                            qs = exps(masked, Form<kProducts>{}, raw, visible, ph, add);
+                        } else if (!decltype(masked)::value && whole) {
+                            if constexpr (!decltype(masked)::value) qs = exps(masked, Form<kForm>{}, raw, visible, ph, add);
+                        } else {
+                            scores_of();
+                            qs = exps(masked, Form<kScores>{}, raw, visible, ph, add);
+                        }
                         const bool big = !(qs <= 32768.f);  // also inf (no reference yet) and NaN
                         if (__any_sync(kFull, big)) {
                             // rare: a new reference for the rows that need one
+                            if (MOD != kPlain && whole) scores_of();
                             float a = 1.f;
                             if (big) {
                                 float qmax = -INFINITY;
@@ -955,7 +1016,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                     const bool vis = !decltype(masked)::value || (visible & (1u << k));
                                     const float r = __uint_as_float(raw[k]);
                                     const int b = EB == 1 ? k >> 4 : 0;
-                                    if (vis) qmax = fmaxf(qmax, MOD ? r + qe[k >> 4] : fmaf(r, qk[b], qe[b]));
+                                    if (vis) qmax = fmaxf(qmax, MOD != kPlain ? r + qe[MOD >= kBias ? k >> 4 : b] : fmaf(r, qk[b], qe[b]));
                                 }
                                 const float mq = ceilf(qmax);
                                 if (mq > m_used) {
@@ -963,7 +1024,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                     const float d = m_used - mq;
                                     a = d < -126.f ? 0.f : __int_as_float(((int)d + 127) << 23);
                                     m_used = mq;
-                                    exps(masked, raw, visible, ph, add);
+                                    exps(masked, Form<MOD != kPlain ? kScores : kProducts>{}, raw, visible, ph, add);
                                 }
                             }
                             psum2.x *= a;
@@ -992,6 +1053,34 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         tc::tmem_st16(tS + 32 * qd, ph);
                     }
                 };
+                auto quarter_factors = [&](int qd, float (&k)[2], float (&e)[2]) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        k[b] = EB == 2 ? sc : __shfl_sync(kFull, my_k, 2 * qd + b);
+                        e[b] = EB == 2 ? v_exp[qd].x : __shfl_sync(kFull, my_e, 2 * qd + b);
+                    }
+                };
+                // The segment's first tile, seen whole: its largest score is the row's reference. From 32
+                // keys alone, as below, scores of a wide spread (6 either way) outgrew it again and again.
+                if (MOD == kCap && j == 0 && !mask_warp && sc >= 0.f) {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int qd = 0; qd < 4; ++qd) {
+                        uint32_t raw[32];
+                        tc::tmem_ld32(tS + 32 * qd, raw);
+                        tc::tmem_wait_ld();
+                        float k[2], e[2], most[2] = {-INFINITY, -INFINITY};
+                        quarter_factors(qd, k, e);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) most[i >> 4] = fmaxf(most[i >> 4], __uint_as_float(raw[i]));
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const float v = most[b] * k[b];
+                            top = fmaxf(top, fmaf(P.cap2, pa::tanh_f32(v), e[b]));
+                        }
+                    }
+                    m_used = ceilf(top);
+                }
                 if (mask_warp) sweep(std::true_type{});
                 else sweep(std::false_type{});
                 l = l * alpha + (psum2.x + psum2.y);
@@ -1228,7 +1317,7 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
     }
 }
 
-template <int G, int D, int EB, bool MOD>
+template <int G, int D, int EB, int MOD>
 int launch_prefill_win(const PrefillParams& Pp, const CUtensorMap& tk, const CUtensorMap& tv, int n_seqs,
                        int n_rows, cudaStream_t stream) {
     auto kern = pa_prefill_win_kernel<G, D, EB, MOD>;
@@ -1255,7 +1344,7 @@ int launch_prefill_win(const PrefillParams& Pp, const CUtensorMap& tk, const CUt
                          n_rows, Pp.n_qp);
 }
 
-template <int D, int EB, bool MOD = false>
+template <int D, int EB, int MOD = kPlain>
 int dispatch_prefill_win(int G, const PrefillParams& P, const CUtensorMap& tk, const CUtensorMap& tv, int n_seqs,
                          int n_rows, cudaStream_t stream) {
     switch (G) {
