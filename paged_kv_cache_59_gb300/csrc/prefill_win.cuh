@@ -983,12 +983,12 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                 }
                             }
                         };
-                        // Products go straight into the exponent while that is one form for all of them: a
-                        // quarter without hidden keys, and with a cap, scores that the short polynomial covers
-                        // (P.small: 0.6 of the cap; 2^-18.6 of the score, 2^-13.7 of a weight at a cap of 50,
-                        // half of P's own rounding). Measured for 2,048 rows under a window of 4,096.
-                        bool whole = !decltype(masked)::value && MOD != kBoth;
-                        if constexpr (MOD == kCap && !decltype(masked)::value) {
+                        // Products go straight into the exponent while that is one form for all of them: with a
+                        // cap, scores that the short polynomial covers (P.small: 0.6 of the cap; 2^-18.6 of the
+                        // score, 2^-13.7 of a weight at a cap of 50, half of P's own rounding); with a bias,
+                        // where no key can come after the row.
+                        bool whole = MOD == kCap || (MOD == kBias && !(decltype(masked)::value && P.prefix));
+                        if constexpr (MOD == kCap) {
                             float most[2];
                             largest_of(raw, most);
                             whole = !__any_sync(kFull, !((EB == 1 ? fmaxf(most[0] * fabsf(qk[0]), most[1] * fabsf(qk[1])) : fmaxf(most[0], most[1])) <= P.small));
@@ -998,8 +998,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         constexpr int kForm = MOD == kCap ? kCapped : MOD == kBias ? kBiased : kProducts;
                         if constexpr (MOD == kPlain) {
                             qs = exps(masked, Form<kProducts>{}, raw, visible, ph, add);
-                        } else if (!decltype(masked)::value && whole) {
-                            if constexpr (!decltype(masked)::value) qs = exps(masked, Form<kForm>{}, raw, visible, ph, add);
+                        } else if (MOD != kBoth && whole) {
+                            qs = exps(masked, Form<kForm>{}, raw, visible, ph, add);
                         } else {
                             scores_of();
                             qs = exps(masked, Form<kScores>{}, raw, visible, ph, add);
