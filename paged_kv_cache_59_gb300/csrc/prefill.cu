@@ -880,11 +880,11 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
     Pp.v_scale = v_scale;
     Pp.reshape = reshape;
     Pp.cap2 = softcap * 1.4426950408889634f;
-    // the coefficients of tanh(x) / x up to |x| = 0.6 (pa_common.cuh has the longer polynomial). bf16: of y = q.k, x = y c,
-    // as far as c^7 stays far from fp32's least; wide caps need tanh exact relative to the score
-    const double c = eb == 2 ? (double)Pp.scale_log2 : 1.0, tanh3[4] = {1.0, -0.33319074, 0.13086419, -0.04138779};
+    // the coefficients of tanh(x) / x up to |x| = 0.6 (pa_common.cuh has the longer polynomial), of y = q.k, x = y c, as
+    // far as c^7 stays far from fp32's least
+    const double c = (double)Pp.scale_log2, tanh3[4] = {1.0, -0.33319074, 0.13086419, -0.04138779};
     for (int i = 0; i < 4; ++i) Pp.poly[i] = (float)(Pp.cap2 * tanh3[i] * c * pow(c * c, i));
-    Pp.small = softcap > 0.f && softcap <= 128.f && fabs(c) >= 0x1p-15 ? (float)(0.6 / fabs(c)) : -1.f;
+    Pp.small = fabs(c) >= 0x1p-15 ? 0.6f : -1.f;
     Pp.slopes = slopes;
     Pp.prefix = prefix;
     // chunk rows bound for the merge grid (rows past the last chunk exit)
@@ -893,7 +893,7 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int nr = (int)n_rows;
     if (reshape) {
-        const bool bias = softcap == 0.f, cap = !bias && !slopes;
+        const bool bias = softcap == 0.f, cap = !bias && !slopes && softcap <= 128.f;
         const auto go = eb == 2 ? (cap ? pa_prefill_dispatch_cap : bias ? pa_prefill_dispatch_bias : pa_prefill_dispatch_both)
                                 : (cap ? pa_prefill_dispatch_cap_fp8 : bias ? pa_prefill_dispatch_bias_fp8 : pa_prefill_dispatch_both_fp8);
         return go(head_dim, G, Pp, tk, tv, n_seqs, nr, st);

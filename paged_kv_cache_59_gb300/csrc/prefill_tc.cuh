@@ -46,7 +46,7 @@ struct PaPrefillParams {
     // none): keys before it are visible to earlier rows too
     int reshape;
     float cap2;
-    float poly[4], small;  // cap2 tanh(x) = y (poly[0] + poly[1] y^2 + ..) for |y| <= small; y = q.k, over E4M3 x
+    float poly[4], small;  // cap2 tanh(x) = y (poly[0] + poly[1] y^2 + ..) for |x| <= small, y = q.k (bf16)
     const float* slopes;
     const int32_t* prefix;
 };

@@ -331,69 +331,53 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
 // Kernels of reshaped scores (pa_prefill_score_mod), one for each way to reshape them, as the
 // instructions of the others cost even where they are not taken (2,048 rows under a window of
 // 4,096, 32 heads: a bias 176 us in a kernel for all, 144 in its own): a cap alone, a bias by
-// distance or none (a prefix over plain scores), and both.
+// distance or none (a prefix over plain scores), and both, or a cap above 128.
 enum { kPlain, kCap, kBias, kBoth };
 
-// The largest magnitude of a quarter's products, by its two blocks.
-__device__ __forceinline__ void largest_of(const uint32_t (&raw)[32], float (&most)[2]) {
+// The largest |q.k * k| of a quarter's products; k: the factors of its two blocks.
+__device__ __forceinline__ float largest_of(const uint32_t (&raw)[32], const float (&k)[2]) {
+    float most[2] = {0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        most[b] = 0.f;
-#pragma unroll
-        for (int i = 16 * b; i < 16 * b + 16; i += 2)
-            asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(most[b]) : "f"(__uint_as_float(raw[i])), "f"(__uint_as_float(raw[i + 1])));
-    }
+    for (int i = 0; i < 32; i += 2)
+        asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(most[i >> 4]) : "f"(__uint_as_float(raw[i])), "f"(__uint_as_float(raw[i + 1])));
+    return fmaxf(most[0] * fabsf(k[0]), most[1] * fabsf(k[1]));
 }
 
-// A quarter's 32 scores, reshaped in place by whatever form of tanh their sizes ask for: in,
-// products q.k; out, in base-2 units, cap2 tanh(q.k * k), or q.k * k where cap2 is 0. k: the
-// factors of the two blocks.
-// - |x| < pa::kTanhSmall in the whole warp: the polynomial of pa::tanh_f32.
-// - Else 1 - 2 / (1 + e^(2x)), an exponential more a score and one reciprocal for four:
-//   r = 1 / (abcd) gives 1 / a = r b cd and so on (|x| <= 10 keeps the product finite). Off
-//   by a few 2^-23 of the cap, so for caps up to kWideCap2 only.
-// - Else pa::tanh_f32, exact relative to the score.
-constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ void reshape_scores(uint32_t (&raw)[32], const float (&k)[2], float cap2) {
-    auto pair = [&](int w) { return make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])); };
-    auto put = [&](int w, float2 v) {
-        raw[2 * w] = __float_as_uint(v.x);
-        raw[2 * w + 1] = __float_as_uint(v.y);
-    };
-    if (cap2 == 0.f) {
+__device__ __forceinline__ float2 pair_of(const uint32_t (&raw)[32], int w) {
+    return make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1]));
+}
+__device__ __forceinline__ void put_pair(uint32_t (&raw)[32], int w, float2 v) {
+    raw[2 * w] = __float_as_uint(v.x);
+    raw[2 * w + 1] = __float_as_uint(v.y);
+}
+
+// A quarter's 32 products q.k, capped in place: cap2 tanh(x), x = q.k * k, in base-2 units.
+// k: the factors of the two blocks; largest: at least this lane's largest |x|.
+// tanh x = 1 - 2 / (1 + e^(2x)), an exponential a score and one reciprocal for four: r = 1 / (abcd)
+// gives 1 / a = r b cd and so on (2,048 rows under a window of 4,096, no other form taken: 218 us;
+// one for two 233, for each 255). Off by a few 2^-23 of the cap, so for caps up to kWideCap. |x| is
+// cut at 10, where tanh is 1 to 2^-28 and the product of four still finite.
+constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
+__device__ __forceinline__ void cap_scores(uint32_t (&raw)[32], const float (&k)[2], float cap2, float largest) {
+    if (__any_sync(kFull, largest > 10.f)) {
 #pragma unroll
-        for (int w = 0; w < 16; ++w) put(w, __fmul2_rn(pair(w), both(k[w >> 3])));
-        return;
+        for (int i = 0; i < 32; ++i) {
+            const float most = 10.f / fabsf(k[i >> 4]);
+            asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+r"(raw[i]) : "r"(__float_as_uint(most)), "r"(__float_as_uint(-most)));
+        }
     }
-    float most[2];
-    largest_of(raw, most);
-    const float largest = fmaxf(most[0] * fabsf(k[0]), most[1] * fabsf(k[1]));
-    if (cap2 <= kWideCap2 && !__any_sync(kFull, largest > 10.f)) {
 #pragma unroll
-        for (int w = 0; w < 16; w += 2) {
-            const float2 f = both(k[w >> 3] * 2.8853900817779268f);
-            float2 a = __fmul2_rn(pair(w), f), c = __fmul2_rn(pair(w + 1), f);
-            a = __fadd2_rn(make_float2(pa::fast_exp2(a.x), pa::fast_exp2(a.y)), both(1.f));
-            c = __fadd2_rn(make_float2(pa::fast_exp2(c.x), pa::fast_exp2(c.y)), both(1.f));
-            const float2 ac = __fmul2_rn(a, c);  // (a.x c.x, a.y c.y)
-            const float r = pa::fast_rcp(ac.x * ac.y);
-            const float2 rr = __fmul2_rn(make_float2(ac.y, ac.x), both(r));  // 1 / (a.x c.x), 1 / (a.y c.y)
-            put(w, __ffma2_rn(__fmul2_rn(rr, c), both(-2.f * cap2), both(cap2)));
-            put(w + 1, __ffma2_rn(__fmul2_rn(rr, a), both(-2.f * cap2), both(cap2)));
-        }
-    } else if (!__any_sync(kFull, largest >= pa::kTanhSmall)) {
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            const float2 x = __fmul2_rn(pair(w), both(k[w >> 3])), z = __fmul2_rn(x, x);
-            float2 q = both(pa::tanh_coef(4) * cap2);
-#pragma unroll
-            for (int i = 3; i >= 0; --i) q = __ffma2_rn(q, z, both(pa::tanh_coef(i) * cap2));
-            put(w, __fmul2_rn(x, __ffma2_rn(q, z, both(cap2))));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(cap2 * pa::tanh_f32(__uint_as_float(raw[i]) * k[i >> 4]));
+    for (int w = 0; w < 16; w += 2) {
+        const float2 f = both(k[w >> 3] * 2.8853900817779268f);
+        float2 a = __fmul2_rn(pair_of(raw, w), f), c = __fmul2_rn(pair_of(raw, w + 1), f);
+        a = __fadd2_rn(make_float2(pa::fast_exp2(a.x), pa::fast_exp2(a.y)), both(1.f));
+        c = __fadd2_rn(make_float2(pa::fast_exp2(c.x), pa::fast_exp2(c.y)), both(1.f));
+        const float2 ac = __fmul2_rn(a, c);  // (a.x c.x, a.y c.y)
+        const float r = pa::fast_rcp(ac.x * ac.y);
+        const float2 rr = __fmul2_rn(make_float2(ac.y, ac.x), both(r));  // 1 / (a.x c.x), 1 / (a.y c.y)
+        put_pair(raw, w, __ffma2_rn(__fmul2_rn(rr, c), both(-2.f * cap2), both(cap2)));
+        put_pair(raw, w + 1, __ffma2_rn(__fmul2_rn(rr, a), both(-2.f * cap2), both(cap2)));
     }
 }
 
@@ -897,7 +881,6 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         if constexpr (decltype(form)::value == kScores) {
                             e = __fadd2_rn(e, both(nm));
                         } else if constexpr (decltype(form)::value == kCapped) {
-                            if constexpr (EB == 1) e = __fmul2_rn(e, both(qk[b]));  // bf16: in the coefficients
                             const float2 z = __fmul2_rn(e, e);
                             float2 q = both(P.poly[3]);
 #pragma unroll
@@ -957,41 +940,55 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                 qe[b] = fmaf(-slope2, back[b], qe[b]);
                             }
                         }
-                        auto scores_of = [&]() {  // whatever raw's products make, the bias's `at` among it
-                            // keys hidden from the row may hold anything, and reshape_scores mixes four of them
+                        float largest = 0.f;
+                        auto scores_of = [&]() {  // of raw's products, the bias's `at` among them
+                            // keys hidden from the row may hold anything, and cap_scores mixes four of them
                             if constexpr (decltype(masked)::value) {
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
                                     if (!(visible & (1u << k))) raw[k] = 0u;
                             }
-                            reshape_scores(raw, qk, MOD == kBias ? 0.f : P.cap2);
+                            if constexpr (MOD == kCap) {
+                                cap_scores(raw, qk, P.cap2, largest);
+                            } else if (MOD == kBoth && P.cap2 <= kWideCap2) {
+                                cap_scores(raw, qk, P.cap2, largest_of(raw, qk));
+                            } else if (MOD == kBoth && !__any_sync(kFull, largest_of(raw, qk) >= pa::kTanhSmall)) {
+#pragma unroll
+                                for (int w = 0; w < 16; ++w) {  // the polynomial of pa::tanh_f32
+                                    const float2 x = __fmul2_rn(pair_of(raw, w), both(qk[w >> 3])), z = __fmul2_rn(x, x);
+                                    float2 q = both(pa::tanh_coef(4));
+#pragma unroll
+                                    for (int i = 3; i >= 0; --i) q = __ffma2_rn(q, z, both(pa::tanh_coef(i)));
+                                    put_pair(raw, w, __fmul2_rn(__fmul2_rn(x, both(P.cap2)), __ffma2_rn(q, z, both(1.f))));
+                                }
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    const float v = __uint_as_float(raw[k]) * qk[k >> 4];
+                                    raw[k] = __float_as_uint(MOD == kBoth ? P.cap2 * pa::tanh_f32(v) : v);
+                                }
+                            }
                             if constexpr (MOD >= kBias) {
-                                auto add_bias = [&](int w, float2 at, float by) {
-                                    const float2 v = __ffma2_rn(at, both(by), make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1])));
-                                    raw[2 * w] = __float_as_uint(v.x);
-                                    raw[2 * w + 1] = __float_as_uint(v.y);
-                                };
 #pragma unroll
-                                for (int w = 0; w < 16; ++w) add_bias(w, make_float2(2 * w & 15, (2 * w & 15) + 1), slope2);
-                                if constexpr (decltype(masked)::value) {
-                                    if (P.prefix) {  // a key after the row, at > back: its distance is at - back
-#pragma unroll
-                                        for (int w = 0; w < 16; ++w)
-                                            add_bias(w, make_float2(fmaxf((2 * w & 15) - back[w >> 3], 0.f), fmaxf((2 * w & 15) + 1 - back[w >> 3], 0.f)),
-                                                     -2.f * slope2);
-                                    }
+                                for (int w = 0; w < 16; ++w) {
+                                    const float at = 2 * w & 15, bk = back[w >> 3];
+                                    float2 v = __ffma2_rn(make_float2(at, at + 1.f), both(slope2), pair_of(raw, w));
+                                    if (decltype(masked)::value && P.prefix)  // a key after the row, at > bk: its distance is at - bk
+                                        v = __ffma2_rn(make_float2(fmaxf(at - bk, 0.f), fmaxf(at + 1.f - bk, 0.f)), both(-2.f * slope2), v);
+                                    put_pair(raw, w, v);
                                 }
                             }
                         };
                         // Products go straight into the exponent while that is one form for all of them: with a
-                        // cap, scores that the short polynomial covers (P.small: 0.6 of the cap; 2^-18.6 of the
+                        // cap, scores that a short polynomial covers (P.small: 0.6 of the cap; 2^-18.6 of the
                         // score, 2^-13.7 of a weight at a cap of 50, half of P's own rounding); with a bias,
-                        // where no key can come after the row.
-                        bool whole = MOD == kCap || (MOD == kBias && !(decltype(masked)::value && P.prefix));
+                        // where no key can come after the row. Not over E4M3 with a cap: loud blocks' scores are
+                        // often beyond it, and taking turns costs more than cap_scores alone (three prompts of
+                        // 1,000 to 1,600 rows, scores of a spread of 6: 250 us, 205; of a spread of 1: 158, 178).
+                        bool whole = (MOD == kCap && EB == 2) || (MOD == kBias && !(decltype(masked)::value && P.prefix));
                         if constexpr (MOD == kCap) {
-                            float most[2];
-                            largest_of(raw, most);
-                            whole = !__any_sync(kFull, !((EB == 1 ? fmaxf(most[0] * fabsf(qk[0]), most[1] * fabsf(qk[1])) : fmaxf(most[0], most[1])) <= P.small));
+                            largest = largest_of(raw, qk);
+                            if (EB == 2) whole = !__any_sync(kFull, !(largest <= P.small));
                         }
                         uint32_t ph[16];
                         float add, qs;
