@@ -1371,10 +1371,10 @@ int launch_partition_mma(const DecodeParams& P, int n_seqs, cudaStream_t stream)
 
 template <int EB, bool BSC, bool SINKS, bool MOD>
 int dispatch_group_mma(int G, const DecodeParams& P, int n_seqs, cudaStream_t stream) {
-    if constexpr (MOD && EB == 2)  // reshaped scores over a bf16 cache: groups of 8 only (see decode_impl)
-        return launch_partition_mma<8, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
     switch (G) {
-        case 1: return launch_partition_mma<1, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
+        case 1:
+            if constexpr (MOD && EB == 2) return PA_ERR_UNSUPPORTED;  // (never asked for, see decode_impl)
+            else return launch_partition_mma<1, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
         case 2: return launch_partition_mma<2, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
         case 4: return launch_partition_mma<4, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
         case 8: return launch_partition_mma<8, EB, BSC, SINKS, MOD>(P, n_seqs, stream);
@@ -1554,8 +1554,12 @@ int decode_impl(int eb, void* out, const void* q, const void* k_pool, const void
     // At head_dim 128, groups of 8 heads and every E4M3 cache run on the tensor
     // cores (the CUDA-core kernel is bound by its instructions there, not by
     // HBM), unless the pool has too many rows for a TMA coordinate;
-    // pa_decode_tc asks for the tensor-core kernel at every group size
-    const bool tensor = force_tc || (head_dim == 128 && tc_rows_ok && (G == 8 || eb == 1));
+    // pa_decode_tc asks for the tensor-core kernel at every group size. With reshaped scores,
+    // and partitions by mma_partition_tokens, it is the faster one from two heads a group on:
+    // 64 sequences of 128 .. 4,096 tokens, 8 KV heads, groups of 4: 83.8 us, 95.4 on the CUDA
+    // cores; of 2: 82.5, 84.0; of 1: 82.0, 80.9; 24 of 1,100, groups of 4: 22.0, 38.2; 1 of
+    // 16,384, 32 KV heads, groups of 1: 52.5, 45.0.
+    const bool tensor = force_tc || (head_dim == 128 && tc_rows_ok && (G == 8 || eb == 1 || (reshape && G >= 2)));
     // default partitions: on the CUDA-core kernel the size in [512, 1024]
     // whose grid fills its last wave of CTA slots best (wave_partition_tokens);
     // 1024 tokens on the tensor-core kernel, whose shorter blocks amortise a
