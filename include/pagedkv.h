@@ -840,13 +840,15 @@ int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t t
 /*
  * Compaction: shortens seq_id to n_tokens (0 .. its length), the kept tokens to be
  * moved by pa_compact_blocks, of which positions below first_moved stay in place
- * (keep[j] == j for j < first_moved; 0 if not known).
+ * (keep[j] == j for j < first_moved, in the list of every KV head; 0 if not known;
+ * n_tokens for a plain cut, which pa_compact_blocks need not follow).
  *  table_out  the table for that call: the sequence's blocks before it, where
  *             blocks that it will write and others share are replaced by fresh ones
  *  pairs_out  int64 [pair_cap][2]: the copies (old, fresh) to make first
  * Then the blocks behind the kept tokens are released, so that the copies and the
  * compaction have to be on the stream before anything that writes blocks handed out
- * later. pa_bm_cache_blocks registers no position from first_moved on afterwards.
+ * later. Where first_moved < n_tokens, pa_bm_cache_blocks registers no position from
+ * first_moved on afterwards.
  * PA_ERR_INVALID_ARG where a block that would be written, or appended to, was
  * released (pa_bm_release_*); PA_ERR_CAPACITY with both counts set, and PA_ERR_OOM:
  * nothing changed. With n_tokens the sequence's length nothing moves.

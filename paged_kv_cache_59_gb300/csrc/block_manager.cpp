@@ -301,7 +301,7 @@ int pa_bm_compact(pa_bm* bm, int64_t seq_id, int64_t n_tokens, int64_t first_mov
         if (s.table[j] >= 0) bm->put(s.table[j]);
     s.table.resize(keep);
     s.len = n_tokens;
-    if (first_moved < s.intact) s.intact = first_moved;
+    if (first_moved < n_tokens && first_moved < s.intact) s.intact = first_moved;  // (a plain cut moves nothing)
     return PA_OK;
 }
 

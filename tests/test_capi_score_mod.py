@@ -132,6 +132,14 @@ def test_compact_and_the_prefix_cache(capi):
     assert bm.cache_blocks(3, more) == 2              # positions from 40 on are no longer the prompt's
     bm.fork(3, 4)
     assert bm.cache_blocks(4, more) == 0
+    bm.free_seq(1), bm.free_seq(2), bm.free_seq(3)
+    bm.add_seq(5)
+    last = list(range(2000, 2100))
+    bm.append_tokens(5, 50)
+    bm.compact(5, 50)                                 # nothing moves, nor does a cut move anything
+    bm.compact(5, 40, 40)
+    bm.append_tokens(5, 60)
+    assert bm.cache_blocks(5, last) == 6
 
 
 def test_compact_refuses_released_destinations(capi):
