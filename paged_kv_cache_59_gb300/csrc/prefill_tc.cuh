@@ -83,14 +83,15 @@ constexpr uint32_t kTmemCols = 512;  // tile X: S at 256X, O at 256X + 128 (D co
 using PrefillParams = PaPrefillParams;
 
 // A sequence's prefix, at most its context; 0 without one.
-// KeyTiles: the key tiles that the rows of a query-tile pair attend to: the cache blocks
+__device__ __forceinline__ int prefix_of(const PrefillParams& P, int s, int ctx) {
+    return P.prefix ? min(P.prefix[s], ctx) : 0;
+}
+
+// The key tiles that the rows of a query-tile pair attend to: the cache blocks
 // that some row sees, in order - the n_sink leading ones that hold sinks, then
 // those from `first` on, the block of `lo`, the first position in the window of
 // the pair's first row (all blocks without a window) - eight a tile, so that a
 // tile may hold sinks and the window's beginning. n tiles.
-__device__ __forceinline__ int prefix_of(const PrefillParams& P, int s, int ctx) {
-    return P.prefix ? min(P.prefix[s], ctx) : 0;
-}
 struct KeyTiles {
     int lo, first, n_sink, n;
     __device__ __forceinline__ KeyTiles(const PrefillParams& P, int first_row_pos, int last_row_pos) {

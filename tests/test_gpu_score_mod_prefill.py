@@ -71,6 +71,19 @@ def test_scores(pk, kind, D, H, Hk, cap, alibi, splits):
 
 @pytest.mark.parametrize("kind", ["bf16", "block"])
 @pytest.mark.parametrize("D,H,Hk", SHAPES)
+@pytest.mark.parametrize("cap,alibi,window,sinks,prefix", [(30.0, False, -1, 0, None), (0.0, True, 130, 5, None),
+                                                            (10.0, True, -1, 0, [1, 17, 130, 300, 400, 10 ** 6, 0, 0]),
+                                                            (300.0, False, 60, 0, [0, 0, 64, 250, 513, 880, 0, 0])])
+def test_wide_tables_are_planned(pk, kind, D, H, Hk, cap, alibi, window, sinks, prefix):
+    """Tables that could hold long contexts: pairs are listed and cut by the plan
+    (short ones run as the grid gives them, in the other tests)."""
+    c = Cache(D + H, kind, CTX, Hk, D, window, sinks, CHUNK)
+    c.tables = np.pad(c.tables, ((0, 0), (0, 100)), constant_values=-1)
+    check(pk, c, H, D, CHUNK, cap, alibi, prefix, 0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "block"])
+@pytest.mark.parametrize("D,H,Hk", SHAPES)
 @pytest.mark.parametrize("window,sinks", [(0, 0), (0, 1), (5, 4), (127, 16), (128, 129), (100, 5), (400, 300), (5000, 4)])
 def test_under_windows_with_sinks(pk, kind, D, H, Hk, window, sinks):
     c = Cache(window + sinks + D + H, kind, CTX, Hk, D, window, sinks, CHUNK)
