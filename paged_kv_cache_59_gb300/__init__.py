@@ -339,8 +339,6 @@ def pa_decode_fp8_block(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, 
 
 
 def _head_slopes(alibi_slopes, n_heads: int, dev: int):
-    if alibi_slopes is None:
-        return None
     if alibi_slopes.numel() != n_heads:
         raise ValueError(f"alibi_slopes needs {n_heads} entries")
     return _at(alibi_slopes, "alibi_slopes", _Types.f32, dev)
@@ -358,8 +356,8 @@ def pa_decode_score_mod(out, q, k_pool, v_pool, block_tables, context_lens, scal
                                                            context_lens, q.shape[0])
     longest, window, n_sinks, partition_tokens = _ints(max_context_len, window, n_sinks, partition_tokens)
     _call("pa_decode_score_mod", dev, stream, *data, *tables, float(scale), float(softcap),
-          _head_slopes(alibi_slopes, sizes[0], dev), *sizes, longest, num_blocks, window, n_sinks, partition_tokens,
-          *_workspace(workspace, dev))
+          None if alibi_slopes is None else _head_slopes(alibi_slopes, sizes[0], dev), *sizes, longest, num_blocks, window,
+          n_sinks, partition_tokens, *_workspace(workspace, dev))
 
 
 def pa_decode_plan(context_lens, n_heads: int, n_kv_heads: int, head_dim: int, max_blocks_per_seq: int,
@@ -429,9 +427,12 @@ class _Types:
         torch = _torch()
         cls.bf16 = (torch.bfloat16, torch.int16, getattr(torch, "uint16", torch.int16))
         cls.e4m3 = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+        cls.movable = cls.bf16 + cls.e4m3
         cls.f32, cls.i32, cls.i64 = (torch.float32,), (torch.int32,), (torch.int64,)
-        cls.current_device = torch.cuda.current_device
+        # torch.cuda.current_device() checks each time whether CUDA is initialised, 0.2 us (a CUDA tensor is at hand);
         # torch.cuda.current_stream() takes 3 us to build its object; a small launch takes 2
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        cls.current_device = staticmethod(device or torch.cuda.current_device)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         cls.raw_stream = staticmethod(raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
         cls.ready = True
@@ -693,8 +694,8 @@ def pa_prefill_score_mod(out, q, k_pool, v_pool, block_tables, context_lens, q_s
         prefix = _at(prefix_lens, "prefix_lens", _Types.i32, dev)
     longest, window, n_sinks, splits = _ints(max_chunk_len, window, n_sinks, splits)
     _call("pa_prefill_score_mod", dev, stream, *data, *tables, _at(q_start_loc, "q_start_loc", _Types.i32, dev),
-          float(scale), float(softcap), _head_slopes(alibi_slopes, sizes[0], dev), prefix, *sizes, longest, num_blocks,
-          window, n_sinks, splits, *_workspace(workspace, dev))
+          float(scale), float(softcap), None if alibi_slopes is None else _head_slopes(alibi_slopes, sizes[0], dev), prefix,
+          *sizes, longest, num_blocks, window, n_sinks, splits, *_workspace(workspace, dev))
 
 
 def pa_compact_blocks(k_pool, v_pool, block_tables, keep, keep_start_loc, k_scale=None, v_scale=None, stream=None) -> None:
@@ -708,9 +709,11 @@ def pa_compact_blocks(k_pool, v_pool, block_tables, keep, keep_start_loc, k_scal
     T = _Types
     num_blocks, n_kv_heads, block_size, head_dim = pool_shape = k_pool.shape
     n_seqs, max_blocks = block_tables.shape
-    if v_pool.shape != pool_shape or v_pool.element_size() != k_pool.element_size():
+    bits = k_pool.element_size()
+    if v_pool.shape != pool_shape or v_pool.element_size() != bits:
         raise ValueError("k_pool and v_pool must have one shape and element size")
-    if keep.dim() not in (1, 2) or (keep.dim() == 2 and keep.shape[0] != n_kv_heads):
+    lists = keep.shape
+    if len(lists) != 1 and (len(lists) != 2 or lists[0] != n_kv_heads):
         raise ValueError("keep must be [n_kept] or [n_kv_heads][n_kept]")
     if keep_start_loc.numel() != n_seqs + 1:
         raise ValueError("keep_start_loc must have n_seqs + 1 entries")
@@ -722,11 +725,11 @@ def pa_compact_blocks(k_pool, v_pool, block_tables, keep, keep_start_loc, k_scal
         ks, vs = _at(k_scale, "k_scale", T.f32, dev), _at(v_scale, "v_scale", T.f32, dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale go together")
-    kinds = T.e4m3 if ks is not None else T.bf16 + T.e4m3
+    kinds = T.e4m3 if ks is not None else T.movable
     _call("pa_compact_blocks", dev, stream, _at(k_pool, "k_pool", kinds, dev), _at(v_pool, "v_pool", kinds, dev), ks, vs,
-          _at(block_tables, "block_tables", T.i32, dev), _at(keep, "keep", T.i32, dev) if keep.numel() else None,
-          _at(keep_start_loc, "keep_start_loc", T.i32, dev), n_kv_heads if keep.dim() == 2 else 1, keep.shape[-1],
-          n_kv_heads, head_dim, block_size, k_pool.element_size(), n_seqs, max_blocks, num_blocks)
+          _at(block_tables, "block_tables", T.i32, dev), _at(keep, "keep", T.i32, dev) if lists[-1] else None,
+          _at(keep_start_loc, "keep_start_loc", T.i32, dev), n_kv_heads if len(lists) == 2 else 1, lists[-1], n_kv_heads,
+          head_dim, block_size, bits, n_seqs, max_blocks, num_blocks)
 
 
 def pa_copy_blocks_fp8_block(k_pool, v_pool, k_scale, v_scale, block_mapping, stream=None) -> None:
