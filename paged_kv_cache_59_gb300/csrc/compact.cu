@@ -22,10 +22,12 @@
 //
 // Bound by HBM: every moved byte is read once and written once. 32 chats of 2,000 to
 // 8,192 tokens that keep a third, a list for each of 8 heads (128 dims, bf16): 72 us,
-// 5.5 TB/s, 0.81 of a copy. One document of 131,072 tokens that keeps 0.6: 124 us,
-// 5.2 TB/s (16 clusters of 8; whole rows in a CTA's own columns, each with all the
+// 5.5 TB/s, 0.81 of a copy. One document of 131,072 tokens that keeps 0.6: 109 us,
+// 5.9 TB/s (16 clusters of 12; a CTA for each slice of the rows' columns, each with all the
 // look-ups, took 302). 6 documents of 23,000 to 65,000 tokens in block-scaled E4M3: 84 us,
 // 5.4 TB/s. 100 chats, a list for all heads: 143 us, 6.3 TB/s.
+#include <algorithm>
+
 #include "pa_common.cuh"
 
 namespace {
@@ -339,13 +341,16 @@ extern "C" int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, flo
     P.num_blocks = num_blocks;
     P.err = err;
     // CTAs of a cluster: until there are two for each SM, as far as a sequence's tokens (on average) give each
-    // a step's share; up to 16 where 8 leave half of the SMs idle (4 sequences, one KV head: 43.5 and 27.0 us),
-    // as a larger cluster's barrier costs more (16 units of one document: 124 and 131 us).
+    // a step's share. Up to 8, and up to 16 where few clusters leave SMs idle, which moves as many bytes a
+    // second as an SM's share of HBM: 1.3 CTAs for each SM, as clusters of CTAs that share SMs with others
+    // hold all of theirs back. (One document's 16 units: 125 us with 8, 107 with 10, 109 with 12, 133 with 16; in
+    // E4M3 72, 61, 53, 72; 8 units of 4 sequences: 45 with 8, 33 with 12, 27 with 16.)
     const int chunks = P.row_bytes / 16, tokens = kThreads / chunks * kUnroll;
     const long long units = 2LL * n_kv_heads * n_seqs;
-    const int most = units * 8 <= sms / 2 ? 16 : 8;
+    const int most = (int)std::min(16LL, std::max(8LL, 13LL * sms / (10 * units)));
     int ctas = 1;
-    while (ctas < most && units * ctas < 2LL * sms && (long long)n_kept > (long long)n_seqs * ctas * tokens) ctas *= 2;
+    while (ctas < most && units * ctas < 2LL * sms && (long long)n_kept > (long long)n_seqs * ctas * tokens)
+        ctas = std::min(2 * ctas, most);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (k_scale) return chunks == 8 ? launch_compact<8, true>(P, ctas, n_seqs, st) : launch_compact<4, true>(P, ctas, n_seqs, st);
     switch (chunks) {

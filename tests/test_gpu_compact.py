@@ -112,6 +112,14 @@ def test_a_long_document(pk):
         check(pk, rng, kind, 1, 128, [40000], [13000], True, 5)
 
 
+def test_clusters_of_odd_sizes(pk):
+    """Few units of long lists: 9 to 16 CTAs take a step together."""
+    rng = np.random.default_rng(14)
+    for kind, Hk, D, ctx in (("bf16", 8, 128, [12000]), ("block", 8, 128, [12000]), ("bf16", 5, 64, [9000, 8000]),
+                             ("block", 3, 128, [9000, 100, 6000]), ("head", 7, 128, [15000])):
+        check(pk, rng, kind, Hk, D, ctx, [n * 9 // 10 for n in ctx], True)
+
+
 def test_scales_far_apart_and_out_of_range(pk):
     """Codes that vanish, subnormal ones, scales that are no powers of two, and ones
     that are read within [2^-32, 2^32]."""
