@@ -251,6 +251,31 @@ __device__ __forceinline__ float reshaped(const DecodeParams& P, float x, float 
     const float y = P.cap2 > 0.f ? P.cap2 * pa::tanh_f32(x) : x;
     return fmaf(-slope2, (float)dist, y);
 }
+// Four reshaped scores at once (of keys that the query sees; 0 for others, as the four share a
+// reciprocal): cap2 tanh x = cap2 - 2 cap2 / (1 + e^(2x)), with r = 1 / (abcd) giving 1 / a = r b cd
+// and so on (an exponent of 30 at most keeps the product finite; 1 - 2^-29 is 1 in fp32). Off by a few
+// 2^-23 of the cap, so for caps up to 128; 30 instructions where pa::tanh_f32 takes 90 (64 sequences
+// of 128 .. 4,096 tokens, 32/8 heads, E4M3, scores of a spread of 6: 51.9 us, 53.4 with that one).
+constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
+__device__ __forceinline__ void reshape4(const DecodeParams& P, float (&x)[4], const float (&slope2)[4], const int (&dist)[4]) {
+    if (P.cap2 > kWideCap2) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = P.cap2 * pa::tanh_f32(x[u]);
+    } else if (P.cap2 > 0.f) {
+        float a[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) a[u] = 1.f + pa::fast_exp2(pa::min_nan(x[u] * 2.8853900817779268f, 30.f));
+        const float ab = a[0] * a[1], cd = a[2] * a[3], r = pa::fast_rcp(ab * cd), rab = r * cd, rcd = r * ab;
+        x[0] = fmaf(-2.f * P.cap2, rab * a[1], P.cap2);
+        x[1] = fmaf(-2.f * P.cap2, rab * a[0], P.cap2);
+        x[2] = fmaf(-2.f * P.cap2, rcd * a[3], P.cap2);
+        x[3] = fmaf(-2.f * P.cap2, rcd * a[2], P.cap2);
+    }
+    if (P.slopes) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = fmaf(-slope2[u], (float)dist[u], x[u]);
+    }
+}
 __device__ __forceinline__ float slope_of(const DecodeParams& P, int head) {
     return P.slopes ? P.slopes[head] * 1.4426950408889634f : 0.f;
 }
@@ -946,17 +971,22 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
                 // fp16's range (the key at the maximum gets p = 1 exactly)
                 float sv[4], pv[4];
                 scales.take(i);
+                if constexpr (MOD) {
+                    const bool see[2] = {visible<SINKS>(tok0 + g, ctx, first_pos, P.n_sinks),
+                                         visible<SINKS>(tok0 + g + 8, ctx, first_pos, P.n_sinks)};
+                    const int back = ctx - 1 - tok0 - g;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int pos = tok0 + g + 8 * (u >> 1);
-                    float s2;
-                    if constexpr (MOD) {
-                        const float x = BSC ? scales.scaled(sT[u]) : sT[u] * sc;
-                        s2 = reshaped(P, x, slope2[u & 1], ctx - 1 - pos) + scales.shift();
-                    } else {
-                        s2 = BSC ? scales.score(sT[u]) : sT[u] * sc;
+                    for (int u = 0; u < 4; ++u) sv[u] = see[u >> 1] ? (BSC ? scales.scaled(sT[u]) : sT[u] * sc) : 0.f;
+                    reshape4(P, sv, {slope2[0], slope2[1], slope2[0], slope2[1]}, {back, back, back - 8, back - 8});
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) sv[u] = see[u >> 1] ? sv[u] + scales.shift() : -INFINITY;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int pos = tok0 + g + 8 * (u >> 1);
+                        const float s2 = BSC ? scales.score(sT[u]) : sT[u] * sc;
+                        sv[u] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
                     }
-                    sv[u] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
                 }
                 auto exps = [&]() {
 #pragma unroll
@@ -1002,15 +1032,20 @@ pa_decode_mma_kernel(const DecodeParams P, const __grid_constant__ CUtensorMap t
             } else {
                 // ---- online softmax of row g over the tile's 16 tokens (this lane: 2t, 2t+1, 8+2t, 9+2t)
                 float sv[4];
+                bool see[4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int pos = tok0 + 8 * n + 2 * t + k;
-                        float s2 = s_acc[n][k] * sc;
-                        if constexpr (MOD) s2 = reshaped(P, s2, slope2[0], ctx - 1 - pos);
-                        sv[2 * n + k] = visible<SINKS>(pos, ctx, first_pos, P.n_sinks) ? s2 : -INFINITY;
+                        see[2 * n + k] = visible<SINKS>(tok0 + 8 * n + 2 * t + k, ctx, first_pos, P.n_sinks);
+                        sv[2 * n + k] = see[2 * n + k] ? s_acc[n][k] * sc : MOD ? 0.f : -INFINITY;
                     }
+                if constexpr (MOD) {
+                    const int back = ctx - 1 - tok0 - 2 * t;
+                    reshape4(P, sv, {slope2[0], slope2[0], slope2[0], slope2[0]}, {back, back - 1, back - 8, back - 9});
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) sv[u] = see[u] ? sv[u] : -INFINITY;
+                }
                 float tmax = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
                 tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 1));
                 tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 2));

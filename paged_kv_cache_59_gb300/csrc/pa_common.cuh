@@ -245,6 +245,12 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return y;
 }
 
+__device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either is
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 // tanh for scores. Below kTanhSmall in magnitude x (1 + z P(z)), z = x^2, P the
 // polynomial of degree 4 whose largest relative error there is least (a linear program
 // over 6,000 points): 2^-20.3 with its coefficients and steps in fp32. Above,
