@@ -679,12 +679,11 @@ int pa_prefill_fp8_block(void* out, const void* q, const void* k_pool, const voi
  *  k_scale, v_scale  both NULL: bf16 pools; both given: E4M3 pools with a scale per
  *                (block, KV head), fp32 [num_blocks][n_kv_heads]. (A cache with
  *                scales per head serves as one whose blocks all have them.)
- * tanh is computed in fp32, within 2^-20 of itself, or for caps up to 128 within a few
- * 2^-23 of 1; the scores' other arithmetic, the
- * partitions, the workspace, a context beyond max_context_len and the errors are
- * those of pa_decode_sinks and pa_decode_fp8_block. Groups of 2 to 8 heads at
- * head_dim 128 run on the tensor-core kernel of pa_decode_tc (pools of at most 2^31 -
- * 16 rows).
+ * tanh is computed in fp32, within 2^-20 of itself, or for caps up to 128 within a
+ * few 2^-23 of 1; the scores' other arithmetic, the partitions, the workspace, a
+ * context beyond max_context_len and the errors are those of pa_decode_sinks and
+ * pa_decode_fp8_block. Groups of 2 to 8 heads at head_dim 128 run on the tensor-core
+ * kernel of pa_decode_tc (pools of at most 2^31 - 16 rows).
  */
 int pa_decode_score_mod(void* out, const void* q, const void* k_pool, const void* v_pool,
                         const float* k_scale, const float* v_scale, const int32_t* block_tables,
