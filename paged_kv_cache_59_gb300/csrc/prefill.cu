@@ -870,7 +870,7 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
     // gives them, one a CTA, without a plan (one prompt of 77 rows, 4 KV heads: 11.9 us with it, 8.8 without;
     // cutting a pair of 8 tiles in two saves as much as joining it costs).
     long long most_tiles = ((long long)max_blocks_per_seq + kBPT - 1) / kBPT;
-    if (window >= 0) most_tiles = std::min(most_tiles, ((long long)window + n_sinks + 2 * (kRows / G)) / kKT + 3);
+    if (window >= 0 && !prefix) most_tiles = std::min(most_tiles, ((long long)window + n_sinks + 2 * (kRows / G)) / kKT + 3);
     const bool direct = reshape && splits == 0 && n_items <= n_cta && most_tiles <= 8;
     if (splits == 0 && !direct) {
         const BalancedLayout bl = balanced_layout(n_items, n_cta);
@@ -889,10 +889,10 @@ int prefill_impl(void* out, const void* q, const void* k_pool, const void* v_poo
     Pp.reshape = reshape;
     Pp.cap2 = softcap * 1.4426950408889634f;
     // the coefficients of tanh(x) / x up to |x| = 0.6 (pa_common.cuh has the longer polynomial), of y = q.k, x = y c, as
-    // far as c^7 stays far from fp32's least
+    // far as c^7 stays far from fp32's least and largest
     const double c = (double)Pp.scale_log2, tanh3[4] = {1.0, -0.33319074, 0.13086419, -0.04138779};
     for (int i = 0; i < 4; ++i) Pp.poly[i] = (float)(Pp.cap2 * tanh3[i] * c * pow(c * c, i));
-    Pp.small = fabs(c) >= 0x1p-15 ? 0.6f : -1.f;
+    Pp.small = fabs(c) >= 0x1p-15 && fabs(c) <= 0x1p15 ? 0.6f : -1.f;
     Pp.slopes = slopes;
     Pp.prefix = prefix;
     // chunk rows bound for the merge grid (rows past the last chunk exit)

@@ -335,7 +335,7 @@ __device__ __forceinline__ void join_pieces(const PrefillParams& P, int slot, in
 // instructions of the others cost even where they are not taken (2,048 rows under a window of
 // 4,096, 32 heads: a bias 176 us in a kernel for all, 144 in its own): a cap alone, a bias by
 // distance or none (a prefix over plain scores), and both, or a cap above 128.
-enum { kPlain, kCap, kBias, kBoth };
+enum { kPlain, kCap, kBias, kCapBias };
 
 // The largest |q.k * k| of a quarter's products; k: the factors of its two blocks.
 __device__ __forceinline__ float largest_of(const uint32_t (&raw)[32], const float (&k)[2]) {
@@ -359,7 +359,7 @@ __device__ __forceinline__ void put_pair(uint32_t (&raw)[32], int w, float2 v) {
 // k: the factors of the two blocks; largest: at least this lane's largest |x|.
 // tanh x = 1 - 2 / (1 + e^(2x)), an exponential a score and one reciprocal for four: r = 1 / (abcd)
 // gives 1 / a = r b cd and so on (2,048 rows under a window of 4,096, no other form taken: 218 us;
-// one for two 233, for each 255). Off by a few 2^-23 of the cap, so for caps up to kWideCap. |x| is
+// one for two 233, for each 255). Off by a few 2^-23 of the cap, so for caps up to 128. |x| is
 // cut at 10, where tanh is 1 to 2^-28 and the product of four still finite.
 constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
 __device__ __forceinline__ void cap_scores(uint32_t (&raw)[32], const float (&k)[2], float cap2, float largest) {
@@ -953,9 +953,9 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             }
                             if constexpr (MOD == kCap) {
                                 cap_scores(raw, qk, P.cap2, largest);
-                            } else if (MOD == kBoth && P.cap2 <= kWideCap2) {
+                            } else if (MOD == kCapBias && P.cap2 <= kWideCap2) {
                                 cap_scores(raw, qk, P.cap2, largest_of(raw, qk));
-                            } else if (MOD == kBoth && !__any_sync(kFull, largest_of(raw, qk) >= pa::kTanhSmall)) {
+                            } else if (MOD == kCapBias && !__any_sync(kFull, largest_of(raw, qk) >= pa::kTanhSmall)) {
 #pragma unroll
                                 for (int w = 0; w < 16; ++w) {  // the polynomial of pa::tanh_f32
                                     const float2 x = __fmul2_rn(pair_of(raw, w), both(qk[w >> 3])), z = __fmul2_rn(x, x);
@@ -968,7 +968,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
                                     const float v = __uint_as_float(raw[k]) * qk[k >> 4];
-                                    raw[k] = __float_as_uint(MOD == kBoth ? P.cap2 * pa::tanh_f32(v) : v);
+                                    raw[k] = __float_as_uint(MOD == kCapBias ? P.cap2 * pa::tanh_f32(v) : v);
                                 }
                             }
                             if constexpr (MOD >= kBias) {
@@ -998,7 +998,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         constexpr int kForm = MOD == kCap ? kCapped : MOD == kBias ? kBiased : kProducts;
                         if constexpr (MOD == kPlain) {
                             qs = exps(masked, Form<kProducts>{}, raw, visible, ph, add);
-                        } else if (MOD != kBoth && whole) {
+                        } else if (MOD != kCapBias && whole) {
                             qs = exps(masked, Form<kForm>{}, raw, visible, ph, add);
                         } else {
                             scores_of();

@@ -161,6 +161,17 @@ def test_another_stream_and_a_captured_graph(pk):
     check_device_error(0)
 
 
+@pytest.mark.parametrize("scale,cap", [(1e8, 1.0), (1e-8, 100.0), (1e30, 50.0)])
+def test_scales_far_from_the_cap(pk, scale, cap):
+    """Scores of zero, whatever multiplies them: the mean of V."""
+    for kind, D, H in (("bf16", 128, 4), ("block", 128, 4), ("bf16", 64, 2), ("bf16", 128, 2)):
+        c = Cache(14, kind, [200], 2, D)
+        q = np.zeros((1, H, D), np.uint16)
+        ref = paged_decode(q, c.k, c.v, c.tables, c.ctx, 1.0, 0.0, None, -1, 0, c.k_scale, c.v_scale)
+        compare(run(pk, c, q, scale, cap), ref, q, c, [slice(0, 1)], D, 0.0, cap, 2.0 ** -11)
+    check_device_error(0)
+
+
 def test_refusals(pk):
     torch = torch_cuda()
     c = Cache(12, "block", [40], 2, 64)

@@ -192,6 +192,17 @@ def test_a_long_capped_window(pk):
         check(pk, c, 4, 128, [257], 30.0, window < 0)
 
 
+@pytest.mark.parametrize("scale,cap", [(1e8, 1.0), (1e-8, 100.0), (1e30, 50.0)])
+def test_scales_far_from_the_cap(pk, scale, cap):
+    """Scores of zero, whatever multiplies them: a row is the mean of V up to it."""
+    for kind, D in (("bf16", 128), ("block", 128), ("bf16", 64)):
+        c = Cache(14, kind, [200], 2, D, chunk=[150])
+        q = np.zeros((150, 4, D), np.uint16)
+        ref = paged_prefill(q, c.k, c.v, c.tables, c.ctx, start_loc([150]), 1.0, 0.0, None, None, -1, 0, c.k_scale, c.v_scale)
+        compare(run(pk, c, q, [150], scale, cap), ref, q, c, [slice(0, 150)], D, 0.0, cap, 2.0 ** -11, 2.0 ** -17 * 8)
+    check_device_error(0)
+
+
 def test_refusals(pk):
     torch = torch_cuda()
     c = Cache(12, "block", [40], 2, 64, chunk=[20])
