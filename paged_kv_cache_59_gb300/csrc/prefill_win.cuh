@@ -32,7 +32,7 @@
 // chunks whose cache comes from HBM.
 // Reshaped scores (MOD, pa_prefill_score_mod): the same kernel, each score capped by a tanh, biased by
 // its key's distance, or both, before the exponential, and prefixes that lift the causal limit. 2,048
-// rows, window 4,096, scores of a spread of 6: 182 us with a cap of 50, 152 with biases.
+// rows, window 4,096, scores of a spread of 6: 177 us with a cap of 50, 152 with biases.
 // 2,048 rows, window 4,096 + 4 sinks (256 items of 33 tiles on 152 SMs): 129.1 us on
 // one cache, 1,066 TFLOP/s of visible pairs, 132.6 over three in turn; 179 us with
 // whole waves, cut tails and a block-wide barrier between segments.
@@ -1221,13 +1221,18 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 // CTA c - 1 and c, its pieces or 0). Piece k of that item: slot 2 ca + 1 for
 // k = 0, else 2 (ca + k). Behind that table, 8 counters for each CTA (see
 // join_pieces), zeroed here.
+// Capped scores over a bf16 cache take 1.5 of a plain tile's time, and starting no more: two
+// of theirs (2,048 rows under a window of 4,096: 184 and 177 us; over E4M3, whose segments take
+// longer to start, three remain: 205, with two 211).
 constexpr int kStart = 3, kLeast = 3;
+constexpr int kStartCap = 2;
 template <int G>
 __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const PrefillParams P) {
     __shared__ long long wsum[32];
     __shared__ int wcnt[32], wmax[32];
     pa::launch_dependents();     // the prefill kernel may be scheduled
     pa::grid_dependency_wait();  // the lengths are written
+    const int start = P.cap2 > 0.f && !P.k_scale ? kStartCap : kStart;
     const int n = P.n_items, t = threadIdx.x, lane = t & 31, wid = t >> 5;
     const int per = (n + 1023) / 1024;
     const int b0 = (int)min((long long)n, (long long)t * per), b1 = min(n, b0 + per);
@@ -1240,7 +1245,7 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
     int cnt = 0, most = 0;
     for (int it = b0; it < b1; ++it) {
         const int nk = item_tiles<G>(P, it);
-        mine += nk > 0 ? nk + kStart : 0;
+        mine += nk > 0 ? nk + start : 0;
         cnt += nk > 0;
         most = max(most, nk);
     }
@@ -1280,8 +1285,8 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
     __syncthreads();
     const long long T = wsum[31];
     const int np = wcnt[31];
-    const bool whole = np <= P.n_cta && wmax[0] <= T / P.n_cta + 2 * kStart;
-    const long long C = max(1LL, min((long long)P.n_cta, T / (kStart + 4)));
+    const bool whole = np <= P.n_cta && wmax[0] <= T / P.n_cta + 2 * start;
+    const long long C = max(1LL, min((long long)P.n_cta, T / (start + 4)));
     long long off = incl - mine + (wid > 0 ? wsum[wid - 1] : 0);
     int r = icnt - cnt + (wid > 0 ? wcnt[wid - 1] : 0);
     for (int it = b0; it < b1; ++it) {
@@ -1291,12 +1296,12 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
             P.work[r] = make_int4(it, 0, nk, -1);
             cta[r] = make_int4(r, r + 1, -1, 0);
         } else {
-            // run c: costs [c T / C, (c + 1) T / C); the item's costs are [off, off + nk + kStart)
-            const int c0 = (int)(((off + 1) * C - 1) / T), c1 = (int)(((off + nk + kStart) * C - 1) / T);
+            // run c: costs [c T / C, (c + 1) T / C); the item's costs are [off, off + nk + start)
+            const int c0 = (int)(((off + 1) * C - 1) / T), c1 = (int)(((off + nk + start) * C - 1) / T);
             auto cut = [&](int c) {  // the item's tile at which run c begins
                 if (c <= c0) return 0;
                 if (c > c1) return nk;
-                const int x = (int)(c * T / C - off) - kStart;
+                const int x = (int)(c * T / C - off) - start;
                 return x < kLeast ? 0 : x > nk - kLeast ? nk : x;
             };
             int ca = c0, cb = c1;  // the CTAs that get tiles
@@ -1312,7 +1317,7 @@ __global__ void __launch_bounds__(1024) pa_prefill_plan_even_kernel(const Prefil
                 cta[c].w = cb - ca + 1;
             }
         }
-        off += nk + kStart;
+        off += nk + start;
         ++r;
     }
 }

@@ -219,3 +219,14 @@ def test_steps_never_read_what_an_earlier_one_wrote():
             assert np.array_equal(held[s], keep[part(s)])
             cells[part(s)] = -1 - held[s]
             scales[np.arange(part(s).start, part(s).stop) // 16] = -1
+
+
+def test_the_capped_prefill_s_work_list(monkeypatch):
+    """The plan's arithmetic with the start of a segment counted as kStartCap tiles."""
+    import re
+
+    import tests.test_prefill_win_protocol as m
+    monkeypatch.setattr(m, "K_START", int(re.search(r"constexpr int kStartCap = (\d+);", m.SRC).group(1)))
+    assert m.K_START == 2
+    m.test_work_list_covers_every_tile_once()
+    m.test_work_list_is_even()
