@@ -436,11 +436,11 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
     Segment g;
     bool ok = true;  // after a failed wait a role goes on without waiting, so that no other role is left alone
     int J0 = 0;      // tiles of the segments before
-    auto tile_of = [&](int j) {  // the segment's j-th tile
-        if constexpr (MOD == kPlain) return g.kt0 + j;
+    auto tile_of = [](const Segment& seg, int j) {  // a segment's j-th tile
+        if constexpr (MOD == kPlain) return seg.kt0 + j;
         constexpr int kEnd = (2 * QT + 2 * kKT - 2) / kKT;  // tiles that hold the rows' own positions, or one more
-        const int lead = MOD != kCap || g.n_kt <= kEnd ? 0 : kEnd;
-        return g.kt0 + g.n_kt - 1 - (j == 0 ? lead : j <= lead ? j - 1 : j);
+        const int lead = MOD != kCap || seg.n_kt <= kEnd ? 0 : kEnd;
+        return seg.kt0 + seg.n_kt - 1 - (j == 0 ? lead : j <= lead ? j - 1 : j);
     };
 
     if (warp == 9 || warp == 14) {
@@ -507,8 +507,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 }
             };
             for (int j = 0; ok && j < g.n_kt; ++j) {
-                load(first, tile_of(j));
-                if (kBoth && ok) load(second, tile_of(j));
+                load(first, tile_of(g, j));
+                if (kBoth && ok) load(second, tile_of(g, j));
             }
         }
         // Every issued copy lands before the CTA exits: normally the converters and the tensor
@@ -674,7 +674,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 // kernel's time.
                 const int w4 = warp - 10;
                 for (int j = 0; j < g.n_kt; ++j) {
-                    const int J = J0 + j, st = J % kVS, tile = tile_of(j);
+                    const int J = J0 + j, st = J % kVS, tile = tile_of(g, j);
                     ok = pa::mbar_wait(bars.v_full(st), (uint32_t)((J / kVS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
@@ -766,7 +766,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     arrive(bars.raw_free(x));
                 };
                 for (int j = 0; j < g.n_kt; ++j) {
-                    const int J = J0 + j, tile = tile_of(j), ks = J % kKS, vs = J % kVS;
+                    const int J = J0 + j, tile = tile_of(g, j), ks = J % kKS, vs = J % kVS;
                     ok = pa::mbar_wait(bars.k_full(0), (uint32_t)(J & 1), P.err, abort_flag);
                     if (ok && J >= kKS) ok = pa::mbar_wait(bars.k_free(ks), (uint32_t)(((J - kKS) / kKS) & 1), P.err, abort_flag);
                     ok = __all_sync(kFull, ok);
@@ -812,7 +812,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             // worked on.
             const int nblk = min((g.ctx + kBS - 1) / kBS, P.max_blocks);
             auto block_id = [&](int j) {
-                const int blk = j < g.n_kt ? keys.block(tile_of(j) * kBPT + (lane & (kBPT - 1))) : nblk;
+                const int blk = j < g.n_kt ? keys.block(tile_of(g, j) * kBPT + (lane & (kBPT - 1))) : nblk;
                 return blk < nblk ? P.tables[(size_t)g.s * P.max_blocks + blk] : -1;
             };
             auto scale_of = [&](const float* scales, int bid) {
@@ -848,7 +848,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                     vst = 0;
                     vph ^= 1;
                 }
-                const int jt = tile_of(j) - g.kt0;
+                const int jt = tile_of(g, j) - g.kt0;
                 const int kb = jt * kKT + (jt < j_win ? kb_sinks : kb_win);
                 // A row does not see keys beyond its position or, sinks apart, before its window. A warp
                 // takes the masking code only for a tile where that hides a key from one of its rows (a
@@ -939,7 +939,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                             if constexpr (EB == 2) qe[1] = qe[0];
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
-                                back[b] = (float)(pos - keys.position(tile_of(j), 32 * qd + kBS * b));
+                                back[b] = (float)(pos - keys.position(tile_of(g, j), 32 * qd + kBS * b));
                                 qe[b] = fmaf(-slope2, back[b], qe[b]);
                             }
                         }
