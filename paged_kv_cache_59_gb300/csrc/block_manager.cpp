@@ -290,12 +290,14 @@ int pa_bm_compact(pa_bm* bm, int64_t seq_id, int64_t n_tokens, int64_t first_mov
         const int32_t b = s.table[j];
         if (bm->ref[b] <= 1) continue;
         const int32_t fresh = bm->alloc();
-        bm->put(b);
         s.table[j] = fresh;
         pairs_out[2 * pairs] = b;
         pairs_out[2 * pairs + 1] = fresh;
         ++pairs;
     }
+    // The copied blocks are let go of when all the fresh ones are taken: one that only the prefix cache
+    // holds then could be evicted for the next, and be a copy's source and another's destination.
+    for (int i = 0; i < pairs; ++i) bm->put((int32_t)pairs_out[2 * i]);
     std::copy(s.table.begin(), s.table.end(), table_out);
     for (int64_t j = keep; j < (int64_t)s.table.size(); ++j)
         if (s.table[j] >= 0) bm->put(s.table[j]);
