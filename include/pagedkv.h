@@ -847,7 +847,8 @@ int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t t
  *  pairs_out  int64 [pair_cap][2]: the copies (old, fresh) to make first
  * Then the blocks behind the kept tokens are released, so that the copies and the
  * compaction have to be on the stream before anything that writes blocks handed out
- * later. Where first_moved < n_tokens, pa_bm_cache_blocks registers no position from
+ * later, the copies of the next pa_bm_compact among them: sequences that one
+ * pa_compact_blocks moves together come from one pa_bm_compact_batch. Where first_moved < n_tokens, pa_bm_cache_blocks registers no position from
  * first_moved on afterwards.
  * PA_ERR_INVALID_ARG where a block that would be written, or appended to, was
  * released (pa_bm_release_*); PA_ERR_CAPACITY with both counts set, and PA_ERR_OOM:
@@ -855,6 +856,19 @@ int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t t
  */
 int pa_bm_compact(pa_bm* bm, int64_t seq_id, int64_t n_tokens, int64_t first_moved, int64_t* pairs_out,
                   int pair_cap, int* n_pairs_out, int32_t* table_out, int table_cap, int* n_table_out);
+
+/*
+ * The same for sequences that one pa_copy_blocks and one pa_compact_blocks serve:
+ * no copy writes a block that another sequence of the batch still reads, and no
+ * sequence moves tokens within one that another one's table holds (forks of one
+ * parent, or a cached prompt's). first_moved NULL: not known for any.
+ *  tables_out    int32 [n][max_blocks], -1 behind a sequence's blocks
+ *  n_blocks_out  the longest table's blocks
+ * PA_ERR_INVALID_ARG also where a sequence is named twice; all or nothing.
+ */
+int pa_bm_compact_batch(pa_bm* bm, const int64_t* seq_ids, const int64_t* n_tokens, const int64_t* first_moved, int n,
+                        int64_t* pairs_out, int pair_cap, int* n_pairs_out, int32_t* tables_out, int max_blocks,
+                        int* n_blocks_out);
 
 /*
  * Preemption by swapping ([MA] 9.1 "Batching and the scheduler": a preempted

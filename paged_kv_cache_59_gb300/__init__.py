@@ -704,7 +704,7 @@ def pa_compact_blocks(k_pool, v_pool, block_tables, keep, keep_start_loc, k_scal
     keep: int32 [n_kept], ascending in each sequence, or [n_kv_heads][n_kept];
     keep_start_loc: int32 [n_seqs + 1]. bf16 or E4M3 pools; k_scale and v_scale
     (fp32 [num_blocks][n_kv_heads]) when E4M3 pools have a scale per block and
-    head. BlockManager.compact gives the tables and frees the blocks."""
+    head. BlockManager.compact_batch gives the tables and frees the blocks."""
     dev = _device(k_pool, "k_pool")
     T = _Types
     num_blocks, n_kv_heads, block_size, head_dim = pool_shape = k_pool.shape
@@ -858,7 +858,9 @@ class BlockManager:
         block table that call needs (the old one, with shared blocks that it
         writes replaced by private ones) and the copy pairs of those blocks
         (pa_copy_blocks first). Positions below first_moved stay where they are;
-        the blocks behind the kept tokens are released."""
+        the blocks behind the kept tokens are released: launch the copies and the
+        compaction before anything that writes blocks handed out later, the next
+        compact's copies among them (compact_batch: several sequences at once)."""
         n_pairs, n_table = C.c_int(0), C.c_int(0)
         st = self._lib.pa_bm_compact(self._h, seq_id, n_tokens, first_moved, None, 0, C.byref(n_pairs), None, 0,
                                      C.byref(n_table))
@@ -871,6 +873,32 @@ class BlockManager:
         check("pa_bm_compact", self._lib.pa_bm_compact(self._h, seq_id, n_tokens, first_moved, pairs, n_pairs.value,
                                                        C.byref(n_pairs), table, n_table.value, C.byref(n_table)))
         return list(table)[:n_table.value], [(pairs[2 * i], pairs[2 * i + 1]) for i in range(n_pairs.value)]
+
+    def compact_batch(self, seq_ids: Sequence[int], n_tokens: Sequence[int], first_moved: Optional[Sequence[int]] = None):
+        """compact for sequences that one pa_compact_blocks moves together: (tables
+        int32 [n][longest] as a numpy array, -1 behind a sequence's blocks, and the
+        copy pairs of all of them, for one pa_copy_blocks)."""
+        import numpy as np
+        n = len(seq_ids)
+        if len(n_tokens) != n or (first_moved is not None and len(first_moved) != n):
+            raise ValueError("seq_ids, n_tokens and first_moved must have one length")
+        p64 = C.POINTER(C.c_int64)
+        ids, lens, firsts = (np.array(x, dtype=np.int64) for x in (seq_ids, n_tokens, [0] * n if first_moved is None else first_moved))
+        n_pairs, n_blocks = C.c_int(0), C.c_int(0)
+
+        def call(pairs, tables):
+            return self._lib.pa_bm_compact_batch(
+                self._h, ids.ctypes.data_as(p64), lens.ctypes.data_as(p64), firsts.ctypes.data_as(p64), n,
+                pairs.ctypes.data_as(p64), len(pairs), C.byref(n_pairs), tables.ctypes.data_as(C.POINTER(C.c_int32)),
+                tables.shape[1], C.byref(n_blocks))
+
+        pairs, tables = np.empty((0, 2), np.int64), np.empty((n, 0), np.int32)
+        st = call(pairs, tables)
+        if st == _capi.PA_ERR_CAPACITY:
+            pairs, tables = np.empty((n_pairs.value, 2), np.int64), np.empty((n, n_blocks.value), np.int32)
+            st = call(pairs, tables)
+        check("pa_bm_compact_batch", st)
+        return tables, [(int(a), int(b)) for a, b in pairs]
 
     def block_table(self, seq_id: int) -> List[int]:
         n = C.c_int(0)

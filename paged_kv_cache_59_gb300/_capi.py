@@ -98,6 +98,8 @@ SIGNATURES = {
     "pa_bm_release_before": (i32, [vp, i64, i64, C.POINTER(C.c_int)]),
     "pa_bm_release_between": (i32, [vp, i64, i64, i64, C.POINTER(C.c_int)]),
     "pa_bm_compact": (i32, [vp, i64, i64, i64, p_i64, i32, C.POINTER(C.c_int), p_i32, i32, C.POINTER(C.c_int)]),
+    "pa_bm_compact_batch": (i32, [vp, p_i64, p_i64, p_i64, i32, p_i64, i32, C.POINTER(C.c_int), p_i32, i32,
+                                  C.POINTER(C.c_int)]),
     "pa_bm_swap_out": (i32, [vp, i64, p_i32, i32, C.POINTER(C.c_int)]),
     "pa_bm_swap_in": (i32, [vp, i64, p_i32, i32, C.POINTER(C.c_int)]),
     "pa_bm_cache_blocks": (i32, [vp, i64, p_i32, i64, C.POINTER(C.c_int)]),

@@ -39,6 +39,7 @@
 #include <list>
 #include <new>
 #include <unordered_map>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/pagedkv.h"
@@ -124,6 +125,55 @@ struct pa_bm {
         return b;
     }
 };
+
+namespace {
+
+// One sequence's compaction: planned, then its copies, then, when all sequences of a call
+// have theirs, its table and the blocks it lets go of.
+struct Compaction {
+    pa_bm::Seq* seq = nullptr;
+    int64_t len = 0, first = 0, from = 0, keep = 0;  // blocks [from, keep) are written, later ones released
+    int pairs = 0;                                   // of those, blocks that others share
+
+    bool plan(pa_bm* bm, pa_bm::Seq* s, int64_t n_tokens, int64_t first_moved) {
+        if (s->swapped >= 0 || n_tokens < 0 || n_tokens > s->len || first_moved < 0 || first_moved > n_tokens) return false;
+        const int64_t bs = bm->block_size;
+        if (n_tokens == s->len) first_moved = n_tokens;  // nothing moves
+        seq = s;
+        len = n_tokens;
+        first = first_moved;
+        keep = (n_tokens + bs - 1) / bs;
+        from = first_moved < n_tokens ? first_moved / bs : keep;
+        for (int64_t j = from; j < keep; ++j) {
+            if (s->table[j] < 0) return false;  // released: there is no block to move into
+            pairs += bm->ref[s->table[j]] > 1;
+        }
+        return n_tokens % bs == 0 || s->table[keep - 1] >= 0;  // nor one to append to
+    }
+    // A block that only others' copies have been taken of (take_copies drops no reference) is shared still.
+    void take_copies(pa_bm* bm, int64_t* out) {
+        for (int64_t j = from; j < keep; ++j) {
+            const int32_t b = seq->table[j];
+            if (bm->ref[b] <= 1) continue;
+            seq->table[j] = bm->alloc();
+            *out++ = b;
+            *out++ = seq->table[j];
+        }
+    }
+    // The copied blocks are let go of when all the fresh ones are taken: one that only the prefix cache
+    // holds then could be evicted for the next, and be a copy's source and another's destination.
+    void finish(pa_bm* bm, const int64_t* copies, int32_t* table_out) {
+        for (int i = 0; i < pairs; ++i) bm->put((int32_t)copies[2 * i]);
+        std::copy(seq->table.begin(), seq->table.end(), table_out);
+        for (int64_t j = keep; j < (int64_t)seq->table.size(); ++j)
+            if (seq->table[j] >= 0) bm->put(seq->table[j]);
+        seq->table.resize(keep);
+        seq->len = len;
+        if (first < len && first < seq->intact) seq->intact = first;  // (a plain cut moves nothing)
+    }
+};
+
+}  // namespace
 
 extern "C" {
 
@@ -270,40 +320,57 @@ int pa_bm_compact(pa_bm* bm, int64_t seq_id, int64_t n_tokens, int64_t first_mov
         return PA_ERR_INVALID_ARG;
     auto it = bm->seqs.find(seq_id);
     if (it == bm->seqs.end()) return PA_ERR_REFCOUNT;
-    pa_bm::Seq& s = it->second;
-    if (s.swapped >= 0 || n_tokens < 0 || n_tokens > s.len || first_moved < 0 || first_moved > n_tokens) return PA_ERR_INVALID_ARG;
-    const int64_t bs = bm->block_size, keep = (n_tokens + bs - 1) / bs;  // blocks that stay
-    if (n_tokens == s.len) first_moved = n_tokens;                       // nothing moves
-    const int64_t from = first_moved < n_tokens ? first_moved / bs : keep;  // blocks from here to `keep` are written
-    int pairs = 0;
-    for (int64_t j = from; j < keep; ++j) {
-        if (s.table[j] < 0) return PA_ERR_INVALID_ARG;  // released: there is no block to move into
-        pairs += bm->ref[s.table[j]] > 1;
+    Compaction c;
+    if (!c.plan(bm, &it->second, n_tokens, first_moved)) return PA_ERR_INVALID_ARG;
+    *n_pairs_out = c.pairs;
+    *n_table_out = (int)it->second.table.size();
+    if (c.pairs > pair_cap || *n_table_out > table_cap) return PA_ERR_CAPACITY;  // nothing changed
+    if (c.pairs > bm->available()) return PA_ERR_OOM;
+    c.take_copies(bm, pairs_out);
+    c.finish(bm, pairs_out, table_out);
+    return PA_OK;
+}
+
+int pa_bm_compact_batch(pa_bm* bm, const int64_t* seq_ids, const int64_t* n_tokens, const int64_t* first_moved, int n,
+                        int64_t* pairs_out, int pair_cap, int* n_pairs_out, int32_t* tables_out, int max_blocks,
+                        int* n_blocks_out) {
+    if (!bm || n < 0 || (n > 0 && (!seq_ids || !n_tokens)) || !n_pairs_out || !n_blocks_out || pair_cap < 0 ||
+        max_blocks < 0 || (pair_cap > 0 && !pairs_out) || (n > 0 && max_blocks > 0 && !tables_out))
+        return PA_ERR_INVALID_ARG;
+    try {
+        std::vector<Compaction> all(n);
+        std::unordered_set<int64_t> once;
+        int64_t pairs = 0, widest = 0;
+        for (int i = 0; i < n; ++i) {
+            auto it = bm->seqs.find(seq_ids[i]);
+            if (it == bm->seqs.end()) return PA_ERR_REFCOUNT;
+            if (!once.insert(seq_ids[i]).second) return PA_ERR_INVALID_ARG;
+            if (!all[i].plan(bm, &it->second, n_tokens[i], first_moved ? first_moved[i] : 0)) return PA_ERR_INVALID_ARG;
+            pairs += all[i].pairs;
+            widest = std::max(widest, (int64_t)it->second.table.size());
+        }
+        if (pairs > INT32_MAX) return PA_ERR_INVALID_ARG;
+        *n_pairs_out = (int)pairs;
+        *n_blocks_out = (int)widest;
+        if (pairs > pair_cap || widest > max_blocks) return PA_ERR_CAPACITY;  // nothing changed
+        if (pairs > bm->available()) return PA_ERR_OOM;
+        // References as they are before the batch decide what is copied, and blocks come free after all copies
+        // have theirs: no sequence is given, or writes in place, what another one's table of the same call holds.
+        int64_t* at = pairs_out;
+        for (Compaction& c : all) {
+            c.take_copies(bm, at);
+            at += 2 * c.pairs;
+        }
+        at = pairs_out;
+        for (int i = 0; i < n; ++i) {
+            int32_t* row = tables_out + (size_t)i * max_blocks;
+            std::fill(row + all[i].seq->table.size(), row + max_blocks, -1);
+            all[i].finish(bm, at, row);
+            at += 2 * all[i].pairs;
+        }
+    } catch (...) {  // (the allocations above the first change)
+        return PA_ERR_OOM;
     }
-    if (n_tokens % bs != 0 && s.table[keep - 1] < 0) return PA_ERR_INVALID_ARG;  // nor one to append to
-    *n_pairs_out = pairs;
-    *n_table_out = (int)s.table.size();
-    if (pairs > pair_cap || (int)s.table.size() > table_cap) return PA_ERR_CAPACITY;  // nothing changed
-    if (pairs > bm->available()) return PA_ERR_OOM;
-    pairs = 0;
-    for (int64_t j = from; j < keep; ++j) {
-        const int32_t b = s.table[j];
-        if (bm->ref[b] <= 1) continue;
-        const int32_t fresh = bm->alloc();
-        s.table[j] = fresh;
-        pairs_out[2 * pairs] = b;
-        pairs_out[2 * pairs + 1] = fresh;
-        ++pairs;
-    }
-    // The copied blocks are let go of when all the fresh ones are taken: one that only the prefix cache
-    // holds then could be evicted for the next, and be a copy's source and another's destination.
-    for (int i = 0; i < pairs; ++i) bm->put((int32_t)pairs_out[2 * i]);
-    std::copy(s.table.begin(), s.table.end(), table_out);
-    for (int64_t j = keep; j < (int64_t)s.table.size(); ++j)
-        if (s.table[j] >= 0) bm->put(s.table[j]);
-    s.table.resize(keep);
-    s.len = n_tokens;
-    if (first_moved < n_tokens && first_moved < s.intact) s.intact = first_moved;  // (a plain cut moves nothing)
     return PA_OK;
 }
 

@@ -79,7 +79,7 @@ def test_a_copied_block_is_not_handed_out_as_a_destination(capi):
 @pytest.mark.parametrize("seed", range(6))
 def test_random_servers_short_of_blocks(capi, seed):
     from paged_kv_cache_59_gb300 import PagedKVError
-    rng, several, moved = random.Random(seed), 0, 0
+    rng, several, moved, batches = random.Random(seed), 0, 0, 0
     for _ in range(150):
         s = Server(rng.randint(6, 14))
         prompts = [[rng.randrange(1000) for _ in range(BS * 5)] for _ in range(2)]
@@ -106,6 +106,16 @@ def test_random_servers_short_of_blocks(capi, seed):
                     seq = rng.choice(live)
                     s.bm.free_seq(seq)
                     del s.want[seq]
+                elif what < 0.82:
+                    some = rng.sample(live, rng.randint(1, len(live)))
+                    keeps = [sorted(rng.sample(range(len(s.want[q])), rng.randint(0, len(s.want[q])))) for q in some]
+                    firsts = [next((j for j, k in enumerate(keep) if j != k), len(keep)) for keep in keeps]
+                    tables, pairs = s.bm.compact_batch(some, [len(k) for k in keeps], rng.choice([None, firsts]))
+                    s.copy(pairs)
+                    s.move(tables.tolist(), keeps)
+                    batches += len(some) > 1 and len(pairs) > 1
+                    for seq, keep in zip(some, keeps):
+                        s.want[seq] = [s.want[seq][k] for k in keep]
                 else:
                     seq = rng.choice(live)
                     n = len(s.want[seq])
@@ -120,4 +130,72 @@ def test_random_servers_short_of_blocks(capi, seed):
             except PagedKVError as e:
                 assert "out of KV blocks" in str(e), e
             s.check()
-    assert moved > 1000 and several > 100
+    assert moved > 500 and several > 20 and batches > 20
+
+
+def compact_together(s, keeps):
+    tables, pairs = s.bm.compact_batch(list(keeps), [len(k) for k in keeps.values()])
+    s.copy(pairs)
+    s.move(tables.tolist(), list(keeps.values()))
+    for seq, keep in keeps.items():
+        s.want[seq] = [s.want[seq][k] for k in keep]
+    s.check()
+    return tables, pairs
+
+
+def test_a_batch_copies_into_no_block_that_it_reads(capi):
+    """One sequence's released tail is free when the next one's copies are asked for. With
+    nothing else free the batch is refused, and nothing has changed."""
+    from paged_kv_cache_59_gb300 import PagedKVError
+    for spare in (0, 2):
+        s = Server(7 + spare)
+        for seq, n in ((1, 80), (2, 32)):
+            s.bm.add_seq(seq)
+            s.write(seq, n)
+        s.bm.fork(2, 3)
+        s.want[3] = list(s.want[2])
+        keeps = {1: list(range(60, 80)), 3: list(range(3, 31))}
+        if spare:
+            tables, pairs = compact_together(s, keeps)
+            assert len(pairs) == 2 and s.bm.num_free() == 3
+            assert not {b for _, b in pairs} & set(tables[0].tolist())
+            assert tables[1].tolist()[2:] == [-1] * 3
+        else:
+            before = [s.bm.block_table(q) for q in (1, 2, 3)]
+            with pytest.raises(PagedKVError):
+                compact_together(s, keeps)
+            assert before == [s.bm.block_table(q) for q in (1, 2, 3)] and s.bm.num_free() == 0
+            s.check()
+
+
+def test_forks_of_one_parent_in_a_batch(capi):
+    """The first keeps one block, the second three: what the second moves in place would be
+    read by the first, were it not copied."""
+    s = Server(20)
+    s.bm.add_seq(1)
+    s.write(1, 64)
+    s.bm.fork(1, 2)
+    s.want[2] = list(s.want[1])
+    keeps = {1: list(range(33, 49)), 2: list(range(10, 50))}
+    _, pairs = compact_together(s, keeps)
+    assert len(pairs) == 4
+
+
+def test_batches_that_are_refused(capi):
+    from paged_kv_cache_59_gb300 import PagedKVError
+    s = Server(8)
+    for seq in (1, 2):
+        s.bm.add_seq(seq)
+        s.write(seq, 40)
+    assert s.bm.compact_batch([], [])[1] == []
+    for ids, lens, firsts in (([1, 1], [10, 10], None), ([1, 9], [10, 10], None), ([1, 2], [10, 41], None),
+                              ([1, 2], [10, 10], [0, 11]), ([2], [-1], None)):
+        with pytest.raises(PagedKVError):
+            s.bm.compact_batch(ids, lens, firsts)
+    for ids, lens, firsts in (([1], [1, 2], None), ([1], [1], [0, 0])):
+        with pytest.raises(ValueError):
+            s.bm.compact_batch(ids, lens, firsts)
+    s.check()
+    tables, pairs = s.bm.compact_batch([1, 2], [40, 0])
+    assert pairs == [] and tables.shape == (2, 3)
+    assert s.bm.seq_len(1) == 40 and s.bm.seq_len(2) == 0 and s.bm.num_free() == 5
