@@ -251,11 +251,13 @@ __device__ __forceinline__ float reshaped(const DecodeParams& P, float x, float 
     const float y = P.cap2 > 0.f ? P.cap2 * pa::tanh_f32(x) : x;
     return fmaf(-slope2, (float)dist, y);
 }
-// Four reshaped scores at once (of keys that the query sees; 0 for others, as the four share a
-// reciprocal): cap2 tanh x = cap2 - 2 cap2 / (1 + e^(2x)), with r = 1 / (abcd) giving 1 / a = r b cd
-// and so on (an exponent of 30 at most keeps the product finite; 1 - 2^-29 is 1 in fp32). Off by a few
-// 2^-23 of the cap, so for caps up to 128; 30 instructions where pa::tanh_f32 takes 90 (64 sequences
-// of 128 .. 4,096 tokens, 32/8 heads, E4M3, scores of a spread of 6: 51.9 us, 53.4 with that one).
+// Four reshaped scores at once (of keys that the query sees; 0 for others, as scores share a
+// reciprocal): cap2 tanh x = cap2 - 2 cap2 / (1 + e^(2x)), a reciprocal r = 1 / (ab) for two scores
+// of one head, [0] and [2], [1] and [3] (1 / a = r b; heads that shared one would share a NaN, too). An
+// exponent of 30 at most keeps the product finite; 1 - 2^-29 is 1 in fp32. Off by a few 2^-23 of the
+// cap, so for caps up to 128; 28 instructions where pa::tanh_f32 takes 90 (64 sequences of 128 .. 4,096
+// tokens, 32/8 heads, E4M3, scores of a spread of 6: 52.4 us, 1.5 more with that one; one reciprocal
+// for all four takes as long).
 constexpr float kWideCap2 = 128.f * 1.4426950408889634f;
 __device__ __forceinline__ void reshape4(const DecodeParams& P, float (&x)[4], const float (&slope2)[4], const int (&dist)[4]) {
     if (P.cap2 > kWideCap2) {
@@ -265,11 +267,12 @@ __device__ __forceinline__ void reshape4(const DecodeParams& P, float (&x)[4], c
         float a[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) a[u] = 1.f + pa::fast_exp2(pa::min_nan(x[u] * 2.8853900817779268f, 30.f));
-        const float ab = a[0] * a[1], cd = a[2] * a[3], r = pa::fast_rcp(ab * cd), rab = r * cd, rcd = r * ab;
-        x[0] = fmaf(-2.f * P.cap2, rab * a[1], P.cap2);
-        x[1] = fmaf(-2.f * P.cap2, rab * a[0], P.cap2);
-        x[2] = fmaf(-2.f * P.cap2, rcd * a[3], P.cap2);
-        x[3] = fmaf(-2.f * P.cap2, rcd * a[2], P.cap2);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float r = pa::fast_rcp(a[u] * a[u + 2]);
+            x[u] = fmaf(-2.f * P.cap2, r * a[u + 2], P.cap2);
+            x[u + 2] = fmaf(-2.f * P.cap2, r * a[u], P.cap2);
+        }
     }
     if (P.slopes) {
 #pragma unroll
