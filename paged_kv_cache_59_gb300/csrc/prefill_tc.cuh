@@ -82,9 +82,9 @@ constexpr uint32_t kTmemCols = 512;  // tile X: S at 256X, O at 256X + 128 (D co
 
 using PrefillParams = PaPrefillParams;
 
-// A sequence's prefix, at most its context; 0 without one.
+// A sequence's prefix, at most its context; 0 without one (an entry below 0 is none).
 __device__ __forceinline__ int prefix_of(const PrefillParams& P, int s, int ctx) {
-    return P.prefix ? min(P.prefix[s], ctx) : 0;
+    return P.prefix ? max(0, min(P.prefix[s], ctx)) : 0;
 }
 
 // The key tiles that the rows of a query-tile pair attend to: the cache blocks
