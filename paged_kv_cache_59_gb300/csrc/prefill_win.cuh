@@ -856,7 +856,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                 // Key k of a quarter is bit k of the quarter's mask: two instructions an element (as
                 // three comparisons, a masked tile took twice a plain one's time).
                 const int lim0 = limit - kb;  // keys k > lim0 of the tile are not visible
-                const int lim1 = P.window >= 0 ? pos - kb - P.window : 0, sink1 = P.n_sinks - kb_sinks - jt * kKT;  // nor k < lim1, k >= sink1
+                // (A prefix may end any distance behind a row, so that the window's beginning comes first.)
+                const int lim1 = P.window >= 0 ? (MOD ? max(pos - P.window, 0) - kb : pos - kb - P.window) : 0, sink1 = P.n_sinks - kb_sinks - jt * kKT;  // nor k < lim1, k >= sink1
                 // (With a bias also for one with a key after a row's own position, which a prefix may show.)
                 const bool mask_warp = __any_sync(kFull, (MOD >= kBias && P.slopes ? pos - kb : lim0) < kKT - 1 || (lim1 > 0 && sink1 < kKT));
                 auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };  // bits 0 .. n-1
