@@ -746,10 +746,11 @@ int pa_prefill_score_mod(void* out, const void* q, const void* k_pool, const voi
  *                  no power of two: then off by at most half a step). Both NULL
  *                  otherwise: the elements are moved as they are
  * A position that is out of order or beyond the table sets PA_DEVERR_POSITION, one
- * in a block outside the pool PA_DEVERR_BLOCK_ID: that token is skipped, its new
- * position keeps its bytes. (Where a list is out of order, which of its other tokens
- * arrive is undefined.) keep_start_loc outside [0, n_kept] sets PA_DEVERR_POSITION too
- * and leaves the sequence as it was. No block that the call writes may be in another
+ * that moves from or to a block outside the pool PA_DEVERR_BLOCK_ID: that token is
+ * skipped, its new position keeps its bytes. (Where a list is out of order, which of
+ * its other tokens arrive is undefined.) keep_start_loc that decreases or leaves
+ * [0, n_kept] sets PA_DEVERR_POSITION too and leaves the sequence as it was; n_kept 0
+ * is a call that reads nothing. No block that the call writes may be in another
  * sequence's table of the same call, nor shared otherwise (pa_bm_compact gives
  * private copies). head_dim 64 or 128, pools 16-byte aligned.
  */

@@ -111,6 +111,28 @@ __device__ int first_moved(const int32_t* keep, int n) {
     return lo;
 }
 
+// Whether one of the positions j < n that this thread looks at, as one of `threads`, is not j. Sixteen are
+// in flight, four a load (8 sequences of 131,008 tokens of which the last 16 move: 9.8 us, a list for each of 8
+// heads 12.2; without a look 8.7).
+__device__ bool changed(const int32_t* keep, int n, int thread, int threads) {
+    const int lead = min(n, (int)(-(reinterpret_cast<uintptr_t>(keep) >> 2) & 3)), quads = (n - lead) / 4;
+    const int4* four = reinterpret_cast<const int4*>(keep + lead);
+    bool bad = false;
+    auto differs = [&](long long i) {
+        const int4 v = four[i];
+        const int j = lead + 4 * (int)i;
+        return v.x != j || v.y != j + 1 || v.z != j + 2 || v.w != j + 3;
+    };
+    long long i = thread;
+    for (; i + 3LL * threads < quads; i += 4LL * threads) {
+        const bool a = differs(i), b = differs(i + threads), c = differs(i + 2LL * threads), d = differs(i + 3LL * threads);
+        bad |= a | b | c | d;
+    }
+    for (; i < quads; i += threads) bad |= differs(i);
+    const int j = thread < lead ? thread : thread + 4 * quads;  // the ends, up to three each
+    return bad || (j < n && keep[j] != j);
+}
+
 // C: 16-byte chunks of a row; grid (CTAs of a cluster, 2 * KV heads, sequences).
 template <int C, bool BSC>
 __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const CompactParams P) {
@@ -124,16 +146,24 @@ __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const Compa
     const int tid = threadIdx.x, side = blockIdx.y & 1, h = blockIdx.y >> 1, b = blockIdx.z;
     pa::launch_dependents();
     pa::grid_dependency_wait();
-    const int first = P.starts[b], n = P.starts[b + 1] - first;
+    const int first = P.starts[b], end = P.starts[b + 1];
     // every CTA of a cluster takes the same branches: they share the sequence and the head
-    if (n <= 0) return;
-    if (first < 0 || first > P.n_kept - n || P.max_blocks <= 0) {
+    if (first < 0 || end < first || end > P.n_kept) {
         if (tid == 0) pa::set_error(P.err, PA_DEVERR_POSITION);
         return;
     }
+    const int n = end - first;
+    if (n == 0) return;
     const int32_t* keep = P.keep + h * P.keep_stride + first;
     const int32_t* table = P.tables + (size_t)b * P.max_blocks;
     const int moved = first_moved(keep, n);
+    // What stays is looked at too, as the search went by samples.
+    const int still = moved >= n ? n : moved / kBS * kBS;
+    // (A list for all heads is shared out among them.)
+    const int part = (P.keep_stride ? 0 : h * (int)gridDim.x * 2) + blockIdx.x * 2 + side;
+    const int parts = gridDim.x * 2 * (P.keep_stride ? 1 : P.n_kv_heads);
+    if (changed(keep, still, part * kThreads + tid, parts * kThreads) || (tid == 0 && (still - 1) / kBS >= P.max_blocks))
+        pa::set_error(P.err, PA_DEVERR_POSITION);
     if (moved >= n) return;
     const int stride = (int)gridDim.x * T;  // tokens of a step
     const int j0 = moved / kBS * kBS + (int)blockIdx.x * T;
