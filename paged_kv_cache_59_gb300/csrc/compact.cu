@@ -26,8 +26,7 @@
 // 5.9 TB/s (16 clusters of 12; a CTA for each slice of the rows' columns, each with all the
 // look-ups, took 302). 6 documents of 23,000 to 65,000 tokens in block-scaled E4M3: 84 us,
 // 5.4 TB/s. 100 chats, a list for all heads: 143 us, 6.3 TB/s.
-#include <algorithm>
-
+#include "compact_clusters.h"
 #include "pa_common.cuh"
 
 namespace {
@@ -53,7 +52,6 @@ struct CompactParams {
     const int32_t* starts;
     long long keep_stride;  // from one KV head's list to the next; 0: one list
     int n_kv_heads;
-    int row_bytes;
     int max_blocks;
     int num_blocks;
     unsigned int* err;
@@ -298,30 +296,40 @@ __global__ void __launch_bounds__(kThreads, 2) compact_blocks_kernel(const Compa
 }
 
 template <int C, bool BSC>
-int launch_compact(const CompactParams& P, int ctas, int n_seqs, cudaStream_t stream) {
+int launch_compact(const CompactParams& P, int sms, int n_seqs, cudaStream_t stream) {
     auto kern = compact_blocks_kernel<C, BSC>;
     constexpr int kRing = kSteps<C, BSC> * kUnroll * kThreads * 16;
-    static bool attr_done[64] = {false};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) != cudaSuccess ||
-            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return PA_ERR_CUDA;
-        attr_done[dev] = true;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.dynamicSmemBytes = kRing;
-    cfg.gridDim = dim3(ctas, 2 * P.n_kv_heads, n_seqs);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    static int largest_of[64] = {0};  // clusters that the device's context holds (above 8: not everywhere); 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_CUDA;
+    int largest = largest_of[dev];
+    if (!largest) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) != cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return PA_ERR_CUDA;
+        cfg.numAttrs = 1;
+        for (largest = 16; largest > 1; --largest) {
+            int fit = 0;
+            cfg.gridDim = dim3(largest);
+            attr[0].val.clusterDim.x = largest;
+            if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) == cudaSuccess && fit > 0) break;
+        }
+        cudaGetLastError();  // (a size that the device does not know is an error)
+        largest_of[dev] = largest;
+    }
+    const int ctas = pa_compact_ctas(2LL * P.n_kv_heads * n_seqs, sms, P.n_kept, n_seqs, kThreads / C * kUnroll, largest);
+    cfg.gridDim = dim3(ctas, 2 * P.n_kv_heads, n_seqs);
+    attr[0].val.clusterDim.x = ctas;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, P) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -366,26 +374,15 @@ extern "C" int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, flo
     P.starts = keep_start_loc;
     P.keep_stride = keep_heads > 1 ? n_kept : 0;
     P.n_kv_heads = n_kv_heads;
-    P.row_bytes = head_dim * elem_bytes;
     P.max_blocks = max_blocks_per_seq;
     P.num_blocks = num_blocks;
     P.err = err;
-    // CTAs of a cluster: until there are two for each SM, as far as a sequence's tokens (on average) give each
-    // a step's share. Up to 8, and up to 16 where few clusters leave SMs idle, which moves as many bytes a
-    // second as an SM's share of HBM: 1.3 CTAs for each SM, as clusters of CTAs that share SMs with others
-    // hold all of theirs back. (One document's 16 units: 125 us with 8, 107 with 10, 109 with 12, 133 with 16; in
-    // E4M3 72, 61, 53, 72; 8 units of 4 sequences: 45 with 8, 33 with 12, 27 with 16.)
-    const int chunks = P.row_bytes / 16, tokens = kThreads / chunks * kUnroll;
-    const long long units = 2LL * n_kv_heads * n_seqs;
-    const int most = (int)std::min(16LL, std::max(8LL, 13LL * sms / (10 * units)));
-    int ctas = 1;
-    while (ctas < most && units * ctas < 2LL * sms && (long long)n_kept > (long long)n_seqs * ctas * tokens)
-        ctas = std::min(2 * ctas, most);
+    const int chunks = head_dim * elem_bytes / 16;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (k_scale) return chunks == 8 ? launch_compact<8, true>(P, ctas, n_seqs, st) : launch_compact<4, true>(P, ctas, n_seqs, st);
+    if (k_scale) return chunks == 8 ? launch_compact<8, true>(P, sms, n_seqs, st) : launch_compact<4, true>(P, sms, n_seqs, st);
     switch (chunks) {
-        case 4: return launch_compact<4, false>(P, ctas, n_seqs, st);
-        case 8: return launch_compact<8, false>(P, ctas, n_seqs, st);
-        default: return launch_compact<16, false>(P, ctas, n_seqs, st);
+        case 4: return launch_compact<4, false>(P, sms, n_seqs, st);
+        case 8: return launch_compact<8, false>(P, sms, n_seqs, st);
+        default: return launch_compact<16, false>(P, sms, n_seqs, st);
     }
 }
