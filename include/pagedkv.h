@@ -671,8 +671,8 @@ int pa_prefill_fp8_block(void* out, const void* q, const void* k_pool, const voi
  *     out[b][h] = sum_t softmax_t(z) V_b[t]
  * over the positions of pa_decode_sinks (window >= 0, n_sinks), or all (window
  * -1: n_sinks is ignored).
- *  softcap       0 (none), or positive with scale / softcap finite, else
- *                PA_ERR_INVALID_ARG
+ *  softcap       0 (none), or positive and at most 2^100 with scale / softcap finite,
+ *                else PA_ERR_INVALID_ARG
  *  alibi_slopes  fp32 [n_heads], device memory, 4-byte aligned, finite; NULL: no
  *                bias. Distances count cache positions: a cache compacted by
  *                pa_compact_blocks has lost those that its tokens were written at

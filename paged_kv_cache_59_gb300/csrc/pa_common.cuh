@@ -29,9 +29,11 @@ void* pa_symbol_address(PaSymbolCache* cache, const void* symbol);
 // Host-side helpers shared by the entry points.
 static inline bool pa_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// A score cap the kernels can work with: 0 (none), or positive with finite scale / cap and cap * log2(e).
+// A score cap the kernels can work with: 0 (none), or positive with finite scale / cap, and at most 2^100: scale / cap
+// times a quiet E4M3 block's scale is a subnormal above, whose error times the cap is one of the scores (a cap of
+// 2e38 over scales of 2^-16: outputs off by 100 times their bound).
 static inline bool pa_softcap_ok(float cap, float scale) {
-    return cap == 0.f || (cap > 0.f && isfinite(scale / cap) && isfinite(cap * 1.4426950408889634f));
+    return cap == 0.f || (cap > 0.f && cap <= 0x1p100f && isfinite(scale / cap));
 }
 
 // Host: launches `kern` with programmatic stream serialization, so its launch
