@@ -675,7 +675,8 @@ int pa_prefill_fp8_block(void* out, const void* q, const void* k_pool, const voi
  *                else PA_ERR_INVALID_ARG
  *  alibi_slopes  fp32 [n_heads], device memory, 4-byte aligned, finite; NULL: no
  *                bias. Distances count cache positions: a cache compacted by
- *                pa_compact_blocks has lost those that its tokens were written at
+ *                pa_compact_blocks has lost those that its tokens were written at.
+ *                A bias is off by up to 2^-22 of itself
  *  k_scale, v_scale  both NULL: bf16 pools; both given: E4M3 pools with a scale per
  *                (block, KV head), fp32 [num_blocks][n_kv_heads]. (A cache with
  *                scales per head serves as one whose blocks all have them.)

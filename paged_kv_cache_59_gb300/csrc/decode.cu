@@ -280,7 +280,7 @@ __device__ __forceinline__ void reshape4(const DecodeParams& P, float (&x)[4], c
     }
 }
 __device__ __forceinline__ float slope_of(const DecodeParams& P, int head) {
-    return P.slopes ? P.slopes[head] * 1.4426950408889634f : 0.f;
+    return P.slopes ? pa::slope_log2(P.slopes[head]) : 0.f;
 }
 
 // EB = bytes per cached element: 2 (bf16) or 1 (E4M3 codes with scales).

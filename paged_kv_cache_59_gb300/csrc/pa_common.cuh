@@ -253,6 +253,12 @@ __device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either i
     return r;
 }
 
+// A head's slope in base-2 units. Far above any score all slopes do the same, one key takes the whole weight; cut
+// at 2^60 either way, their products with distances stay finite. (A NaN stays one.)
+__device__ __forceinline__ float slope_log2(float slope) {
+    return -min_nan(-min_nan(slope, 0x1p60f), 0x1p60f) * 1.4426950408889634f;
+}
+
 // tanh for scores. Below kTanhSmall in magnitude x (1 + z P(z)), z = x^2, P the
 // polynomial of degree 4 whose largest relative error there is least (a linear program
 // over 6,000 points): 2^-20.3 with its coefficients and steps in fp32. Above,

@@ -385,8 +385,8 @@ __device__ __forceinline__ void cap_scores(uint32_t (&raw)[32], const float (&k)
 }
 
 // What a quarter's registers hold: products q.k (to be scaled; to be scaled and capped; to be
-// scaled and biased), or scores.
-enum { kProducts, kCapped, kBiased, kScores };
+// scaled and biased), or scores (the exponent block by block; score by score, see the new reference).
+enum { kProducts, kCapped, kBiased, kScores, kEachScore };
 template <int X>
 using Form = std::integral_constant<int, X>;
 
@@ -800,7 +800,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
             const int pos = g.ctx - g.L + i;  // this row's position (padding rows: beyond the chunk)
             const int limit = MOD ? max(pos, prefix_of(P, g.s, g.ctx) - 1) : pos;  // the last position it sees
             float slope2 = 0.f;
-            if constexpr (MOD >= kBias) slope2 = P.slopes ? P.slopes[g.kvh * G + r % G] * 1.4426950408889634f : 0.f;
+            if constexpr (MOD >= kBias) slope2 = P.slopes ? pa::slope_log2(P.slopes[g.kvh * G + r % G]) : 0.f;
             float m_used = -INFINITY, l = 0.f;
             // Key k of tile j is at position 128 j + k + kb_sinks if it is a sink, else + kb_win. In tiles
             // from j_win on, the limits below are those of the window's keys: where such a tile begins
@@ -884,6 +884,8 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                         float2 e = make_float2(__uint_as_float(raw[2 * w]), __uint_as_float(raw[2 * w + 1]));
                         if constexpr (decltype(form)::value == kScores) {
                             e = __fadd2_rn(e, both(nm));
+                        } else if constexpr (decltype(form)::value == kEachScore) {
+                            e = __fadd2_rn(__fadd2_rn(e, both(qe[MOD >= kBias ? w >> 3 : b])), both(-m_used));
                         } else if constexpr (decltype(form)::value == kCapped) {
                             const float2 z = __fmul2_rn(e, e);
                             float2 q = both(P.poly[3]);
@@ -1025,8 +1027,12 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
                                     const float d = m_used - mq;
                                     a = d < -126.f ? 0.f : __int_as_float(((int)d + 127) << 23);
                                     m_used = mq;
-                                    exps(masked, Form<MOD != kPlain ? kScores : kProducts>{}, raw, visible, ph, add);
+                                    if constexpr (MOD < kBias) exps(masked, Form<MOD != kPlain ? kScores : kProducts>{}, raw, visible, ph, add);
                                 }
+                                // Steep biases make scores whose roundings, of a block's bias less the reference, are
+                                // above fp16's range (of 2^27 and up; also without a new reference). Rounded as the
+                                // largest was, no score is above it.
+                                if constexpr (MOD >= kBias) exps(masked, Form<kEachScore>{}, raw, visible, ph, add);
                             }
                             psum2.x *= a;
                             psum2.y *= a;
