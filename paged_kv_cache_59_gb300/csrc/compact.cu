@@ -322,9 +322,10 @@ int launch_compact(const CompactParams& P, int sms, int n_seqs, cudaStream_t str
             int fit = 0;
             cfg.gridDim = dim3(largest);
             attr[0].val.clusterDim.x = largest;
-            if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) == cudaSuccess && fit > 0) break;
+            const cudaError_t asked = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
+            if (asked == cudaSuccess && fit > 0) break;
+            if (asked != cudaSuccess) cudaGetLastError();  // a size that the device does not know
         }
-        cudaGetLastError();  // (a size that the device does not know is an error)
         largest_of[dev] = largest;
     }
     const int ctas = pa_compact_ctas(2LL * P.n_kv_heads * n_seqs, sms, P.n_kept, n_seqs, kThreads / C * kUnroll, largest);
