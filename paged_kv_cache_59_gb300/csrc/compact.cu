@@ -22,8 +22,8 @@
 //
 // Bound by HBM: every moved byte is read once and written once. 32 chats of 2,000 to
 // 8,192 tokens that keep a third, a list for each of 8 heads (128 dims, bf16): 72 us,
-// 5.5 TB/s, 0.81 of a copy. One document of 131,072 tokens that keeps 0.6: 109 us,
-// 5.9 TB/s (16 clusters of 12; a CTA for each slice of the rows' columns, each with all the
+// 5.5 TB/s, 0.81 of a copy. One document of 131,072 tokens that keeps 0.6: 108 us,
+// 6.0 TB/s (16 clusters of 12; a CTA for each slice of the rows' columns, each with all the
 // look-ups, took 302). 6 documents of 23,000 to 65,000 tokens in block-scaled E4M3: 84 us,
 // 5.4 TB/s. 100 chats, a list for all heads: 143 us, 6.3 TB/s.
 #include "compact_clusters.h"

@@ -39,8 +39,8 @@
 //    tensor-core variant further down: the same decomposition, with each
 //    block's two products as warp-level MMAs over TMA-staged, swizzled tiles.
 //  * Reshaped scores (pa_decode_score_mod, MOD): each score capped by a tanh, biased by its key's
-//    distance, or both, before the running maximum; HBM bounds them still (64 sequences of 128 ..
-//    4,096 tokens, 32/8 heads, a cap: 83.7 us, 6.2 TB/s).
+//    distance, or both, before the running maximum; at head_dim 128 HBM bounds them still (64 sequences
+//    of 128 .. 4,096 tokens, 32/8 heads, a cap: 83.7 us, 6.2 TB/s), at 64 the instructions (67, 3.9).
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -32,7 +32,8 @@
 // chunks whose cache comes from HBM.
 // Reshaped scores (MOD, pa_prefill_score_mod): the same kernel, each score capped by a tanh, biased by
 // its key's distance, or both, before the exponential, and prefixes that lift the causal limit. 2,048
-// rows, window 4,096, scores of a spread of 6: 177 us with a cap of 50, 152 with biases.
+// rows, window 4,096, scores of a spread of 6, on one cache again and again: 177 us with a cap of 50, 152 with
+// biases (caches in turn 180 and 155).
 // 2,048 rows, window 4,096 + 4 sinks (256 items of 33 tiles on 152 SMs): 129.1 us on
 // one cache, 1,066 TFLOP/s of visible pairs, 132.6 over three in turn; 179 us with
 // whole waves, cut tails and a block-wide barrier between segments.
@@ -1229,7 +1230,7 @@ pa_prefill_win_kernel(const PrefillParams P, const __grid_constant__ CUtensorMap
 // k = 0, else 2 (ca + k). Behind that table, 8 counters for each CTA (see
 // join_pieces), zeroed here.
 // Capped scores over a bf16 cache take 1.5 of a plain tile's time, and starting no more: two
-// of theirs (2,048 rows under a window of 4,096: 184 and 177 us; over E4M3, whose segments take
+// of theirs (2,048 rows under a window of 4,096, on one cache again and again: 184 and 177 us; over E4M3, whose segments take
 // longer to start, three remain: 205, with two 211).
 constexpr int kStart = 3, kLeast = 3;
 constexpr int kStartCap = 2;
