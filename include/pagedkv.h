@@ -752,8 +752,8 @@ int pa_prefill_score_mod(void* out, const void* q, const void* k_pool, const voi
  * its other tokens arrive is undefined.) keep_start_loc that decreases or leaves
  * [0, n_kept] sets PA_DEVERR_POSITION too and leaves the sequence as it was; n_kept 0
  * is a call that reads nothing. No block that the call writes may be in another
- * sequence's table of the same call, nor shared otherwise (pa_bm_compact gives
- * private copies). head_dim 64 or 128, pools 16-byte aligned.
+ * sequence's table of the same call, nor shared otherwise (pa_bm_compact_batch
+ * gives private copies). head_dim 64 or 128, pools 16-byte aligned.
  */
 int pa_compact_blocks(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
                       const int32_t* block_tables, const int32_t* keep, const int32_t* keep_start_loc,
@@ -850,8 +850,9 @@ int pa_bm_release_between(pa_bm* bm, int64_t seq_id, int64_t from_pos, int64_t t
  * Then the blocks behind the kept tokens are released, so that the copies and the
  * compaction have to be on the stream before anything that writes blocks handed out
  * later, the copies of the next pa_bm_compact among them: sequences that one
- * pa_compact_blocks moves together come from one pa_bm_compact_batch. Where first_moved < n_tokens, pa_bm_cache_blocks registers no position from
- * first_moved on afterwards.
+ * pa_compact_blocks moves together come from one pa_bm_compact_batch. Where
+ * first_moved < n_tokens, pa_bm_cache_blocks registers no position from first_moved
+ * on afterwards.
  * PA_ERR_INVALID_ARG where a block that would be written, or appended to, was
  * released (pa_bm_release_*); PA_ERR_CAPACITY with both counts set, and PA_ERR_OOM:
  * nothing changed. With n_tokens the sequence's length nothing moves.
